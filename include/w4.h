@@ -304,6 +304,39 @@ w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const
                           const void* bias, void* out, float* token_scales_out,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* Root-mean-square norm of every row of x [M,K] (x_type W4_F16 or W4_BF16),
+ * with the residual stream's addition before it: the step that makes a
+ * product's activations ([PT]: one scale per token fuses with the
+ * normalisation before the GEMM).  In fp32, for every row:
+ *   h     = x + residual                  (residual NULL: h = x)
+ *   rstd  = 1 / sqrt(sum_k h^2 / K + eps)
+ *   y     = h * rstd * weight             (weight [K] of x_type, NULL: ones)
+ * y_type == x_type: y [M,K] is rounded once to it; y_scales NULL.
+ * y_type W4_S8 or W4_E4M3: y [M,K] holds codes and y_scales [M] (fp32) one
+ *   scale per row, y = code * scale, the `a` and `a_token_scales` of a W4A8
+ *   product: with hw = h * weight, A the row's largest |hw| and t = 127
+ *   (int8) or 448 (E4M3),
+ *     code  = hw * (t * (1 / A)), each operation rounded to fp32, then to the
+ *             nearest integer / E4M3 value, ties to even;
+ *     scale = rstd * A / t.
+ *   A row with A = 0 gets scale 0 and codes 0.  A row holding an infinity
+ *   or a NaN, or whose sum of squares is above the fp32 range, gets scale
+ *   NaN and codes 0.
+ * residual_out  [M,K] of x_type, receives h rounded once, or NULL (needs a
+ *   residual).  The norm is that of the unrounded h.
+ * residual_out and a 16-bit y may each be x or residual itself (in place);
+ * any other overlap of an output with another array is rejected.  A row of
+ * zeros with eps 0 gives NaN in 16 bits.  Arrays that are 16-byte aligned
+ * (y_scales: 4) with K % 8 == 0 take the vectorised path; any other K and
+ * alignment give the same results, slower.  No workspace.
+ * M == 0 is a no-op; K == 0 sets every scale to 0.  Errors:
+ * INVALID_ARGUMENT (negative size, bad type, negative or non-finite eps,
+ * residual_out without residual, scales missing or not wanted, a null or
+ * misaligned pointer, overlap), UNSUPPORTED (M or K > 2^31 - 1), CUDA. */
+w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void* residual,
+                     const void* weight, float eps, void* residual_out, void* y, int y_type,
+                     float* y_scales, void* stream);
+
 /* Static text for a status code; message of the last failed call on this
  * host thread ("" when none). */
 const char* w4_status_string(int status);

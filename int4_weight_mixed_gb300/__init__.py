@@ -96,6 +96,8 @@ def load():
         lib.w4_gemm_dynamic.restype = i32
         lib.w4_quantize_per_token_fp8.argtypes = [p, i32, i64, i64, p, p, p]
         lib.w4_quantize_per_token_fp8.restype = i32
+        lib.w4_rmsnorm.argtypes = [p, i32, i64, i64, p, p, ctypes.c_float, p, p, i32, p, p]
+        lib.w4_rmsnorm.restype = i32
         lib.w4_check_status.argtypes = [p, sz, p]
         lib.w4_check_status.restype = i32
         lib.w4_status_string.argtypes = [i32]
@@ -362,6 +364,68 @@ def quantize_per_token_fp8(a: torch.Tensor, out: torch.Tensor | None = None,
                                          _ptr(scales), _stream(a.device)),
            "w4_quantize_per_token_fp8")
     return out, scales
+
+
+def _norm_call(x, weight, eps, residual, y, scales, residual_out):
+    """w4_rmsnorm after the checks that need tensors: device, contiguity,
+    types and sizes."""
+    lib = load()
+    _dense_on(x.device, x=x, weight=weight, residual=residual, out=y, scales=scales,
+              residual_out=residual_out)
+    if x.dim() == 0:
+        raise ValueError("x needs at least one dimension")
+    M, K = x.shape[:-1].numel(), x.shape[-1]
+    for name, t, n in (("weight", weight, K), ("residual", residual, x.numel()),
+                       ("residual_out", residual_out, x.numel())):
+        if t is not None and (t.dtype != x.dtype or t.numel() != n):
+            raise ValueError(f"{name} must hold {n} values of {x.dtype}")
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be fp16 or bf16 (got {x.dtype})")
+    _check(lib.w4_rmsnorm(_ptr(x), _DTYPE_CODE[x.dtype], M, K, _ptr(residual), _ptr(weight),
+                          eps, _ptr(residual_out), _ptr(y), _DTYPE_CODE[y.dtype], _ptr(scales),
+                          _stream(x.device)), "w4_rmsnorm")
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+            residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            residual_out: torch.Tensor | None = None):
+    """w4_rmsnorm, 16-bit output: the rows (last dimension) of x (+ residual)
+    over their root mean square, times weight; the activations of a W4A16
+    product.  Returns out, or (out, residual_out) when a residual is given:
+    residual_out is x + residual, the residual stream after this addition.
+    out and residual_out may be x or residual (in place)."""
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError("out must have x's type and shape")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    _norm_call(x, weight, eps, residual, out, None, residual_out)
+    return out if residual is None else (out, residual_out)
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                  residual: torch.Tensor | None = None, act_dtype: torch.dtype = torch.int8,
+                  out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                  residual_out: torch.Tensor | None = None):
+    """w4_rmsnorm, 8-bit output: the same norm as int8 (act_dtype torch.int8)
+    or E4M3 (torch.float8_e4m3fn) codes and one fp32 scale per row, the `a`
+    and `token_scales` of a W4A8 gemm.  Returns (codes, scales), or (codes,
+    scales, residual_out) when a residual is given."""
+    if act_dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise ValueError("act_dtype must be torch.int8 or torch.float8_e4m3fn")
+    if out is None:
+        out = torch.empty(x.shape, dtype=act_dtype, device=x.device)
+    elif out.dtype != act_dtype or out.shape != x.shape:
+        raise ValueError(f"out must be {act_dtype} of x's shape")
+    if scales is None:
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    elif scales.dtype != torch.float32 or scales.shape != x.shape[:-1]:
+        raise ValueError("scales must be fp32, one per row of x")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    _norm_call(x, weight, eps, residual, out, scales, residual_out)
+    return (out, scales) if residual is None else (out, scales, residual_out)
 
 
 def check_status(ws: torch.Tensor) -> int:

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdlib>
 #include <cstdio>
@@ -505,6 +506,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether [p, p + np) and [q, q + nq) share a byte; null arrays share none.
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a && b && a < b + nq && b < a + np;
+}
+// The same for two arrays that may also be one and the same.
+bool overlap_but_same(const void* p, size_t np, const void* q, size_t nq) {
+  return p != q && overlap(p, np, q, nq);
+}
 
 struct Problem {
   int mode;
@@ -1122,6 +1133,57 @@ w4_status w4_quantize_per_token_fp8(const void* a, int a_type, int64_t M, int64_
   cudaError_t e = launch_quant_per_token(a_type == W4_BF16, a, M, K, a_q, s_tok, 2,
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "quantize launch");
+}
+
+w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void* residual,
+                     const void* weight, float eps, void* residual_out, void* y, int y_type,
+                     float* y_scales, void* stream) {
+  if (M < 0 || K < 0) return fail(W4_ERR_INVALID_ARGUMENT, "negative size");
+  if (x_type != W4_F16 && x_type != W4_BF16)
+    return fail(W4_ERR_INVALID_ARGUMENT, "x_type must be W4_F16 or W4_BF16");
+  const bool q8 = y_type == W4_S8 || y_type == W4_E4M3;
+  if (!q8 && y_type != x_type)
+    return fail(W4_ERR_INVALID_ARGUMENT, "y_type must be x_type, W4_S8 or W4_E4M3");
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(W4_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
+  if (residual_out && !residual)
+    return fail(W4_ERR_INVALID_ARGUMENT, "residual_out without a residual");
+  if (y_scales && !q8) return fail(W4_ERR_INVALID_ARGUMENT, "a 16-bit output takes no scales");
+  if (M == 0) return W4_OK;
+  if (q8 && !y_scales) return fail(W4_ERR_INVALID_ARGUMENT, "an 8-bit output needs y_scales");
+  if (K > 0 && (!x || !y)) return fail(W4_ERR_INVALID_ARGUMENT, "null pointer");
+  if (!aligned_to(x, 2) || !aligned_to(residual, 2) || !aligned_to(weight, 2) ||
+      !aligned_to(residual_out, 2) || !aligned_to(y, q8 ? 1 : 2) || !aligned_to(y_scales, 4))
+    return fail(W4_ERR_INVALID_ARGUMENT, "a pointer is not aligned to its element size");
+  if (M > 0x7fffffff) return fail(W4_ERR_UNSUPPORTED, "M above 2^31 - 1");
+  if (K > 0x7fffffff) return fail(W4_ERR_UNSUPPORTED, "K above 2^31 - 1");
+  // an output may take the place of x or residual, element for element
+  const size_t e16 = static_cast<size_t>(M) * K * 2, ey = q8 ? e16 / 2 : e16;
+  const size_t es = q8 ? static_cast<size_t>(M) * 4 : 0, ew = weight ? K * 2 : 0;
+  const bool bad =
+      overlap_but_same(residual_out, e16, x, e16) ||
+      overlap_but_same(residual_out, e16, residual, e16) ||
+      (q8 ? overlap(y, ey, x, e16) || overlap(y, ey, residual, e16)
+          : overlap_but_same(y, ey, x, e16) || overlap_but_same(y, ey, residual, e16)) ||
+      overlap(residual_out, e16, y, ey) || overlap(residual_out, e16, weight, ew) ||
+      overlap(y, ey, weight, ew) || overlap(y_scales, es, x, e16) ||
+      overlap(y_scales, es, residual, e16) || overlap(y_scales, es, weight, ew) ||
+      overlap(y_scales, es, y, ey) || overlap(y_scales, es, residual_out, e16);
+  if (bad) return fail(W4_ERR_INVALID_ARGUMENT, "an output overlaps another array");
+  NormArgs a{};
+  a.bf16 = x_type == W4_BF16;
+  a.out = y_type == W4_S8 ? kNormS8 : y_type == W4_E4M3 ? kNormE4M3 : kNorm16;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.h_out = residual_out;
+  a.y = y;
+  a.scales = y_scales;
+  a.M = M;
+  a.K = K;
+  a.eps = eps;
+  cudaError_t e = launch_norm(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4_OK : cuda_fail(e, "norm launch");
 }
 
 w4_status w4_check_status(void* workspace, size_t workspace_bytes, void* stream) {

@@ -179,6 +179,21 @@ cudaError_t launch_a8_to_bf16(const int8_t* a, int64_t count, void* out, cudaStr
 // out: 0 int8 codes, 1 int8 codes as bf16 values, 2 E4M3 codes
 cudaError_t launch_quant_per_token(bool bf16, const void* a, int64_t M, int64_t K, void* q,
                                    float* s_tok, int out, cudaStream_t s);
+// Root-mean-square norm of M rows of K values (w4_norm.cu).
+enum NormOut { kNorm16 = 0, kNormS8 = 1, kNormE4M3 = 2 };
+struct NormArgs {
+  bool bf16;             // x, residual, weight, h_out (and a 16-bit y): bf16, else fp16
+  int out;               // NormOut
+  const void* x;
+  const void* residual;  // or null
+  const void* weight;    // or null (ones)
+  void* h_out;           // x + residual, or null
+  void* y;
+  float* scales;         // [M], 8-bit outputs
+  int64_t M, K;
+  float eps;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_tc(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
                       const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s);
 cudaError_t launch_dk(const DkPlan& plan, const void* a, const TcArgs& args, cudaStream_t s);
