@@ -183,6 +183,42 @@ w4_status w4_gemm_bias(const void* a, int a_type, int64_t M, int64_t K, const vo
                        const float* ch_scales, const void* bias, void* out, int out_type,
                        void* workspace, size_t workspace_bytes, void* stream, int schedule);
 
+/* Activations of the epilogue entry points, in fp32:
+ *   RELU max(v, 0), SILU v / (1 + e^-v), GELU v * (1 + erf(v / sqrt 2)) / 2,
+ *   GELU_TANH v * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3))) / 2. */
+typedef enum w4_act {
+  W4_ACT_NONE = 0,
+  W4_ACT_RELU = 1,
+  W4_ACT_SILU = 2,
+  W4_ACT_GELU = 3,
+  W4_ACT_GELU_TANH = 4
+} w4_act;
+
+/* w4_gemm_bias with the step after the product in the same launch.  With
+ * v[m][n] the fp32 value of w4_gemm_bias before its rounding (product,
+ * scales, bias), and act a w4_act:
+ *   gated == 0: out[m][n] = round(act(v[m][n]) + residual[m][n])   [M, N]
+ *   gated != 0: out[m][j] = round(act(v[m][2j]) * v[m][2j+1]
+ *                                 + residual[m][j])                [M, N/2]
+ * with one rounding to out_type (fp16 / bf16) at the end: the [M, N] product
+ * is never written.  A gated product has its gate columns and the columns
+ * they multiply interleaved (gate 0, up 0, gate 1, ...) in the weights,
+ * scales, zero-points, channel scales and bias; N is even.
+ *   residual  array of out's type and shape, or NULL.  It may be out itself
+ *             (the residual stream updated in place).
+ * With act NONE, gated 0 and residual NULL this is exactly w4_gemm_bias.
+ * The schedules, workspace and heuristic are those of w4_gemm for the same
+ * M, N and K.  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
+ * an odd N with gated, an epilogue on the raw int32 output, a residual not
+ * aligned to 2 bytes or one that overlaps out without being out.  With
+ * K == 0 the product is 0. */
+w4_status w4_gemm_epilogue(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
+                           int wtype, int64_t N, const void* b_scales, int scale_type,
+                           const void* b_zeros, int64_t group_size, const float* a_token_scales,
+                           const float* ch_scales, const void* bias, int act, int gated,
+                           const void* residual, void* out, int out_type, void* workspace,
+                           size_t workspace_bytes, void* stream, int schedule);
+
 /* Schedules: their count, names, and the one the default heuristic picks
  * for a problem (-1 when none can run it). */
 int w4_num_schedules(void);
@@ -303,6 +339,16 @@ w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const
                           int64_t group_size, const float* ch_scales, int act_type,
                           const void* bias, void* out, float* token_scales_out,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* w4_gemm_dynamic with the epilogue of w4_gemm_epilogue (act, gated,
+ * residual): out is [M, N], gated [M, N/2].  Errors as both. */
+w4_status w4_gemm_dynamic_epilogue(const void* a, int a_type, int64_t M, int64_t K,
+                                   const void* b_packed, int wtype, int64_t N,
+                                   const void* b_scales, int scale_type, int64_t group_size,
+                                   const float* ch_scales, int act_type, const void* bias,
+                                   int act, int gated, const void* residual, void* out,
+                                   float* token_scales_out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* Root-mean-square norm of every row of x [M,K] (x_type W4_F16 or W4_BF16),
  * with the residual stream's addition before it: the step that makes a

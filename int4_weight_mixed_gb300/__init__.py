@@ -25,6 +25,7 @@ from . import _build_lib
 UINT4B8, UINT4, INT4 = 0, 1, 2
 KN_SEQ, NK_SEQ, NK_EXLLAMA = 0, 1, 2
 F16, BF16, S8, S32, E4M3 = 0, 1, 2, 3, 4
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(6)
 
 _DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.int8: S8, torch.int32: S32,
@@ -80,6 +81,8 @@ def load():
         lib.w4_gemm_ex.restype = i32
         lib.w4_gemm_bias.argtypes = gemm_args[:13] + [p] + gemm_args[13:] + [i32]
         lib.w4_gemm_bias.restype = i32
+        lib.w4_gemm_epilogue.argtypes = gemm_args[:13] + [p, i32, i32, p] + gemm_args[13:] + [i32]
+        lib.w4_gemm_epilogue.restype = i32
         lib.w4_num_schedules.restype = i32
         lib.w4_schedule_name.argtypes = [i32]
         lib.w4_schedule_name.restype = ctypes.c_char_p
@@ -94,6 +97,9 @@ def load():
         lib.w4_gemm_dynamic.argtypes = [p, i32, i64, i64, p, i32, i64, p, i32, i64, p, i32, p,
                                         p, p, p, sz, p]
         lib.w4_gemm_dynamic.restype = i32
+        lib.w4_gemm_dynamic_epilogue.argtypes = [p, i32, i64, i64, p, i32, i64, p, i32, i64, p,
+                                                 i32, p, i32, i32, p, p, p, p, sz, p]
+        lib.w4_gemm_dynamic_epilogue.restype = i32
         lib.w4_quantize_per_token_fp8.argtypes = [p, i32, i64, i64, p, p, p]
         lib.w4_quantize_per_token_fp8.restype = i32
         lib.w4_rmsnorm.argtypes = [p, i32, i64, i64, p, p, ctypes.c_float, p, p, i32, p, p]
@@ -255,34 +261,71 @@ def autotune(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int, instal
     return times
 
 
+def interleave_columns(gate: torch.Tensor, up: torch.Tensor, dim: int = -1) -> torch.Tensor:
+    """The columns of a gated product's two weights as one weight's, for
+    gemm(..., gated=True): gate 0, up 0, gate 1, up 1, ...  For packed words
+    dim is the N dimension (KN_SEQ: 1; NK_SEQ and NK_EXLLAMA: 0); scales,
+    zeros, channel_scales and bias are interleaved along their last one."""
+    if gate.shape != up.shape:
+        raise ValueError(f"gate {tuple(gate.shape)} and up {tuple(up.shape)} differ in shape")
+    dim %= gate.dim()
+    return torch.stack((gate, up), dim=dim + 1).flatten(dim, dim + 1).contiguous()
+
+
+def _check_epilogue(M, N, gated, bias, residual, out, out_dtype):
+    """The types and sizes of what the epilogue reads and writes."""
+    cols = N // 2 if gated else N
+    if bias is not None and (bias.dtype != out_dtype or bias.numel() != N):
+        raise ValueError(f"bias must be [{N}] of {out_dtype}")
+    if out.dtype != out_dtype or out.numel() != M * cols:
+        raise ValueError(f"out must be [{M}, {cols}] of {out_dtype}")
+    if residual is not None and (residual.dtype != out_dtype or residual.numel() != M * cols):
+        raise ValueError(f"residual must be [{M}, {cols}] of {out_dtype}")
+
+
 def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
          scales: torch.Tensor | None = None, zeros: torch.Tensor | None = None,
          group_size: int = -1, token_scales: torch.Tensor | None = None,
          channel_scales: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
          out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-         schedule: int = -1, bias: torch.Tensor | None = None) -> torch.Tensor:
-    """w4_gemm_ex / w4_gemm_bias: out[M,N] = a[M,K] x dequant(W) (+ bias).
+         schedule: int = -1, bias: torch.Tensor | None = None, act: int = ACT_NONE,
+         gated: bool = False, residual: torch.Tensor | None = None) -> torch.Tensor:
+    """w4_gemm_ex / w4_gemm_bias / w4_gemm_epilogue:
+    out[M,N] = act(a[M,K] x dequant(W) (+ bias)) (+ residual).
 
     W4A16: a fp16/bf16, scales [G,N] of a's dtype, zeros [G,N] pre-scaled or
     None.  W4A8: a int8, scales = int8 group scales [G,N] or None
     (per-channel), token_scales [M] and channel_scales [N] fp32 for fp16
     output, or out_dtype=torch.int32 for the raw accumulator.  bias: [N] of
     the output dtype, added before the output rounding, or None.
+
+    act: ACT_RELU, ACT_SILU, ACT_GELU or ACT_GELU_TANH, applied in fp32 before
+    the rounding.  gated: the even columns are gates, out[M, N/2] =
+    act(even column) * odd column (see interleave_columns).  residual: an
+    array of out's type and shape, added last; it may be out itself.
     """
     lib = load()
     _dense_on(a.device, a=a, b_packed=b_packed, scales=scales, zeros=zeros,
               token_scales=token_scales, channel_scales=channel_scales, out=out, ws=ws,
-              bias=bias)
+              bias=bias, residual=residual)
     M, K = a.shape
     a_code = _DTYPE_CODE[a.dtype]
     if out_dtype is None:
         out_dtype = torch.float16 if a.dtype in (torch.int8, torch.float8_e4m3fn) else a.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = torch.empty((M, N // 2 if gated else N), dtype=out_dtype, device=a.device)
     if ws is None:  # (a given workspace is checked against the plan by the library)
         ws = workspace(a.device, workspace_size(M, N, K, a.dtype, group_size))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
-    if bias is None:
+    if act != ACT_NONE or gated or residual is not None:
+        _check_epilogue(M, N, gated, bias, residual, out, out_dtype)
+        st = lib.w4_gemm_epilogue(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
+                                  scale_code, _ptr(zeros), group_size, _ptr(token_scales),
+                                  _ptr(channel_scales), _ptr(bias), act, int(gated),
+                                  _ptr(residual), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
+                                  ws.numel(), _stream(a.device), schedule)
+        _check(st, "w4_gemm_epilogue")
+    elif bias is None:
         st = lib.w4_gemm_ex(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                             scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                             _ptr(channel_scales), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
@@ -305,22 +348,32 @@ def gemm_dynamic(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
                  group_size: int = -1, channel_scales: torch.Tensor | None = None,
                  bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
                  token_scales_out: torch.Tensor | None = None,
-                 ws: torch.Tensor | None = None) -> torch.Tensor:
-    """w4_gemm_dynamic: fp16/bf16 activations quantized per token to int8
+                 ws: torch.Tensor | None = None, act: int = ACT_NONE, gated: bool = False,
+                 residual: torch.Tensor | None = None) -> torch.Tensor:
+    """w4_gemm_dynamic / w4_gemm_dynamic_epilogue: fp16/bf16 activations quantized per token to int8
     (act_dtype torch.int8) or E4M3 (torch.float8_e4m3fn) inside the call,
-    then the W4A8 product; fp16 out [M, N]."""
+    then the W4A8 product; fp16 out [M, N].  act, gated and residual as in
+    gemm()."""
     lib = load()
     _dense_on(a.device, a=a, b_packed=b_packed, scales=scales, channel_scales=channel_scales,
-              bias=bias, out=out, token_scales_out=token_scales_out, ws=ws)
+              bias=bias, out=out, token_scales_out=token_scales_out, ws=ws, residual=residual)
     M, K = a.shape
-    act = _DTYPE_CODE[act_dtype]
+    code = _DTYPE_CODE[act_dtype]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=a.device)
+        out = torch.empty((M, N // 2 if gated else N), dtype=torch.float16, device=a.device)
     if ws is None:  # (a given workspace is checked against the plan by the library)
-        ws = workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, act, group_size)))
+        ws = workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, code, group_size)))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else S8
+    if act != ACT_NONE or gated or residual is not None:
+        _check_epilogue(M, N, gated, bias, residual, out, torch.float16)
+        _check(lib.w4_gemm_dynamic_epilogue(
+            _ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N, _ptr(scales), scale_code,
+            group_size, _ptr(channel_scales), code, _ptr(bias), act, int(gated), _ptr(residual),
+            _ptr(out), _ptr(token_scales_out), _ptr(ws), ws.numel(), _stream(a.device)),
+            "w4_gemm_dynamic_epilogue")
+        return out
     _check(lib.w4_gemm_dynamic(_ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N,
-                               _ptr(scales), scale_code, group_size, _ptr(channel_scales), act,
+                               _ptr(scales), scale_code, group_size, _ptr(channel_scales), code,
                                _ptr(bias), _ptr(out), _ptr(token_scales_out), _ptr(ws),
                                ws.numel(), _stream(a.device)), "w4_gemm_dynamic")
     return out

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libw4.so")
 SOURCES = ["w4_api.cu", "w4_kernels.cu", "w4_tc.cu", "w4_tc2.cu", "w4_tc3.cu", "w4_dk.cu", "w4_noalloc.cu",
-           "w4_ds.cu", "w4_quant.cu", "w4_gv.cu", "w4_norm.cu"]
+           "w4_ds.cu", "w4_quant.cu", "w4_gv.cu", "w4_norm.cu",
+           "w4_tc_ep.cu", "w4_tc_ep2.cu"]
 HEADERS = ["w4_internal.h", "w4_ptx.cuh", "w4_tc_kernel.cuh", "w4_epilogue.cuh", os.path.join("..", "..", "include", "w4.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

@@ -740,14 +740,40 @@ size_t w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int a_type, int64
 }  // extern "C"
 
 namespace {
+// What follows the product (w4_gemm_epilogue): nothing, or an activation, a
+// gate and a residual.
+struct Epilogue {
+  int act = W4_ACT_NONE;
+  int gated = 0;
+  const void* residual = nullptr;
+  bool any() const { return act != W4_ACT_NONE || gated || residual; }
+};
+
+w4_status check_epilogue(const Epilogue& ep, int64_t M, int64_t N, const void* out,
+                         int out_type) {
+  if (ep.act < W4_ACT_NONE || ep.act > W4_ACT_GELU_TANH)
+    return fail(W4_ERR_INVALID_ARGUMENT, "bad act");
+  if (!ep.any()) return W4_OK;
+  if (out_type == W4_S32)
+    return fail(W4_ERR_INVALID_ARGUMENT, "the raw int32 output takes no epilogue");
+  if (ep.gated && N % 2 != 0)
+    return fail(W4_ERR_INVALID_ARGUMENT, "a gated product needs an even N");
+  if (!aligned_to(ep.residual, 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "residual is not aligned to its element size");
+  const size_t bytes = static_cast<size_t>(M) * (ep.gated ? N / 2 : N) * 2;
+  if (overlap_but_same(ep.residual, bytes, out, bytes))
+    return fail(W4_ERR_INVALID_ARGUMENT, "residual overlaps out without being out");
+  return W4_OK;
+}
+
 // prestaged: W4A8 on the tensor-core schedule with its bf16 activation copy
 // already in the workspace (the dynamic-quantization entry point writes it)
 w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
                     int wtype, int64_t N, const void* b_scales, int scale_type,
                     const void* b_zeros, int64_t group_size, const float* a_token_scales,
-                    const float* ch_scales, const void* bias, void* out, int out_type,
-                    void* workspace, size_t workspace_bytes, void* stream, int schedule,
-                    bool prestaged = false) {
+                    const float* ch_scales, const void* bias, const Epilogue& ep, void* out,
+                    int out_type, void* workspace, size_t workspace_bytes, void* stream,
+                    int schedule, bool prestaged = false) {
   Problem pr{};
   w4_status st = validate(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
                           group_size, a_token_scales, ch_scales, out, out_type, pr);
@@ -758,9 +784,25 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
     if (!aligned_to(bias, 2))
       return fail(W4_ERR_INVALID_ARGUMENT, "bias is not aligned to its element size");
   }
+  st = check_epilogue(ep, M, N, out, out_type);
+  if (st != W4_OK) return st;
   if (schedule >= kNumSchedules) return fail(W4_ERR_INVALID_ARGUMENT, "bad schedule index");
   if (M == 0 || N == 0) return W4_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0 && ep.any()) {  // the epilogue of a product of zeros
+    EpArgs ea{};
+    ea.s_tok = a_token_scales;
+    ea.s_ch = ch_scales;
+    ea.out = out;
+    ea.bias = bias;
+    ea.M = M;
+    ea.N = N;
+    ea.residual = ep.residual;
+    ea.act = ep.act;
+    ea.gated = ep.gated;
+    cudaError_t e = launch_epilogue_rows(pr.mode, ea, s);
+    return e == cudaSuccess ? W4_OK : cuda_fail(e, "epilogue launch");
+  }
   if (K == 0 && !bias) {
     const size_t esz = (pr.mode == kW4A8 && out_type == W4_S32) ? 4 : 2;
     cudaError_t e = cudaMemsetAsync(out, 0, static_cast<size_t>(M) * N * esz, s);
@@ -804,9 +846,21 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
   args.group_size = pr.gs;
   args.status = static_cast<int*>(workspace);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // runs a launcher on the arguments of the kernels with or without an
+  // epilogue of their own
+  auto with_epilogue = [&](auto&& launch) -> cudaError_t {
+    if (!ep.any()) return launch(args);
+    EpArgs ea{};
+    static_cast<TcArgs&>(ea) = args;
+    ea.residual = ep.residual;
+    ea.act = ep.act;
+    ea.gated = ep.gated;
+    return launch(ea);
+  };
 
   if (kSchedules[si].engine == kEngineSimt) {
-    cudaError_t e = launch_simt(pr.mode, a, args, s);
+    cudaError_t e =
+        with_epilogue([&](const auto& x) { return launch_simt(pr.mode, a, x, s); });
     return e == cudaSuccess ? W4_OK : cuda_fail(e, "simt launch");
   }
   if (kSchedules[si].engine == kEngineDk) {
@@ -819,7 +873,8 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
       fprintf(stderr, "w4: %s M=%lld N=%lld K=%lld nj=%d tiles=%d kblocks=%d ksplit=%d grid=%d smem=%zu\n",
               kSchedules[si].name, (long long)M, (long long)N, (long long)K, dp.nj, dp.n_tiles,
               dp.kblocks, dp.ksplit, dp.grid, dp.smem_bytes);
-    cudaError_t e = launch_dk(dp, a, args, s);
+    cudaError_t e =
+        with_epilogue([&](const auto& x) { return launch_dk(dp, a, x, s); });
     return e == cudaSuccess ? W4_OK : cuda_fail(e, "dk launch");
   }
   if (kSchedules[si].engine == kEngineDs) {
@@ -833,7 +888,8 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
               "segs=%d smem=%zu\n",
               kSchedules[si].name, (long long)M, (long long)N, (long long)K, dp.nj, dp.n_tiles,
               dp.kblocks, dp.sb, dp.stages, dp.grid, dp.max_segs, dp.smem_bytes);
-    cudaError_t e = launch_ds(dp, a, args, ws + dp.ws_prep, s);
+    cudaError_t e =
+        with_epilogue([&](const auto& x) { return launch_ds(dp, a, x, ws + dp.ws_prep, s); });
     return e == cudaSuccess ? W4_OK : cuda_fail(e, "ds launch");
   }
 
@@ -875,7 +931,8 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
                       "stages=%d grid=%d smem=%zu\n",
               kSchedules[si].name, (long long)M, (long long)N, (long long)K, gp.nj, gp.n_tiles,
               gp.kblocks, gp.cluster, gp.stages, gp.grid, gp.smem_bytes);
-    cudaError_t e = launch_gv(gp, amap, args, s);
+    cudaError_t e =
+        with_epilogue([&](const auto& x) { return launch_gv(gp, amap, x, s); });
     return e == cudaSuccess ? W4_OK : cuda_fail(e, "gv launch");
   }
 
@@ -970,7 +1027,8 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
     cudaError_t e = launch_a8_to_bf16(static_cast<const int8_t*>(a), M * K, ws + plan.ws_act, s);
     if (e != cudaSuccess) return cuda_fail(e, "int8->bf16 launch");
   }
-  cudaError_t e = launch_tc(plan, amap, smap, zmap, args, s);
+  cudaError_t e =
+      with_epilogue([&](const auto& x) { return launch_tc(plan, amap, smap, zmap, x, s); });
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "tc launch");
 }
 
@@ -1021,11 +1079,15 @@ size_t w4_gemm_dynamic_workspace_size(int64_t M, int64_t N, int64_t K, int act_t
   return (any > d.gemm_ws ? align256(any) : d.gemm_ws) + extra;
 }
 
-w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
+}  // extern "C"
+
+namespace {
+w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
                           int wtype, int64_t N, const void* b_scales, int scale_type,
                           int64_t group_size, const float* ch_scales, int act_type,
-                          const void* bias, void* out, float* token_scales_out,
-                          void* workspace, size_t workspace_bytes, void* stream) {
+                          const void* bias, const Epilogue& ep, void* out,
+                          float* token_scales_out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
   if (M < 0 || N < 0 || K < 0) return fail(W4_ERR_INVALID_ARGUMENT, "negative size");
   if (a_type != W4_F16 && a_type != W4_BF16)
     return fail(W4_ERR_INVALID_ARGUMENT, "a_type must be W4_F16 or W4_BF16");
@@ -1057,6 +1119,8 @@ w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const
     if (st != W4_OK) return st;
     if (bias && !aligned_to(bias, 2))
       return fail(W4_ERR_INVALID_ARGUMENT, "bias is not aligned to its element size");
+    st = check_epilogue(ep, M, N, out, W4_F16);
+    if (st != W4_OK) return st;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* qdst = codes;
@@ -1071,8 +1135,33 @@ w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const
   cudaError_t e = launch_quant_per_token(a_type == W4_BF16, a, M, K, qdst, stok, qout, s);
   if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
   return gemm_impl(codes, act_type, M, K, b_packed, wtype, N, b_scales, scale_type, nullptr,
-                   group_size, stok, ch_scales, bias, out, W4_F16, workspace, d.gemm_ws, stream,
+                   group_size, stok, ch_scales, bias, ep, out, W4_F16, workspace, d.gemm_ws, stream,
                    prestage ? d.si : -1, prestage);
+}
+}  // namespace
+
+extern "C" {
+
+w4_status w4_gemm_dynamic(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
+                          int wtype, int64_t N, const void* b_scales, int scale_type,
+                          int64_t group_size, const float* ch_scales, int act_type,
+                          const void* bias, void* out, float* token_scales_out,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return dynamic_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, group_size,
+                      ch_scales, act_type, bias, Epilogue{}, out, token_scales_out, workspace,
+                      workspace_bytes, stream);
+}
+
+w4_status w4_gemm_dynamic_epilogue(const void* a, int a_type, int64_t M, int64_t K,
+                                   const void* b_packed, int wtype, int64_t N,
+                                   const void* b_scales, int scale_type, int64_t group_size,
+                                   const float* ch_scales, int act_type, const void* bias,
+                                   int act, int gated, const void* residual, void* out,
+                                   float* token_scales_out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return dynamic_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, group_size,
+                      ch_scales, act_type, bias, Epilogue{act, gated != 0 ? 1 : 0, residual}, out,
+                      token_scales_out, workspace, workspace_bytes, stream);
 }
 
 w4_status w4_gemm_ex(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
@@ -1081,8 +1170,8 @@ w4_status w4_gemm_ex(const void* a, int a_type, int64_t M, int64_t K, const void
                      const float* ch_scales, void* out, int out_type, void* workspace,
                      size_t workspace_bytes, void* stream, int schedule) {
   return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
-                   group_size, a_token_scales, ch_scales, nullptr, out, out_type, workspace,
-                   workspace_bytes, stream, schedule);
+                   group_size, a_token_scales, ch_scales, nullptr, Epilogue{}, out, out_type,
+                   workspace, workspace_bytes, stream, schedule);
 }
 
 w4_status w4_gemm_bias(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
@@ -1091,7 +1180,19 @@ w4_status w4_gemm_bias(const void* a, int a_type, int64_t M, int64_t K, const vo
                        const float* ch_scales, const void* bias, void* out, int out_type,
                        void* workspace, size_t workspace_bytes, void* stream, int schedule) {
   return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
-                   group_size, a_token_scales, ch_scales, bias, out, out_type, workspace,
+                   group_size, a_token_scales, ch_scales, bias, Epilogue{}, out, out_type,
+                   workspace, workspace_bytes, stream, schedule);
+}
+
+w4_status w4_gemm_epilogue(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
+                           int wtype, int64_t N, const void* b_scales, int scale_type,
+                           const void* b_zeros, int64_t group_size, const float* a_token_scales,
+                           const float* ch_scales, const void* bias, int act, int gated,
+                           const void* residual, void* out, int out_type, void* workspace,
+                           size_t workspace_bytes, void* stream, int schedule) {
+  return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
+                   group_size, a_token_scales, ch_scales, bias,
+                   Epilogue{act, gated != 0 ? 1 : 0, residual}, out, out_type, workspace,
                    workspace_bytes, stream, schedule);
 }
 

@@ -106,9 +106,9 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
 
 // One CTA = one unit: 128 weight columns (tile nt) x K blocks [kb0, kb1).
 // NJ = number of 8-row activation tiles (M <= 8 * NJ).
-template <int MODE, int NJ>
+template <int MODE, int NJ, class Args>
 __global__ void __launch_bounds__(kDkThreads, 2)
-    dk_gemm_kernel(const void* __restrict__ act, const DkPlan p, const TcArgs args) {
+    dk_gemm_kernel(const void* __restrict__ act, const DkPlan p, const Args args) {
   constexpr bool F16 = MODE == kW4A16_F16;
   using T16 = typename std::conditional<F16, __half, __nv_bfloat16>::type;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(kDkThreads, 2)
 
   // ---- epilogue: direct store, or split-K partials + last-arriver reduce
   auto store = [&](int64_t m, int64_t n, float vf, int32_t vi) {
-    if (m >= M || n >= N) return;
-    store_out<MODE>(args, m, n, vf, vi);
+    // lanes 4 apart hold neighbouring weight columns of the same rows
+    store_lane<MODE, 4>(args, m, n, m < M && n < N, vf, vi, 0xffffffffu);
   };
   if (p.ksplit == 1) {
 #pragma unroll
@@ -427,9 +427,10 @@ size_t dk_smem_bytes(int nj, int kbu_max) {
   return static_cast<size_t>(kbu_max) * 8 * nj * 32 * 8 + static_cast<size_t>(kbu_max) * 8 * nj * 4;
 }
 
-cudaError_t launch_dk(const DkPlan& plan, const void* a, const TcArgs& args, cudaStream_t s) {
+template <class Args>
+cudaError_t launch_dk(const DkPlan& plan, const void* a, const Args& args, cudaStream_t s) {
   const void* fn = nullptr;
-#define W4_DK_FN(MODE, NJ) reinterpret_cast<const void*>(&dk_gemm_kernel<MODE, NJ>)
+#define W4_DK_FN(MODE, NJ) reinterpret_cast<const void*>(&dk_gemm_kernel<MODE, NJ, Args>)
   if (plan.mode == kW4A16_F16) fn = plan.nj == 1 ? W4_DK_FN(kW4A16_F16, 1) : W4_DK_FN(kW4A16_F16, 2);
   else if (plan.mode == kW4A16_BF16)
     fn = plan.nj == 1 ? W4_DK_FN(kW4A16_BF16, 1) : W4_DK_FN(kW4A16_BF16, 2);
@@ -439,8 +440,10 @@ cudaError_t launch_dk(const DkPlan& plan, const void* a, const TcArgs& args, cud
                                        static_cast<int>(plan.smem_bytes));
   if (e != cudaSuccess) return e;
   void* params[3] = {const_cast<void**>(&a), const_cast<DkPlan*>(&plan),
-                     const_cast<TcArgs*>(&args)};
+                     const_cast<Args*>(&args)};
   return cudaLaunchKernel(fn, dim3(plan.grid), dim3(kDkThreads), params, plan.smem_bytes, s);
 }
+template cudaError_t launch_dk(const DkPlan&, const void*, const TcArgs&, cudaStream_t);
+template cudaError_t launch_dk(const DkPlan&, const void*, const EpArgs&, cudaStream_t);
 
 }  // namespace w4

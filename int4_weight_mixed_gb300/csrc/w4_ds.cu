@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(128 * NJ) ds_prep_kernel(const void* __restric
 }
 
 // ---------------------------------------------------------------- ds_gemm
-template <int MODE, int NJ>
+template <int MODE, int NJ, class Args>
 __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
-    ds_gemm_kernel(const DsPlan p, const TcArgs args, const uint8_t* __restrict__ prep) {
+    ds_gemm_kernel(const DsPlan p, const Args args, const uint8_t* __restrict__ prep) {
   constexpr int kDsRP = DsShape<NJ>::RP, kDsCols = DsShape<NJ>::Cols;
   constexpr int kDsConsumers = DsShape<NJ>::Consumers;
   constexpr int kDsWProd = DsShape<NJ>::WProd, kDsAProd = DsShape<NJ>::AProd;
@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
   const int fold_blocks =
       pc ? (MODE == kW4A8 ? 64 : (1 << 30)) : static_cast<int>(args.group_size / kBlkK);
   auto store = [&](int64_t m, int64_t n, float vf, int32_t vi) {
-    if (m >= M || n >= N) return;
-    store_out<MODE>(args, m, n, vf, vi);
+    // lanes 4 apart hold neighbouring weight columns of the same rows
+    store_lane<MODE, 4>(args, m, n, m < M && n < N, vf, vi, 0xffffffffu);
   };
 
   uint32_t it = 0, cs = 0, cph = 0;  // stage count, it % S, (it / S) & 1
@@ -622,8 +622,8 @@ constexpr int kDsRedRows = 2;
 constexpr int kDsRedThreads = kDsRedRows * kTileN;
 constexpr int kDsRedMaxSlots = 64;  // slot offsets kept in shared memory
 
-template <int MODE, int NJ>
-__global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p, const TcArgs args) {
+template <int MODE, int NJ, class Args>
+__global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p, const Args args) {
   asm volatile("griddepcontrol.launch_dependents;");  // the next call may start its prologue
   asm volatile("griddepcontrol.wait;" ::: "memory");  // ds_gemm is complete
   using T16 = typename std::conditional<MODE == kW4A16_F16, __half, __nv_bfloat16>::type;
@@ -646,6 +646,7 @@ __global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p
   const int64_t M = args.M, N = args.N;
   const int m = blockIdx.y * kDsRedRows + threadIdx.x / kTileN, col = threadIdx.x % kTileN;
   const int64_t n = static_cast<int64_t>(tile) * kTileN + col;
+  const unsigned live = __ballot_sync(0xffffffffu, m < M && n < N);
   if (m >= M || n >= N) return;
   const uint32_t* part = static_cast<const uint32_t*>(args.partials);
   const size_t off = static_cast<size_t>(m) * kTileN + col;
@@ -667,12 +668,12 @@ __global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p
       else af = sl == 0 ? __uint_as_float(x[q]) : af + __uint_as_float(x[q]);
     }
   }
-  store_out<MODE>(args, m, n, af, ai);
+  store_lane<MODE, 1>(args, m, n, true, af, ai, live);
 }
 
 namespace {
-template <int MODE, int NJ>
-cudaError_t launch_ds_t(const DsPlan& plan, const void* a, const TcArgs& args, uint8_t* prep,
+template <int MODE, int NJ, class Args>
+cudaError_t launch_ds_t(const DsPlan& plan, const void* a, const Args& args, uint8_t* prep,
                         cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -685,7 +686,7 @@ cudaError_t launch_ds_t(const DsPlan& plan, const void* a, const TcArgs& args, u
   pcfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&pcfg, &ds_prep_kernel<MODE, NJ>, a, args.M, args.K, prep);
   if (e != cudaSuccess) return e;
-  auto fn = &ds_gemm_kernel<MODE, NJ>;
+  auto fn = &ds_gemm_kernel<MODE, NJ, Args>;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(plan.smem_bytes));
   if (e != cudaSuccess) return e;
@@ -708,11 +709,12 @@ cudaError_t launch_ds_t(const DsPlan& plan, const void* a, const TcArgs& args, u
   cfg.gridDim = dim3(plan.n_tiles, static_cast<unsigned>((args.M + kDsRedRows - 1) / kDsRedRows));
   cfg.blockDim = dim3(kDsRedThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, &ds_reduce_kernel<MODE, NJ>, plan, args);
+  return cudaLaunchKernelEx(&cfg, &ds_reduce_kernel<MODE, NJ, Args>, plan, args);
 }
 }  // namespace
 
-cudaError_t launch_ds(const DsPlan& plan, const void* a, const TcArgs& args, uint8_t* prep,
+template <class Args>
+cudaError_t launch_ds(const DsPlan& plan, const void* a, const Args& args, uint8_t* prep,
                       cudaStream_t s) {
   if (plan.nj == 1) {
     if (plan.mode == kW4A16_F16) return launch_ds_t<kW4A16_F16, 1>(plan, a, args, prep, s);
@@ -728,5 +730,7 @@ cudaError_t launch_ds(const DsPlan& plan, const void* a, const TcArgs& args, uin
   if (plan.mode == kW4A16_BF16) return launch_ds_t<kW4A16_BF16, 4>(plan, a, args, prep, s);
   return launch_ds_t<kW4A8, 4>(plan, a, args, prep, s);
 }
+template cudaError_t launch_ds(const DsPlan&, const void*, const TcArgs&, uint8_t*, cudaStream_t);
+template cudaError_t launch_ds(const DsPlan&, const void*, const EpArgs&, uint8_t*, cudaStream_t);
 
 }  // namespace w4

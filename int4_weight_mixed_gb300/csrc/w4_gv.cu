@@ -206,9 +206,9 @@ size_t gv_smem_bytes(int nj, int mode, int stages) {
          static_cast<size_t>(8 * nj) * kTileN * 4 + 2 * 8 * stages + 16;
 }
 
-template <int MODE, int NJ>
+template <int MODE, int NJ, class Args>
 __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
-    gv_gemm_kernel(const __grid_constant__ CUtensorMap amap, const GvPlan p, const TcArgs args) {
+    gv_gemm_kernel(const __grid_constant__ CUtensorMap amap, const GvPlan p, const Args args) {
   constexpr int RP = GvShape<NJ>::RP, Cols = GvShape<NJ>::Cols;
   constexpr int Consumers = GvShape<NJ>::Consumers, Prod = GvShape<NJ>::Prod;
   constexpr bool F16 = MODE == kW4A16_F16;
@@ -514,7 +514,9 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
           for (int e = 0; e < 4; ++e) {
             const int64_t m = j * 8 + 2 * t + (e & 1);
             const int64_t n = n0 + Cols * w + 16 * R + g + 8 * (e >> 1);
-            if (m < M && n < N) store_out<MODE>(args, m, n, res[R][j][e], ires[R][j][e]);
+            // lanes 4 apart hold neighbouring weight columns of the same rows
+            store_lane<MODE, 4>(args, m, n, m < M && n < N, res[R][j][e], ires[R][j][e],
+                                0xffffffffu);
           }
     } else {
 #pragma unroll
@@ -534,7 +536,48 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
 
   // ---- cluster reduction: CTA `rank` owns columns [c_lo, c_hi) of the tile
   cluster_sync();
-  {
+  if constexpr (std::is_same<Args, EpArgs>::value) {
+    // a thread takes both columns of a pair (a gate and what it multiplies)
+    const int p_lo = rank * (kTileN / 2) / C, p_hi = (rank + 1) * (kTileN / 2) / C;
+    const int np = p_hi - p_lo;
+    const int rows = static_cast<int>(M < 8 * NJ ? M : 8 * NJ);
+    const uint32_t red0 = smem_addr(red);
+    for (int i = threadIdx.x; i < rows * np; i += GvShape<NJ>::Threads) {
+      const int m = i / np, col = 2 * (p_lo + (i - m * np));
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t n = n0 + col + e;
+        const uint32_t local = red0 + static_cast<uint32_t>(m * kTileN + col + e) * 4;
+        uint32_t parts[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (q < C) parts[q] = ld_dsmem(dsmem_addr(local, static_cast<uint32_t>(q)));
+        float af = __uint_as_float(parts[0]);
+        int32_t ai = static_cast<int32_t>(parts[0]);
+#pragma unroll
+        for (int q = 1; q < 16; ++q)
+          if (q < C) {
+            af += __uint_as_float(parts[q]);
+            ai += static_cast<int32_t>(parts[q]);
+          }
+        v[e] = n < N ? ep_value<MODE>(args, m, n, af, ai) : 0.f;
+      }
+      const int64_t n = n0 + col;
+      if (n >= N) continue;
+      if (args.gated) {
+        const int64_t o = m * (N >> 1) + (n >> 1);
+        ep_store<MODE>(args, o, ep_act(v[0], args.act) * v[1] + ep_residual<MODE>(args, o));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (n + e >= N) break;
+          const int64_t o = m * N + n + e;
+          ep_store<MODE>(args, o, ep_act(v[e], args.act) + ep_residual<MODE>(args, o));
+        }
+      }
+    }
+  } else {
     const int c_lo = rank * kTileN / C, c_hi = (rank + 1) * kTileN / C;
     const int nc = c_hi - c_lo;
     const int rows = static_cast<int>(M < 8 * NJ ? M : 8 * NJ);
@@ -567,30 +610,34 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
 }
 
 namespace {
-template <int MODE, int NJ>
+template <int MODE, int NJ, class Args>
 const void* gv_fn() {
-  return reinterpret_cast<const void*>(&gv_gemm_kernel<MODE, NJ>);
+  return reinterpret_cast<const void*>(&gv_gemm_kernel<MODE, NJ, Args>);
 }
-template <int NJ>
+template <int NJ, class Args>
 const void* gv_select_nj(int mode) {
   switch (mode) {
-    case kW4A16_F16: return gv_fn<kW4A16_F16, NJ>();
-    case kW4A16_BF16: return gv_fn<kW4A16_BF16, NJ>();
-    case kW4A8F8: return gv_fn<kW4A8F8, NJ>();
-    default: return gv_fn<kW4A8, NJ>();
+    case kW4A16_F16: return gv_fn<kW4A16_F16, NJ, Args>();
+    case kW4A16_BF16: return gv_fn<kW4A16_BF16, NJ, Args>();
+    case kW4A8F8: return gv_fn<kW4A8F8, NJ, Args>();
+    default: return gv_fn<kW4A8, NJ, Args>();
   }
 }
+template <class Args>
 const void* gv_select(int mode, int nj) {
-  return nj == 1 ? gv_select_nj<1>(mode) : nj == 2 ? gv_select_nj<2>(mode) : gv_select_nj<4>(mode);
+  return nj == 1   ? gv_select_nj<1, Args>(mode)
+         : nj == 2 ? gv_select_nj<2, Args>(mode)
+                   : gv_select_nj<4, Args>(mode);
 }
 }  // namespace
 
 int gv_threads(int nj) { return nj >= 4 ? GvShape<4>::Threads : GvShape<1>::Threads; }
 
 // Clusters of C CTAs that can be resident at once; -1 when it cannot be
-// determined (no device).
+// determined (no device).  The kernels with an epilogue of their own take the
+// same plans, so that a product does not depend on what follows it.
 int gv_max_clusters(int mode, int nj, int C, size_t smem) {
-  const void* fn = gv_select(mode, nj);
+  const void* fn = gv_select<TcArgs>(mode, nj);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -622,9 +669,10 @@ int gv_max_clusters(int mode, int nj, int C, size_t smem) {
   return n;
 }
 
-cudaError_t launch_gv(const GvPlan& plan, const CUtensorMap& amap, const TcArgs& args,
+template <class Args>
+cudaError_t launch_gv(const GvPlan& plan, const CUtensorMap& amap, const Args& args,
                       cudaStream_t s) {
-  const void* fn = gv_select(plan.mode, plan.nj);
+  const void* fn = gv_select<Args>(plan.mode, plan.nj);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(plan.smem_bytes));
   if (e != cudaSuccess) return e;
@@ -647,8 +695,10 @@ cudaError_t launch_gv(const GvPlan& plan, const CUtensorMap& amap, const TcArgs&
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   void* params[3] = {const_cast<CUtensorMap*>(&amap), const_cast<GvPlan*>(&plan),
-                     const_cast<TcArgs*>(&args)};
+                     const_cast<Args*>(&args)};
   return cudaLaunchKernelExC(&cfg, fn, params);
 }
+template cudaError_t launch_gv(const GvPlan&, const CUtensorMap&, const TcArgs&, cudaStream_t);
+template cudaError_t launch_gv(const GvPlan&, const CUtensorMap&, const EpArgs&, cudaStream_t);
 
 }  // namespace w4

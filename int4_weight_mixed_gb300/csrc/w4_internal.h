@@ -117,6 +117,17 @@ struct TcArgs {
   int32_t* icopy;          // tc W4A8 with gicopy: per-CTA int32 running sums
 };
 
+// The same for a product with an epilogue of its own (activation, gate,
+// residual).  A type of its own, so that the kernels without one keep their
+// arguments and code: every GEMM kernel is a template over it, and one
+// overload of the output step takes each (w4_epilogue.cuh).
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct EpArgs : TcArgs {
+  const void* residual;  // [M][out columns] of the output type, or null; may be out itself
+  int act;               // Act
+  int gated;             // out[m][j] = act(v[m][2j]) * v[m][2j+1]: N / 2 output columns
+};
+
 // Skinny-M schedule (mma.sync, weights dequantized into register fragments).
 struct DkPlan {
   int mode;
@@ -171,8 +182,13 @@ cudaError_t launch_prepack(const int32_t* w_q, int wtype, int layout, int64_t K,
                            uint8_t* out, cudaStream_t s);
 cudaError_t launch_unprepack(const uint8_t* packed, int wtype, int layout, int64_t K,
                              int64_t N, int32_t* w_q, cudaStream_t s);
-cudaError_t launch_simt(int mode, const void* a, const TcArgs& args, cudaStream_t s);
+// Args: TcArgs, or EpArgs for a product with an epilogue of its own (both
+// are instantiated where the function is defined).
+template <class Args>
+cudaError_t launch_simt(int mode, const void* a, const Args& args, cudaStream_t s);
 // K == 0 with a bias: out[m][n] = bias[n] (W4A16), fp16_rn(0 * s_tok * s_ch + bias) (W4A8)
+// K == 0 with an epilogue of its own: the epilogue of a product of zeros
+cudaError_t launch_epilogue_rows(int mode, const EpArgs& args, cudaStream_t s);
 cudaError_t launch_bias_rows(int mode, int64_t M, int64_t N, const void* bias, bool w4a8,
                              void* out, cudaStream_t s);
 cudaError_t launch_a8_to_bf16(const int8_t* a, int64_t count, void* out, cudaStream_t s);
@@ -196,15 +212,20 @@ struct NormArgs {
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_tc(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
                       const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s);
-cudaError_t launch_dk(const DkPlan& plan, const void* a, const TcArgs& args, cudaStream_t s);
+cudaError_t launch_tc(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
+                      const CUtensorMap& zmap, const EpArgs& args, cudaStream_t s);
+template <class Args>
+cudaError_t launch_dk(const DkPlan& plan, const void* a, const Args& args, cudaStream_t s);
 size_t dk_smem_bytes(int nj, int kbu_max);
-cudaError_t launch_ds(const DsPlan& plan, const void* a, const TcArgs& args, uint8_t* prep,
+template <class Args>
+cudaError_t launch_ds(const DsPlan& plan, const void* a, const Args& args, uint8_t* prep,
                       cudaStream_t s);
 size_t ds_smem_bytes(int sb, int nj, int m, int stages);
 size_t ds_prep_bytes(int nj, int m, int kblocks);
 size_t gv_smem_bytes(int nj, int mode, int stages);
 int gv_max_clusters(int mode, int nj, int C, size_t smem);
-cudaError_t launch_gv(const GvPlan& plan, const CUtensorMap& amap, const TcArgs& args,
+template <class Args>
+cudaError_t launch_gv(const GvPlan& plan, const CUtensorMap& amap, const Args& args,
                       cudaStream_t s);
 size_t tc_stage_bytes(int bm, int nsub, int nt, int wblk);
 size_t tc_smem_bytes(int bm, int nsub, int nt, int stages, int wblk);

@@ -150,9 +150,10 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
 
 // CUDA-core W4A16: one thread per output, w_hat = fma(v, s, -w_z) rounded
 // once to T, fp32 accumulation over k ascending.
-template <typename T>
-__global__ void simt_w4a16_kernel(const T* __restrict__ a, TcArgs args) {
+template <typename T, class Args>
+__global__ void simt_w4a16_kernel(const T* __restrict__ a, Args args) {
   const int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const unsigned live = __ballot_sync(0xffffffffu, n < args.N);
   if (n >= args.N) return;
   const T* s = static_cast<const T*>(args.scales);
   const T* z = static_cast<const T*>(args.zeros);
@@ -172,13 +173,16 @@ __global__ void simt_w4a16_kernel(const T* __restrict__ a, TcArgs args) {
         acc = fmaf(to_f(a[m * K + k0 + j]), to_f(w), acc);
       }
     }
-    store_out<std::is_same<T, __half>::value ? kW4A16_F16 : kW4A16_BF16>(args, m, n, acc, 0);
+    store_lane<std::is_same<T, __half>::value ? kW4A16_F16 : kW4A16_BF16, 1>(args, m, n, true, acc,
+                                                                            0, live);
   }
 }
 
 // CUDA-core W4A8: exact int32 accumulation of a * v * sg.
-__global__ void simt_w4a8_kernel(const int8_t* __restrict__ a, TcArgs args) {
+template <class Args>
+__global__ void simt_w4a8_kernel(const int8_t* __restrict__ a, Args args) {
   const int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const unsigned live = __ballot_sync(0xffffffffu, n < args.N);
   if (n >= args.N) return;
   const int8_t* sg = static_cast<const int8_t*>(args.scales);
   const uint32_t* wp = reinterpret_cast<const uint32_t*>(args.b_packed);
@@ -194,14 +198,16 @@ __global__ void simt_w4a8_kernel(const int8_t* __restrict__ a, TcArgs args) {
         acc += static_cast<int32_t>(a[m * K + k0 + j]) * v * mul;
       }
     }
-    store_out<kW4A8>(args, m, n, 0.f, acc);
+    store_lane<kW4A8, 1>(args, m, n, true, 0.f, acc, live);
   }
 }
 
 // CUDA-core W4A8 with E4M3 activations: fp32 accumulation, k ascending, of
 // the exact products decode(a) * v.
-__global__ void simt_w4a8f8_kernel(const __nv_fp8_storage_t* __restrict__ a, TcArgs args) {
+template <class Args>
+__global__ void simt_w4a8f8_kernel(const __nv_fp8_storage_t* __restrict__ a, Args args) {
   const int64_t n = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const unsigned live = __ballot_sync(0xffffffffu, n < args.N);
   if (n >= args.N) return;
   const uint32_t* wp = reinterpret_cast<const uint32_t*>(args.b_packed);
   const int64_t K = args.K;
@@ -216,7 +222,7 @@ __global__ void simt_w4a8f8_kernel(const __nv_fp8_storage_t* __restrict__ a, TcA
         acc = fmaf(__half2float(h), v, acc);
       }
     }
-    store_out<kW4A8F8>(args, m, n, acc, 0);
+    store_lane<kW4A8F8, 1>(args, m, n, true, acc, 0, live);
   }
 }
 
@@ -267,7 +273,30 @@ cudaError_t launch_bias_rows(int mode, int64_t M, int64_t N, const void* bias, b
   return cudaGetLastError();
 }
 
-cudaError_t launch_simt(int mode, const void* a, const TcArgs& args, cudaStream_t s) {
+// K == 0 with an epilogue of its own: one thread per output element
+template <int MODE>
+__global__ void epilogue_rows_kernel(EpArgs args) {
+  const int64_t cols = args.gated ? args.N >> 1 : args.N;
+  for (int64_t o = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; o < args.M * cols;
+       o += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t m = o / cols, j = o - m * cols, n = args.gated ? 2 * j : j;
+    float r = ep_act(ep_value<MODE>(args, m, n, 0.f, 0), args.act);
+    if (args.gated) r *= ep_value<MODE>(args, m, n + 1, 0.f, 0);
+    ep_store<MODE>(args, o, r + ep_residual<MODE>(args, o));
+  }
+}
+
+cudaError_t launch_epilogue_rows(int mode, const EpArgs& args, cudaStream_t s) {
+  const int grid = grid_for(args.M * args.N, 256);
+  if (mode == kW4A16_F16) epilogue_rows_kernel<kW4A16_F16><<<grid, 256, 0, s>>>(args);
+  else if (mode == kW4A16_BF16) epilogue_rows_kernel<kW4A16_BF16><<<grid, 256, 0, s>>>(args);
+  else if (mode == kW4A8F8) epilogue_rows_kernel<kW4A8F8><<<grid, 256, 0, s>>>(args);
+  else epilogue_rows_kernel<kW4A8><<<grid, 256, 0, s>>>(args);
+  return cudaGetLastError();
+}
+
+template <class Args>
+cudaError_t launch_simt(int mode, const void* a, const Args& args, cudaStream_t s) {
   dim3 grid(static_cast<unsigned>((args.N + 127) / 128),
             static_cast<unsigned>(args.M < 65535 ? args.M : 65535));
   if (mode == kW4A16_F16)
@@ -281,5 +310,7 @@ cudaError_t launch_simt(int mode, const void* a, const TcArgs& args, cudaStream_
     simt_w4a8_kernel<<<grid, 128, 0, s>>>(static_cast<const int8_t*>(a), args);
   return cudaGetLastError();
 }
+template cudaError_t launch_simt(int, const void*, const TcArgs&, cudaStream_t);
+template cudaError_t launch_simt(int, const void*, const EpArgs&, cudaStream_t);
 
 }  // namespace w4

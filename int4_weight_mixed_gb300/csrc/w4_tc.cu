@@ -34,7 +34,7 @@ cudaError_t launch_tc_pair(const TcPlan& plan, const CUtensorMap& amap, const CU
 cudaError_t launch_tc(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
                       const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s) {
   if (plan.pair) return launch_tc_pair(plan, amap, smap, zmap, args, s);
-  if (!tc_mma2(plan)) return launch_tc_t<false>(plan, amap, smap, zmap, args, s);
+  if (!tc_mma2(plan)) return launch_tc_t<false, false>(plan, amap, smap, zmap, args, s);
   return launch_tc_mma2(plan, amap, smap, zmap, args, s);
 }
 

@@ -6,7 +6,7 @@ namespace w4 {
 
 cudaError_t launch_tc_mma2(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
                            const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s) {
-  return launch_tc_t<true>(plan, amap, smap, zmap, args, s);
+  return launch_tc_t<true, false>(plan, amap, smap, zmap, args, s);
 }
 
 }  // namespace w4

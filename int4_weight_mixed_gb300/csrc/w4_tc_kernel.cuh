@@ -293,11 +293,11 @@ __device__ __forceinline__ void add_chunk_sums(uint32_t (&d)[8], const uint32_t 
 // per-channel W4A8 pair kernel, whose time is spent in a few long exact
 // chunks and the stream-K fix-up, was 3-14% slower in every variant of it
 // tried; that one is instantiated without it.
-template <int MODE, bool MMA2, bool PAIR = false, bool LEAN = false>
+template <int MODE, bool MMA2, bool PAIR, bool LEAN, class Args>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap smap,
-                   const __grid_constant__ CUtensorMap zmap, const TcPlan p, const TcArgs args) {
+                   const __grid_constant__ CUtensorMap zmap, const TcPlan p, const Args args) {
   using T16 = typename std::conditional<MODE == kW4A16_F16, __half, __nv_bfloat16>::type;
   // W4A8 with fp8 activations: K blocks of 128 E4M3 values (one 128-byte
   // activation row, 8 KB of nibbles per 128-column tile) on kind::f8f6f4;
@@ -1089,11 +1089,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int i = 0; i < 8; ++i) d[i] = acc[i];
             }
             // outputs
+            if constexpr (std::is_same<Args, EpArgs>::value) {
+              store_block8<MODE>(args, m0 + cc, nrow, d);
+            } else {
   #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int64_t m = m0 + cc + i;
-              if (nrow < N && m < M)
-                store_out<MODE>(args, m, nrow, __uint_as_float(d[i]), static_cast<int32_t>(d[i]));
+              for (int i = 0; i < 8; ++i) {
+                const int64_t m = m0 + cc + i;
+                if (nrow < N && m < M)
+                  store_out<MODE>(args, m, nrow, __uint_as_float(d[i]), static_cast<int32_t>(d[i]));
+              }
             }
           }
           tc_fence_before();
@@ -1214,10 +1218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 
 namespace {
-template <int MODE, bool MMA2, bool PAIR, bool LEAN = false>
+template <int MODE, bool MMA2, bool PAIR, bool LEAN, class Args>
 cudaError_t launch_tc_mode(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
-                           const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s) {
-  auto* fn = &tc_gemm_kernel<MODE, MMA2, PAIR, LEAN>;
+                           const CUtensorMap& zmap, const Args& args, cudaStream_t s) {
+  auto* fn = &tc_gemm_kernel<MODE, MMA2, PAIR, LEAN, Args>;
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(plan.smem_bytes));
@@ -1251,20 +1255,20 @@ cudaError_t launch_tc_mode(const TcPlan& plan, const CUtensorMap& amap, const CU
 
 // fp8 activations are read by TMA straight from the caller's buffer; W4A8
 // int8 from the workspace's bf16 copy; W4A16 from the caller's buffer.
-template <bool MMA2, bool PAIR = false>
+template <bool MMA2, bool PAIR, class Args>
 cudaError_t launch_tc_t(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
-                        const CUtensorMap& zmap, const TcArgs& args, cudaStream_t s) {
+                        const CUtensorMap& zmap, const Args& args, cudaStream_t s) {
   // CTA pairs: LEAN except for per-channel W4A8 (see tc_gemm_kernel)
   switch (plan.mode) {
     case kW4A16_F16:
-      return launch_tc_mode<kW4A16_F16, MMA2, PAIR, PAIR>(plan, amap, smap, zmap, args, s);
+      return launch_tc_mode<kW4A16_F16, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
     case kW4A16_BF16:
-      return launch_tc_mode<kW4A16_BF16, MMA2, PAIR, PAIR>(plan, amap, smap, zmap, args, s);
-    case kW4A8F8: return launch_tc_mode<kW4A8F8, MMA2, PAIR, PAIR>(plan, amap, smap, zmap, args, s);
+      return launch_tc_mode<kW4A16_BF16, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
+    case kW4A8F8: return launch_tc_mode<kW4A8F8, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
     default:
       if (PAIR && tc_grouped(plan))
-        return launch_tc_mode<kW4A8, MMA2, PAIR, PAIR>(plan, amap, smap, zmap, args, s);
-      return launch_tc_mode<kW4A8, MMA2, PAIR>(plan, amap, smap, zmap, args, s);
+        return launch_tc_mode<kW4A8, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
+      return launch_tc_mode<kW4A8, MMA2, PAIR, false, Args>(plan, amap, smap, zmap, args, s);
   }
 }
 
@@ -1272,7 +1276,7 @@ cudaError_t launch_tc_t(const TcPlan& plan, const CUtensorMap& amap, const CUten
 // at once with `smem` bytes of shared memory per CTA (-1 when unknown).
 template <int MODE>
 int tc_pair_clusters_mode(size_t smem) {
-  auto* fn = &tc_gemm_kernel<MODE, false, true>;
+  auto* fn = &tc_gemm_kernel<MODE, false, true, false, TcArgs>;
   if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess) {
