@@ -356,7 +356,7 @@ w4_status w4_gemm_dynamic_epilogue(const void* a, int a_type, int64_t M, int64_t
  * normalisation before the GEMM).  In fp32, for every row:
  *   h     = x + residual                  (residual NULL: h = x)
  *   rstd  = 1 / sqrt(sum_k h^2 / K + eps)
- *   y     = h * rstd * weight             (weight [K] of x_type, NULL: ones)
+ *   y     = h * weight * rstd             (weight [K] of x_type, NULL: ones)
  * y_type == x_type: y [M,K] is rounded once to it; y_scales NULL.
  * y_type W4_S8 or W4_E4M3: y [M,K] holds codes and y_scales [M] (fp32) one
  *   scale per row, y = code * scale, the `a` and `a_token_scales` of a W4A8
@@ -374,7 +374,9 @@ w4_status w4_gemm_dynamic_epilogue(const void* a, int a_type, int64_t M, int64_t
  * any other overlap of an output with another array is rejected.  A row of
  * zeros with eps 0 gives NaN in 16 bits.  Arrays that are 16-byte aligned
  * (y_scales: 4) with K % 8 == 0 take the vectorised path; any other K and
- * alignment give the same results, slower.  No workspace.
+ * alignment give the same codes, and y and scales that differ by the fp32
+ * rounding of another order of the sum.  The bits of a row do not depend on
+ * M.  No workspace.
  * M == 0 is a no-op; K == 0 sets every scale to 0.  Errors:
  * INVALID_ARGUMENT (negative size, bad type, negative or non-finite eps,
  * residual_out without residual, scales missing or not wanted, a null or

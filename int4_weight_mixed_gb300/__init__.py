@@ -55,6 +55,8 @@ def build(force: bool = False) -> str:
 def load():
     """Load libw4.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -126,8 +128,25 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us less a
+# call on the host), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _is_dense(device, *tensors) -> bool:
+    """Whether _dense_on would accept these tensors (None: not given)."""
+    if device.type != "cuda":
+        return False
+    for t in tensors:
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            return False
+    return True
 
 
 def _dense_on(device, **tensors):
@@ -186,7 +205,7 @@ def workspace(device, nbytes: int) -> torch.Tensor:
     stream is capturing a CUDA graph: an allocation there would come from the
     graph's private pool and its zero-fill would be recorded into the graph,
     so callers that capture pass a workspace allocated beforehand."""
-    dev = torch.device(device)
+    dev = device if isinstance(device, torch.device) else torch.device(device)
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("w4: pass ws= (allocated before capture) to calls captured in a "
                            "CUDA graph")
@@ -305,17 +324,20 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     array of out's type and shape, added last; it may be out itself.
     """
     lib = load()
-    _dense_on(a.device, a=a, b_packed=b_packed, scales=scales, zeros=zeros,
-              token_scales=token_scales, channel_scales=channel_scales, out=out, ws=ws,
-              bias=bias, residual=residual)
+    dev = a.device
+    if not _is_dense(dev, a, b_packed, scales, zeros, token_scales, channel_scales, out, ws, bias,
+                     residual):
+        _dense_on(dev, a=a, b_packed=b_packed, scales=scales, zeros=zeros,
+                  token_scales=token_scales, channel_scales=channel_scales, out=out, ws=ws,
+                  bias=bias, residual=residual)
     M, K = a.shape
     a_code = _DTYPE_CODE[a.dtype]
     if out_dtype is None:
         out_dtype = torch.float16 if a.dtype in (torch.int8, torch.float8_e4m3fn) else a.dtype
     if out is None:
-        out = torch.empty((M, N // 2 if gated else N), dtype=out_dtype, device=a.device)
+        out = torch.empty((M, N // 2 if gated else N), dtype=out_dtype, device=dev)
     if ws is None:  # (a given workspace is checked against the plan by the library)
-        ws = workspace(a.device, workspace_size(M, N, K, a.dtype, group_size))
+        ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
     if act != ACT_NONE or gated or residual is not None:
         _check_epilogue(M, N, gated, bias, residual, out, out_dtype)
@@ -323,13 +345,13 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
                                   scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                                   _ptr(channel_scales), _ptr(bias), act, int(gated),
                                   _ptr(residual), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
-                                  ws.numel(), _stream(a.device), schedule)
+                                  ws.numel(), _stream(dev), schedule)
         _check(st, "w4_gemm_epilogue")
     elif bias is None:
         st = lib.w4_gemm_ex(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                             scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                             _ptr(channel_scales), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
-                            ws.numel(), _stream(a.device), schedule)
+                            ws.numel(), _stream(dev), schedule)
         _check(st, "w4_gemm")
     else:
         if bias.dtype != out_dtype or bias.numel() != N:
@@ -337,7 +359,7 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
         st = lib.w4_gemm_bias(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                               scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                               _ptr(channel_scales), _ptr(bias), _ptr(out),
-                              _DTYPE_CODE[out_dtype], _ptr(ws), ws.numel(), _stream(a.device),
+                              _DTYPE_CODE[out_dtype], _ptr(ws), ws.numel(), _stream(dev),
                               schedule)
         _check(st, "w4_gemm_bias")
     return out
@@ -422,21 +444,27 @@ def quantize_per_token_fp8(a: torch.Tensor, out: torch.Tensor | None = None,
 def _norm_call(x, weight, eps, residual, y, scales, residual_out):
     """w4_rmsnorm after the checks that need tensors: device, contiguity,
     types and sizes."""
-    lib = load()
-    _dense_on(x.device, x=x, weight=weight, residual=residual, out=y, scales=scales,
-              residual_out=residual_out)
-    if x.dim() == 0:
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if not _is_dense(dev, x, weight, residual, y, scales, residual_out):
+        _dense_on(dev, x=x, weight=weight, residual=residual, out=y, scales=scales,
+                  residual_out=residual_out)
+    if not shape:
         raise ValueError("x needs at least one dimension")
-    M, K = x.shape[:-1].numel(), x.shape[-1]
-    for name, t, n in (("weight", weight, K), ("residual", residual, x.numel()),
-                       ("residual_out", residual_out, x.numel())):
-        if t is not None and (t.dtype != x.dtype or t.numel() != n):
-            raise ValueError(f"{name} must hold {n} values of {x.dtype}")
-    if x.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError(f"x must be fp16 or bf16 (got {x.dtype})")
-    _check(lib.w4_rmsnorm(_ptr(x), _DTYPE_CODE[x.dtype], M, K, _ptr(residual), _ptr(weight),
-                          eps, _ptr(residual_out), _ptr(y), _DTYPE_CODE[y.dtype], _ptr(scales),
-                          _stream(x.device)), "w4_rmsnorm")
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise ValueError(f"x must be fp16 or bf16 (got {dt})")
+    K, n = shape[-1], x.numel()
+    M = n // K if K else shape[:-1].numel()
+    if weight is not None and (weight.dtype is not dt or weight.numel() != K):
+        raise ValueError(f"weight must hold {K} values of {dt}")
+    if residual is not None and (residual.dtype is not dt or residual.numel() != n):
+        raise ValueError(f"residual must hold {n} values of {dt}")
+    if residual_out is not None and (residual_out.dtype is not dt or residual_out.numel() != n):
+        raise ValueError(f"residual_out must hold {n} values of {dt}")
+    st = load().w4_rmsnorm(x.data_ptr(), _DTYPE_CODE[dt], M, K, _ptr(residual), _ptr(weight), eps,
+                           _ptr(residual_out), y.data_ptr(), _DTYPE_CODE[y.dtype], _ptr(scales),
+                           _stream(dev))
+    if st:
+        _check(st, "w4_rmsnorm")
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,

@@ -318,7 +318,7 @@ DkPlan make_dk_plan(int si, int mode, int64_t M, int64_t N, int64_t K, size_t* w
 
 // Plan of the streamed skinny-M schedule: two or three persistent CTAs per SM over a
 // stream-K split of the (128-column tile, 128-K block) iterations.
-DsPlan make_ds_plan(int si, int mode, int64_t M, int64_t N, int64_t K) {
+DsPlan make_ds_plan_uncached(int si, int mode, int64_t M, int64_t N, int64_t K) {
   DsPlan p{};
   p.mode = mode;
   p.nj = kSchedules[si].bm / 8;
@@ -351,6 +351,29 @@ DsPlan make_ds_plan(int si, int mode, int64_t M, int64_t N, int64_t K) {
   const size_t part = static_cast<size_t>(p.grid) * p.max_segs * 8 * p.nj * kTileN * 4;
   p.ws_prep = align256(p.ws_partials + part);
   p.ws_total = align256(p.ws_prep + ds_prep_bytes(p.nj, static_cast<int>(M), p.kblocks));
+  return p;
+}
+
+// The plan of a streamed schedule, remembered per shape and device as the tc
+// plans are.
+DsPlan make_ds_plan(int si, int mode, int64_t M, int64_t N, int64_t K) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  const auto key = std::make_tuple(si, mode, M, N, K, dev);
+  static std::mutex mu;
+  static std::map<decltype(key), DsPlan> cache;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+  }
+  const DsPlan p = make_ds_plan_uncached(si, mode, M, N, K);
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache.size() >= 4096) cache.clear();
+  cache.emplace(key, p);
   return p;
 }
 

@@ -6,7 +6,7 @@
 //
 //   h     = x + r                         (r optional)
 //   rstd  = 1 / sqrt(sum(h^2) / K + eps)
-//   16-bit: y = h * rstd * w
+//   16-bit: y = (h * w) * rstd
 //   8-bit : y is held as codes times one scale per row, the scale taking the
 //           row's largest |y| to t.  rstd divides out of y / scale:
 //             A     = max |h * w|
@@ -23,16 +23,32 @@
 
 #include "w4_epilogue.cuh"
 #include "w4_internal.h"
+#include "w4_ptx.cuh"
 
 namespace w4 {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;      // a CTA of short rows
+constexpr int kNormMaxThreads = 1024;  // a CTA of one long row
+constexpr int kNormMaxCluster = 8;
+constexpr size_t kNormMaxSmem = 224 * 1024;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// waits for all but the newest N groups
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int OUT>
@@ -59,84 +75,501 @@ __device__ __forceinline__ RowCode row_code(float sum, float A, float rstd) {
   if (A == 0.f && sum < kInf) c.scale = 0.f;
   return c;
 }
+// hw = h * w as the codes take it: itself but for the rare rows above
+__device__ __forceinline__ bool plain_codes(const RowCode& c) { return c.inv != 0.f && c.up == 1.f; }
+__device__ __forceinline__ float fit_code(float hw, const RowCode& c) {
+  return c.inv == 0.f ? 0.f : __fmul_rn(hw, c.up);
+}
 
-// the byte of one code (hw = h * w)
+// The low byte is the code of a fitted hw.  int8: adding 1.5 * 2^23 rounds
+// to the nearest integer, ties to even, and leaves it in the low mantissa
+// bits (|q| <= 127 (1 + 2^-22)).
 template <int OUT>
-__device__ __forceinline__ uint32_t code_of(float hw, const RowCode& c) {
-  if (c.inv == 0.f) return 0u;
-  const float q = __fmul_rn(c.up == 1.f ? hw : __fmul_rn(hw, c.up), c.inv);
+__device__ __forceinline__ uint32_t code_of(float hw, float inv) {
+  const float q = __fmul_rn(hw, inv);
   if constexpr (OUT == kNormE4M3) {
     uint16_t e2;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e2) : "f"(0.f), "f"(q));
-    return e2 & 0xFFu;
+    return e2;
   } else {
-    return static_cast<uint32_t>(__float2int_rn(q)) & 0xFFu;
+    return __float_as_uint(__fadd_rn(q, 12582912.f));
+  }
+}
+template <int OUT>
+__device__ __forceinline__ uint32_t code4_of(const float* hw, float inv) {
+  if constexpr (OUT == kNormE4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(lo) : "f"(__fmul_rn(hw[1], inv)), "f"(__fmul_rn(hw[0], inv)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(hi) : "f"(__fmul_rn(hw[3], inv)), "f"(__fmul_rn(hw[2], inv)));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  } else {
+    const uint32_t lo = __byte_perm(code_of<OUT>(hw[0], inv), code_of<OUT>(hw[1], inv), 0x0040);
+    const uint32_t hi = __byte_perm(code_of<OUT>(hw[2], inv), code_of<OUT>(hw[3], inv), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   }
 }
 
-// One CTA per row, element by element: any K and alignment.  The row is read
-// for the two reductions and again for the outputs; h and y are written only
-// then, by the thread that has read the element, so they may take the place
-// of x or r.
-template <typename T, int OUT>
-__global__ void __launch_bounds__(kNormThreads)
-    norm_row_kernel(const T* x, const T* r, const T* w, int64_t K, float eps, T* h_out, void* y,
-                    float* scales) {
-  __shared__ float red[2][kNormThreads / 32];
-  const int64_t m = blockIdx.x;
-  const T* xr = x + m * K;
-  const T* rr = r ? r + m * K : nullptr;
-  auto h_at = [&](int64_t k) {
-    const float v = ep_f32(xr[k]);
-    return rr ? __fadd_rn(v, ep_f32(rr[k])) : v;
-  };
-  auto w_at = [&](int64_t k) { return w ? ep_f32(w[k]) : 1.f; };
-  float sum = 0.f, A = 0.f;
-  for (int64_t k = threadIdx.x; k < K; k += kNormThreads) {
-    const float h = h_at(k);
-    sum = fmaf(h, h, sum);
-    if (OUT != kNorm16) A = max_nan(A, fabsf(__fmul_rn(h, w_at(k))));
-  }
+// Eight 16-bit values of a 16-byte load, or one value.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    } else {  // a bf16 is the upper half of its fp32
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  } else {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
+// The rows' reductions: sum and A of each row's blockDim.x threads (a power
+// of two up to 32, or a multiple of 32), in an order that depends on
+// blockDim.x alone; red: [2][kNormMaxThreads / 32].
+template <int OUT>
+__device__ __forceinline__ void reduce_row(float& sum, float& A, float (*red)[kNormMaxThreads / 32]) {
+  const int tpr = blockDim.x;
+  for (int o = (tpr < 32 ? tpr : 32) / 2; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (OUT != kNorm16) A = max_nan(A, __shfl_xor_sync(0xffffffffu, A, o));
   }
+  if (tpr <= 32) return;
+  const int nw = tpr / 32, w0 = threadIdx.y * nw;
   if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = sum;
-    red[1][threadIdx.x >> 5] = A;
+    red[0][w0 + threadIdx.x / 32] = sum;
+    red[1][w0 + threadIdx.x / 32] = A;
   }
   __syncthreads();
-  sum = red[0][0];
-  A = red[1][0];
-#pragma unroll
-  for (int i = 1; i < kNormThreads / 32; ++i) {
-    sum += red[0][i];
-    A = max_nan(A, red[1][i]);
+  sum = red[0][w0];
+  A = red[1][w0];
+  for (int i = 1; i < nw; ++i) {
+    sum += red[0][w0 + i];
+    if (OUT != kNorm16) A = max_nan(A, red[1][w0 + i]);
   }
+}
+
+// The same over the CTAs of a row's cluster: every CTA writes its sums into
+// each CTA's array, and adds them in the order of the ranks.
+template <int OUT>
+__device__ __forceinline__ void reduce_cluster(float& sum, float& A) {
+  __shared__ float part[kNormMaxCluster][2];
+  const uint32_t C = cluster_size(), me = cluster_rank();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA runs
+  if (threadIdx.x < C) {
+    const uint32_t to = peer_addr(smem_addr(&part[me][0]), threadIdx.x);
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(sum), "f"(A) : "memory");
+  }
+  cluster_sync_all();  // no CTA touches another's memory after this
+  sum = part[0][0];
+  A = part[0][1];
+  for (uint32_t i = 1; i < C; ++i) {
+    sum += part[i][0];
+    if (OUT != kNorm16) A = max_nan(A, part[i][1]);
+  }
+}
+
+// h of eight elements from 16 bytes of x and of r
+template <typename T>
+__device__ __forceinline__ void add8(const uint4& xv, const uint4& rv, bool has_r, float (&h)[8]) {
+  unpack<T>(xv, h);
+  if (has_r) {
+    float g[8];
+    unpack<T>(rv, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = __fadd_rn(h[e], g[e]);
+  }
+}
+// the outputs of eight elements from hw = h * w
+template <typename T, int OUT>
+__device__ __forceinline__ void store8(const float* hw, float rstd, float inv, void* y,
+                                       int64_t row, int i) {
+  if constexpr (OUT == kNorm16) {
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = pack2<T>(__fmul_rn(hw[2 * e], rstd), __fmul_rn(hw[2 * e + 1], rstd));
+    reinterpret_cast<uint4*>(static_cast<T*>(y) + row)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + row)[i] =
+        make_uint2(code4_of<OUT>(hw, inv), code4_of<OUT>(hw + 4, inv));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&h)[8]) {
+  return make_uint4(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]), pack2<T>(h[4], h[5]),
+                    pack2<T>(h[6], h[7]));
+}
+
+// Aligned rows, held in registers: each of a row's threads reads NV vectors
+// of 16 bytes, all loads issued before the first is used, so x and r are read
+// once.  h is stored as soon as it is formed, y once the row's statistics are
+// known; every element is read and written by one thread, so an output may
+// take the place of x or r.  CLUSTER: a row is split over the CTAs of a
+// cluster, which exchange their sums through distributed shared memory.
+// Bound by HBM: 4 bytes read and 3 or 4 written per element.
+template <typename T, int OUT, int NV, bool CLUSTER>
+__global__ void __launch_bounds__(kNormThreads, 4)
+    norm_held_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K, float eps,
+                     T* h_out, void* y, float* scales) {
+  __shared__ float red[2][kNormMaxThreads / 32];
+  // launched while the kernel before may still run: wait for it, then let
+  // the next one do the same
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tpr = blockDim.x;
+  const int64_t m = CLUSTER ? blockIdx.x / cluster_size()
+                            : static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = CLUSTER || m < M;
+  if constexpr (CLUSTER)  // this CTA runs: the others may write its shared memory
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // this CTA's vectors of the row: i0 .. i0 + n - 1
+  const int i0 = CLUSTER ? static_cast<int>(cluster_rank()) * NV * tpr : 0;
+  const int n = CLUSTER ? min(K / 8 - i0, NV * tpr) : K / 8;
+  const int64_t row = (live ? m : 0) * K + i0 * 8;
+  if (CLUSTER && w) w += i0 * 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 xv[NV], rv[NV], wv[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * tpr;
+    const bool in = live && i < n;
+    xv[v] = in ? reinterpret_cast<const uint4*>(x + row)[i] : zero;
+    rv[v] = in && r ? reinterpret_cast<const uint4*>(r + row)[i] : zero;
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * tpr;
+    wv[v] = w && i < n ? __ldg(reinterpret_cast<const uint4*>(w) + i) : zero;
+  }
+  float hw[NV * 8];
+  float sum = 0.f, A = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * tpr;
+    float h[8], u[8];
+    add8<T>(xv[v], rv[v], r != nullptr, h);
+    if (h_out && live && i < n) reinterpret_cast<uint4*>(h_out + row)[i] = pack8<T>(h);
+    if (w) unpack<T>(wv[v], u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sum = fmaf(h[e], h[e], sum);
+      hw[v * 8 + e] = w ? __fmul_rn(h[e], u[e]) : h[e];
+      if (OUT != kNorm16) A = max_nan(A, fabsf(hw[v * 8 + e]));
+    }
+  }
+  reduce_row<OUT>(sum, A, red);
+  if constexpr (CLUSTER) reduce_cluster<OUT>(sum, A);
+  if (!live) return;
   const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(K)) + eps);
   RowCode c{};
   if (OUT != kNorm16) {
     c = row_code<OUT>(sum, A, rstd);
-    if (threadIdx.x == 0) scales[m] = K == 0 ? 0.f : c.scale;
+    if (i0 == 0 && threadIdx.x == 0) scales[m] = c.scale;
+    if (!plain_codes(c)) {
+#pragma unroll
+      for (int e = 0; e < NV * 8; ++e) hw[e] = fit_code(hw[e], c);
+    }
   }
-  for (int64_t k = threadIdx.x; k < K; k += kNormThreads) {
-    const float h = h_at(k);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = threadIdx.x + v * tpr;
+    if (i < n) store8<T, OUT>(hw + v * 8, rstd, c.inv, y, row, i);
+  }
+}
+
+// Any K up to 1024 * NV.  A block of blockDim.y rows is a contiguous range of
+// x and of r, copied to shared memory in 16-byte pieces whatever the rows' own
+// alignment (x and r start at 16-byte boundaries; what is left at the arrays'
+// end by element).  A CTA takes every gridDim.x-th block and copies the next
+// one while it works on this one, element by element, NV values of a row held
+// by each of its threads.  A piece that two blocks' rows share is read by
+// both, each using its own values.
+template <typename T, int OUT, int NV, bool RES>
+__global__ void __launch_bounds__(kNormMaxThreads)
+    norm_ragged_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K,
+                       float eps, T* h_out, void* y, float* scales, uint32_t range) {
+  extern __shared__ __align__(16) uint8_t raw[];  // [2][x range, r range]
+  __shared__ float red[2][kNormMaxThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int R = blockDim.y, tpr = blockDim.x;
+  const int t = threadIdx.y * tpr + threadIdx.x, nt = tpr * R;
+  const int64_t blocks = (M + R - 1) / R;
+  const uint32_t stage = RES ? 2 * range : range;
+  auto copy = [&](int64_t b, uint32_t at) {  // block b to the stage at byte `at`
+    const int64_t m0 = b * R, m1 = m0 + R < M ? m0 + R : M;
+    const int64_t g0 = m0 * K / 8, e1 = m1 * K;         // first piece, end of the range
+    const int64_t g1 = m1 == M ? e1 / 8 : (e1 + 7) / 8;  // end of the whole pieces
+    const uint32_t sx = smem_addr(raw) + at;
+    const int pieces = static_cast<int>(g1 - g0);
+    const uint4* px = reinterpret_cast<const uint4*>(x) + g0;
+    const uint4* pr = reinterpret_cast<const uint4*>(r) + g0;
+    for (int g = t; g < pieces; g += nt) {
+      cp_async16(sx + g * 16, px + g);
+      if (RES) cp_async16(sx + range + g * 16, pr + g);
+    }
+    T* const tx = reinterpret_cast<T*>(raw + at);
+    T* const tr = reinterpret_cast<T*>(raw + at + range);
+    for (int64_t e = g1 * 8 + t; e < e1; e += nt) {
+      tx[e - g0 * 8] = x[e];
+      if (RES) tr[e - g0 * 8] = r[e];
+    }
+  };
+  uint32_t at = 0;
+  if (blockIdx.x < blocks) copy(blockIdx.x, 0);
+  cp_async_commit();
+  float wv[NV];  // a thread has the same columns in every row
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = threadIdx.x + v * tpr;
+    wv[v] = w && k < K ? ep_f32(w[k]) : 1.f;
+  }
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, at ^= stage) {
+    if (b + gridDim.x < blocks) copy(b + gridDim.x, at ^ stage);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();  // everyone's copies of this block
+    const int64_t m = b * R + threadIdx.y;
+    const bool live = m < M;
+    const int len = live ? K : 0;
+    // (rows beyond the last read this block's first one and store nothing)
+    const int shift = static_cast<int>((live ? m : b * R) * K - b * R * K / 8 * 8) + threadIdx.x;
+    const T* const xr = reinterpret_cast<const T*>(raw + at) + shift;
+    const T* const rr = reinterpret_cast<const T*>(raw + at + range) + shift;
+    T* const hr = RES && h_out ? h_out + m * K + threadIdx.x : nullptr;
+    float u[NV];
+    float sum = 0.f, A = 0.f;
+    // without branches: what lies past the row (its threads' last values, in
+    // shared memory all the same) counts as zero
+    auto take = [&](int v, T* h_to) {
+      const bool in = static_cast<int>(threadIdx.x) + v * tpr < len;
+      float h = ep_f32(xr[v * tpr]);
+      if (RES) h = __fadd_rn(h, ep_f32(rr[v * tpr]));
+      h = in ? h : 0.f;
+      if (RES && h_to && in) h_to[v * tpr] = ep_round<T>(h);
+      sum = fmaf(h, h, sum);
+      u[v] = __fmul_rn(h, wv[v]);
+      if (OUT != kNorm16) A = max_nan(A, fabsf(u[v]));
+    };
+    if (hr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) take(v, hr);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) take(v, nullptr);
+    }
+    reduce_row<OUT>(sum, A, red);
+    const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(K)) + eps);
+    float by = rstd;
+    if (OUT != kNorm16) {
+      const RowCode c = row_code<OUT>(sum, A, rstd);
+      if (live && threadIdx.x == 0) scales[m] = c.scale;
+      by = c.inv;
+      if (!plain_codes(c)) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) u[v] = fit_code(u[v], c);
+      }
+    }
+    T* const y16 = static_cast<T*>(y) + (OUT == kNorm16 ? m * K + threadIdx.x : 0);
+    uint8_t* const y8 = static_cast<uint8_t*>(y) + m * K + threadIdx.x;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (static_cast<int>(threadIdx.x) + v * tpr < len) {
+        if constexpr (OUT == kNorm16) y16[v * tpr] = ep_round<T>(__fmul_rn(u[v], by));
+        else y8[v * tpr] = static_cast<uint8_t>(code_of<OUT>(u[v], by));
+      }
+    }
+    __syncthreads();  // before the stage and the sums are written again
+  }
+}
+
+// Whatever the others do not take (arrays that start off a 16-byte boundary,
+// longer rows): both passes read x and r themselves, the second from L2; h
+// and y are written in the second, by the thread that has read the element.
+// A row is summed in the ragged kernel's order.
+template <typename T, int OUT>
+__global__ void __launch_bounds__(kNormMaxThreads)
+    norm_any_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, uint32_t K,
+                    float eps, T* h_out, void* y, float* scales) {
+  __shared__ float red[2][kNormMaxThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = m < M;
+  const uint32_t tpr = blockDim.x;
+  const T* const xr = x + m * K;
+  const T* const rr = r + (r ? m * K : 0);
+  auto h_at = [&](uint32_t k) {
+    const float v = ep_f32(xr[k]);
+    return r ? __fadd_rn(v, ep_f32(rr[k])) : v;
+  };
+  auto hw_at = [&](uint32_t k, float h) { return w ? __fmul_rn(h, ep_f32(w[k])) : h; };
+  float sum = 0.f, A = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (uint32_t k = threadIdx.x; k < K; k += tpr) {
+      const float h = h_at(k);
+      sum = fmaf(h, h, sum);
+      if (OUT != kNorm16) A = max_nan(A, fabsf(hw_at(k, h)));
+    }
+  }
+  reduce_row<OUT>(sum, A, red);
+  if (!live) return;
+  const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(K)) + eps);
+  RowCode c{};
+  if (OUT != kNorm16) {
+    c = row_code<OUT>(sum, A, rstd);
+    if (threadIdx.x == 0) scales[m] = c.scale;
+  }
+#pragma unroll 2
+  for (uint32_t k = threadIdx.x; k < K; k += tpr) {
+    const float h = h_at(k), hw = hw_at(k, h);
     if (h_out) h_out[m * K + k] = ep_round<T>(h);
     if constexpr (OUT == kNorm16)
-      static_cast<T*>(y)[m * K + k] = ep_round<T>(__fmul_rn(__fmul_rn(h, rstd), w_at(k)));
+      static_cast<T*>(y)[m * K + k] = ep_round<T>(__fmul_rn(hw, rstd));
     else
       static_cast<uint8_t*>(y)[m * K + k] =
-          static_cast<uint8_t>(code_of<OUT>(__fmul_rn(h, w_at(k)), c));
+          static_cast<uint8_t>(code_of<OUT>(fit_code(hw, c), c.inv));
   }
+}
+
+cudaLaunchConfig_t norm_config(dim3 grid, dim3 block, cudaLaunchAttribute* attr, cudaStream_t s) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Threads for `per` of a row's n pieces of work each: a power of two within
+// a warp, whole warps beyond.
+int row_threads(int64_t n, int per) {
+  const int64_t t = (n + per - 1) / per;
+  int p = 1;
+  while (p < 32 && p < t) p *= 2;
+  if (t <= 32) return p;
+  return static_cast<int>(t < kNormMaxThreads ? (t + 31) / 32 * 32 : kNormMaxThreads);
+}
+// rows of a CTA: one, or as many short ones as make kNormThreads threads
+int cta_rows(int tpr) { return tpr < kNormThreads ? kNormThreads / tpr : 1; }
+
+template <typename T, int OUT, int NV>
+cudaError_t launch_held(const NormArgs& a, int tpr, cudaStream_t s) {
+  const int rows = cta_rows(tpr);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      norm_config(dim3(static_cast<unsigned>((a.M + rows - 1) / rows)), dim3(tpr, rows), &attr, s);
+  return cudaLaunchKernelEx(&cfg, &norm_held_kernel<T, OUT, NV, false>, static_cast<const T*>(a.x),
+                            static_cast<const T*>(a.residual), static_cast<const T*>(a.weight),
+                            a.M, static_cast<int>(a.K), a.eps, static_cast<T*>(a.h_out), a.y,
+                            a.scales);
+}
+
+// A row over the CTAs of a cluster, NV vectors a thread.
+template <typename T, int OUT, int NV>
+cudaError_t launch_split(const NormArgs& a, int64_t n, cudaStream_t s) {
+  const int C = static_cast<int>((n + NV * kNormThreads - 1) / (NV * kNormThreads));
+  const int tpr = static_cast<int>((n + NV * C * 32 - 1) / (NV * C * 32)) * 32;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg =
+      norm_config(dim3(static_cast<unsigned>(a.M * C)), dim3(tpr), attr, s);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, &norm_held_kernel<T, OUT, NV, true>, static_cast<const T*>(a.x),
+                            static_cast<const T*>(a.residual), static_cast<const T*>(a.weight),
+                            a.M, static_cast<int>(a.K), a.eps, static_cast<T*>(a.h_out), a.y,
+                            a.scales);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory.
+template <class Fn>
+cudaError_t allow_smem(Fn* fn, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kNormMaxSmem));
+}
+
+// Shared memory of a CTA of the ragged kernel: two stages of x and r, each
+// from one 16-byte boundary to another, and what a row's threads read past
+// its end.
+size_t ragged_range(const NormArgs& a, int rows) {
+  return (static_cast<size_t>(rows) * a.K * 2 + 31) / 16 * 16;
+}
+size_t ragged_bytes(const NormArgs& a, int tpr, int rows, int nv) {
+  return ragged_range(a, rows) * (a.residual ? 4 : 2) + static_cast<size_t>(nv * tpr - a.K) * 2;
+}
+
+template <typename T, int OUT, int NV>
+cudaError_t launch_ragged(const NormArgs& a, int tpr, int rows, cudaStream_t s) {
+  const size_t bytes = ragged_bytes(a, tpr, rows, NV);
+  auto* fn = a.residual ? &norm_ragged_kernel<T, OUT, NV, true>
+                        : &norm_ragged_kernel<T, OUT, NV, false>;
+  cudaError_t e = allow_smem(fn, bytes);
+  if (e != cudaSuccess) return e;
+  // the CTAs that are resident at once
+  int dev = 0, sms = 0, per_sm = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, tpr * rows, bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (a.M + rows - 1) / rows, most = static_cast<int64_t>(sms) * per_sm;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = norm_config(dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                       dim3(tpr, rows), &attr, s);
+  cfg.dynamicSmemBytes = bytes;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<const T*>(a.x),
+                            static_cast<const T*>(a.residual), static_cast<const T*>(a.weight),
+                            a.M, static_cast<int>(a.K), a.eps, static_cast<T*>(a.h_out), a.y,
+                            a.scales, static_cast<uint32_t>(ragged_range(a, rows)));
 }
 
 template <typename T, int OUT>
 cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s) {
-  norm_row_kernel<T, OUT><<<static_cast<unsigned>(a.M), kNormThreads, 0, s>>>(
-      static_cast<const T*>(a.x), static_cast<const T*>(a.residual),
-      static_cast<const T*>(a.weight), a.K, a.eps, static_cast<T*>(a.h_out), a.y, a.scales);
-  return cudaGetLastError();
+  const auto at = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  const bool in16 = at(a.x, 16) && at(a.residual, 16);
+  const int64_t n = a.K / 8;
+  if (a.K % 8 == 0 && in16 && at(a.weight, 16) && at(a.h_out, 16) &&
+      at(a.y, OUT == kNorm16 ? 16 : 8)) {
+    if (n <= 32) return launch_held<T, OUT, 1>(a, row_threads(n, 1), s);
+    if (n <= 512) return launch_held<T, OUT, 2>(a, row_threads(n, 2), s);
+    if (n <= 1024) return launch_held<T, OUT, 4>(a, row_threads(n, 4), s);
+    if (n <= 4 * kNormThreads * kNormMaxCluster) return launch_split<T, OUT, 4>(a, n, s);
+  }
+  const int tpr = row_threads(a.K, 16), rows = cta_rows(tpr);
+  const int nv = a.K <= 16 * kNormMaxThreads ? 16 : 32;
+  if (in16 && a.K <= nv * kNormMaxThreads && ragged_bytes(a, tpr, rows, nv) <= kNormMaxSmem)
+    return nv == 16 ? launch_ragged<T, OUT, 16>(a, tpr, rows, s)
+                    : launch_ragged<T, OUT, 32>(a, tpr, rows, s);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      norm_config(dim3(static_cast<unsigned>((a.M + rows - 1) / rows)), dim3(tpr, rows), &attr, s);
+  return cudaLaunchKernelEx(&cfg, &norm_any_kernel<T, OUT>, static_cast<const T*>(a.x),
+                            static_cast<const T*>(a.residual), static_cast<const T*>(a.weight),
+                            a.M, static_cast<uint32_t>(a.K), a.eps, static_cast<T*>(a.h_out), a.y,
+                            a.scales);
 }
 template <typename T>
 cudaError_t launch_norm_out(const NormArgs& a, cudaStream_t s) {
