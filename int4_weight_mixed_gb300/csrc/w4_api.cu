@@ -878,6 +878,7 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
     ea.residual = ep.residual;
     ea.act = ep.act;
     ea.gated = ep.gated;
+    ea.vec = aligned16(out) && aligned16(ep.residual) && aligned16(bias) && aligned16(ch_scales);
     return launch(ea);
   };
 

@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kDkThreads, 2)
   // ---- epilogue: direct store, or split-K partials + last-arriver reduce
   auto store = [&](int64_t m, int64_t n, float vf, int32_t vi) {
     // lanes 4 apart hold neighbouring weight columns of the same rows
-    store_lane<MODE, 4>(args, m, n, m < M && n < N, vf, vi, 0xffffffffu);
+    const bool ok = m < M && n < N;
+    store_lane<MODE, 4>(args, m, n, ok, vf, vi, ep_side<MODE>(args, m, n, ok), 0xffffffffu);
   };
   if (p.ksplit == 1) {
 #pragma unroll

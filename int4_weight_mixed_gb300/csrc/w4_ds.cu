@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
       pc ? (MODE == kW4A8 ? 64 : (1 << 30)) : static_cast<int>(args.group_size / kBlkK);
   auto store = [&](int64_t m, int64_t n, float vf, int32_t vi) {
     // lanes 4 apart hold neighbouring weight columns of the same rows
-    store_lane<MODE, 4>(args, m, n, m < M && n < N, vf, vi, 0xffffffffu);
+    const bool ok = m < M && n < N;
+    store_lane<MODE, 4>(args, m, n, ok, vf, vi, ep_side<MODE>(args, m, n, ok), 0xffffffffu);
   };
 
   uint32_t it = 0, cs = 0, cph = 0;  // stage count, it % S, (it / S) & 1
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
 
     // ---- this tile's result: the output, or a partial slot for ds_reduce
     if (u.nslots == 1) {
+      ep_wait(args);
 #pragma unroll
       for (int R = 0; R < kDsRP; ++R)
 #pragma unroll
@@ -648,6 +650,7 @@ __global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p
   const int64_t n = static_cast<int64_t>(tile) * kTileN + col;
   const unsigned live = __ballot_sync(0xffffffffu, m < M && n < N);
   if (m >= M || n >= N) return;
+  const float side = ep_side<MODE>(args, m, n, true);  // in flight beside the partial sums
   const uint32_t* part = static_cast<const uint32_t*>(args.partials);
   const size_t off = static_cast<size_t>(m) * kTileN + col;
   float af = 0.f;
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p
       else af = sl == 0 ? __uint_as_float(x[q]) : af + __uint_as_float(x[q]);
     }
   }
-  store_lane<MODE, 1>(args, m, n, true, af, ai, live);
+  store_lane<MODE, 1>(args, m, n, true, af, ai, side, live);
 }
 
 namespace {

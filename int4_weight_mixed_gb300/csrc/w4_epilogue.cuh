@@ -89,15 +89,17 @@ __device__ __forceinline__ float ep_value(const EpArgs& args, int64_t m, int64_t
 }
 
 // act(v).  The logistic and the tanh go through one exponential; each is
-// exact to a few units of fp32, far below the output's 11 or 8 bits.
+// exact to a few units of fp32, far below the output's 11 or 8 bits.  (The
+// fast division gives 0 for a quotient by more than 2^126: SiLU and the tanh
+// form reach 0 at -87, where they are below 1e-36.)
 __device__ __forceinline__ float ep_act(float v, int act) {
   switch (act) {
     case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
-    case kActSilu: return v / (1.f + __expf(-v));
+    case kActSilu: return __fdividef(v, 1.f + __expf(-v));
     case kActGelu: return 0.5f * v * erfcf(v * -0.70710678f);  // exact in the tail too
     case kActGeluTanh: {  // (1 + tanh(u)) / 2 = 1 / (1 + e^-2u)
       const float u2 = 1.5957691f * fmaf(0.044715f * v * v, v, v);
-      return v / (1.f + __expf(-u2));
+      return __fdividef(v, 1.f + __expf(-u2));
     }
     default: return v;
   }
@@ -117,66 +119,181 @@ __device__ __forceinline__ void ep_store(const EpArgs& args, int64_t o, float r)
   static_cast<T16*>(args.out)[o] = ep_round<T16>(r);
 }
 
+// Where column n of row m goes: its element of out (gated: its pair's)
+__device__ __forceinline__ int64_t ep_offset(const EpArgs& args, int64_t m, int64_t n) {
+  return args.gated ? m * (args.N >> 1) + (n >> 1) : m * args.N + n;
+}
+// The residual that element (m, n) takes, to be asked for before the sums
+// are ready; nothing for a product without an epilogue of its own.  A grid
+// that may run beside the one that wrote the residual waits for it first
+// (ep_wait, by every thread that reads it).
+template <int MODE>
+__device__ __forceinline__ float ep_side(const TcArgs&, int64_t, int64_t, bool) { return 0.f; }
+template <int MODE>
+__device__ __forceinline__ float ep_side(const EpArgs& args, int64_t m, int64_t n, bool ok) {
+  return ok ? ep_residual<MODE>(args, ep_offset(args, m, n)) : 0.f;
+}
+__device__ __forceinline__ void ep_wait(const TcArgs&) {}
+__device__ __forceinline__ void ep_wait(const EpArgs&) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The output step of one element per lane, for both kinds of arguments: `ok`
-// says whether (m, n) is in range.  Lanes whose indexes differ in bit XOR
-// hold the columns n and n ^ 1 of the same row, and all lanes of `mask` call
-// it together.
+// says whether (m, n) is in range, `side` is ep_side of it.  Lanes whose
+// indexes differ in bit XOR hold the columns n and n ^ 1 of the same row, and
+// all lanes of `mask` call it together.
 template <int MODE, int XOR>
 __device__ __forceinline__ void store_lane(const TcArgs& args, int64_t m, int64_t n, bool ok,
-                                           float vf, int32_t vi, unsigned) {
+                                           float vf, int32_t vi, float, unsigned) {
   if (ok) store_out<MODE>(args, m, n, vf, vi);
 }
 template <int MODE, int XOR>
 __device__ __forceinline__ void store_lane(const EpArgs& args, int64_t m, int64_t n, bool ok,
-                                           float vf, int32_t vi, unsigned mask) {
-  const float v = ok ? ep_value<MODE>(args, m, n, vf, vi) : 0.f;
+                                           float vf, int32_t vi, float side, unsigned mask) {
+  float v = ok ? ep_value<MODE>(args, m, n, vf, vi) : 0.f;
+  bool mine = ok;
   if (args.gated) {
     const float up = __shfl_xor_sync(mask, v, XOR);
-    if (ok && !(n & 1)) {
-      const int64_t o = m * (args.N >> 1) + (n >> 1);
-      ep_store<MODE>(args, o, ep_act(v, args.act) * up + ep_residual<MODE>(args, o));
-    }
-  } else if (ok) {
-    const int64_t o = m * args.N + n;
-    ep_store<MODE>(args, o, ep_act(v, args.act) + ep_residual<MODE>(args, o));
+    mine = ok && !(n & 1);
+    if (mine) v = ep_act(v, args.act) * up;
+  } else {
+    v = ep_act(v, args.act);
   }
+  if (mine) ep_store<MODE>(args, ep_offset(args, m, n), v + side);
 }
 
-// The output step of eight rows m0..m0+7 of column n, one column per lane of
-// a full warp (the lanes cover 32 columns from a multiple of 32): d holds the
-// sums (fp32 bits, or int32).  Gated: even lanes take the first four rows of
-// their pair of columns, odd lanes the last four, so all lanes work and each
-// stored row covers 32 contiguous bytes.
+// ------------------------------------------- eight rows by 32 columns a warp
+// The tensor-core schedules hand a warp eight rows of 32 columns, a column a
+// lane.  Here the block is transposed by shuffles, so that lane l has row
+// l % 8 and the eight columns from 8 * (l / 8): the residual is one 16-byte
+// load and out one 16-byte store a lane (8 bytes each when gated, whose pairs
+// then lie in one lane), where a column a lane takes eight 2-byte ones.
+// (W4A8 1024 x 8192 x 21760 with a residual: %%.)
+
+// The residual of a lane's eight columns (gated: of its four pairs)
 template <int MODE>
-__device__ __forceinline__ void store_block8(const EpArgs& args, int64_t m0, int64_t n,
-                                             const uint32_t (&d)[8]) {
-  const bool col = n < args.N;
+__device__ __forceinline__ uint4 ep_side8(const EpArgs& args, int64_t m0, int64_t n0) {
+  const int lane = threadIdx.x & 31;
+  const int64_t m = m0 + (lane & 7), n = n0 + (lane >> 3) * 8;
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if (!args.residual || m >= args.M || n >= args.N) return r;
+  const unsigned short* p =
+      static_cast<const unsigned short*>(args.residual) + ep_offset(args, m, n);
+  if (args.vec) {
+    if (args.gated) {
+      const uint2 h = __ldcg(reinterpret_cast<const uint2*>(p));
+      r.x = h.x;
+      r.y = h.y;
+    } else {
+      r = __ldcg(reinterpret_cast<const uint4*>(p));
+    }
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < 4 || !args.gated) w[e >> 1] |= static_cast<uint32_t>(__ldcg(p + e)) << (16 * (e & 1));
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+// brings that residual nearer while the sums are still being made
+__device__ __forceinline__ void ep_prefetch8(const EpArgs& args, int64_t m0, int64_t n0) {
+  const int lane = threadIdx.x & 31;
+  const int64_t m = m0 + (lane & 7), n = n0 + (lane >> 3) * 8;
+  if (args.residual && m < args.M && n < args.N)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+        static_cast<const unsigned short*>(args.residual) + ep_offset(args, m, n)));
+}
+
+template <typename T16>
+__device__ __forceinline__ float2 ep_pair(uint32_t w) {
+  return make_float2(ep_f32(reinterpret_cast<const T16*>(&w)[0]),
+                     ep_f32(reinterpret_cast<const T16*>(&w)[1]));
+}
+template <typename T16>
+__device__ __forceinline__ uint32_t ep_pack(float a, float b) {
+  T16 h[2] = {ep_round<T16>(a), ep_round<T16>(b)};
+  return *reinterpret_cast<const uint32_t*>(h);
+}
+
+// d: the sums (fp32 bits, or int32) of rows m0..m0+7 of column n0 + lane, n0
+// a multiple of 32; N is a multiple of 8.  side: ep_side8.
+template <int MODE>
+__device__ __forceinline__ void store_block8(const EpArgs& args, int64_t m0, int64_t n0,
+                                             const uint32_t (&d)[8], const uint4& side) {
+  using T16 = typename std::conditional<MODE == kW4A16_BF16, __nv_bfloat16, __half>::type;
+  const int lane = threadIdx.x & 31;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    v[i] = col && m0 + i < args.M ? ep_value<MODE>(args, m0 + i, n, __uint_as_float(d[i]),
-                                                   static_cast<int32_t>(d[i]))
-                                  : 0.f;
+    v[i] = MODE == kW4A8 ? static_cast<float>(static_cast<int32_t>(d[i])) : __uint_as_float(d[i]);
+#pragma unroll
+  for (int s = 1; s < 8; s *= 2) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & s) continue;
+      const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i | s], s);
+      if (up) v[i] = got;
+      else v[i | s] = got;
+    }
+  }
+  const int64_t m = m0 + (lane & 7), n = n0 + (lane >> 3) * 8;
+  if (m >= args.M || n >= args.N) return;
+  if constexpr (MODE == kW4A8 || MODE == kW4A8F8) {
+    const float st = args.s_tok[m];
+    if (args.vec) {
+      const float4 a = *reinterpret_cast<const float4*>(args.s_ch + n);
+      const float4 b = *reinterpret_cast<const float4*>(args.s_ch + n + 4);
+      const float sc[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * st * sc[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * st * args.s_ch[n + e];
+    }
+  }
+  if (args.bias) {
+    const T16* b = static_cast<const T16*>(args.bias) + n;
+    if (args.vec) {
+      const uint4 w = *reinterpret_cast<const uint4*>(b);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = ep_pair<T16>(u[i]);
+        v[2 * i] += p.x;
+        v[2 * i + 1] += p.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += ep_f32(b[e]);
+    }
+  }
+  const uint32_t r[4] = {side.x, side.y, side.z, side.w};
+  uint32_t o[4];
   if (args.gated) {
-    const bool odd = n & 1;
-    const int64_t cols = args.N >> 1, mh = m0 + (odd ? 4 : 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 p = ep_pair<T16>(r[i]);
+      o[i] = ep_pack<T16>(ep_act(v[4 * i], args.act) * v[4 * i + 1] + p.x,
+                          ep_act(v[4 * i + 2], args.act) * v[4 * i + 3] + p.y);
+    }
+    o[2] = o[3] = 0u;
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[4 + i], 1);
-      const float gate = odd ? other : v[i], up = odd ? v[4 + i] : other;
-      if (!col || mh + i >= args.M) continue;
-      const int64_t o = (mh + i) * cols + (n >> 1);
-      ep_store<MODE>(args, o, ep_act(gate, args.act) * up + ep_residual<MODE>(args, o));
+      const float2 p = ep_pair<T16>(r[i]);
+      o[i] = ep_pack<T16>(ep_act(v[2 * i], args.act) + p.x, ep_act(v[2 * i + 1], args.act) + p.y);
     }
+  }
+  T16* const out = static_cast<T16*>(args.out) + ep_offset(args, m, n);
+  if (args.vec) {
+    if (args.gated) *reinterpret_cast<uint2*>(out) = make_uint2(o[0], o[1]);
+    else *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
   } else {
-    float r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      r[i] = col && m0 + i < args.M ? ep_residual<MODE>(args, (m0 + i) * args.N + n) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col && m0 + i < args.M)
-        ep_store<MODE>(args, (m0 + i) * args.N + n, ep_act(v[i], args.act) + r[i]);
+    for (int e = 0; e < 8; ++e)
+      if (e < 4 || !args.gated) out[e] = reinterpret_cast<const T16*>(o)[e];
   }
 }
 

@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
     // ---- this CTA's sums of its K range: the output (C == 1), or the
     // partial-sum tile of the cluster reduction
     if (C == 1) {
+      ep_wait(args);
 #pragma unroll
       for (int R = 0; R < RP; ++R)
 #pragma unroll
@@ -515,8 +516,9 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
             const int64_t m = j * 8 + 2 * t + (e & 1);
             const int64_t n = n0 + Cols * w + 16 * R + g + 8 * (e >> 1);
             // lanes 4 apart hold neighbouring weight columns of the same rows
-            store_lane<MODE, 4>(args, m, n, m < M && n < N, res[R][j][e], ires[R][j][e],
-                                0xffffffffu);
+            const bool ok = m < M && n < N;
+            store_lane<MODE, 4>(args, m, n, ok, res[R][j][e], ires[R][j][e],
+                                ep_side<MODE>(args, m, n, ok), 0xffffffffu);
           }
     } else {
 #pragma unroll
@@ -535,49 +537,44 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
   if (C == 1) return;
 
   // ---- cluster reduction: CTA `rank` owns columns [c_lo, c_hi) of the tile
-  cluster_sync();
   if constexpr (std::is_same<Args, EpArgs>::value) {
-    // a thread takes both columns of a pair (a gate and what it multiplies)
-    const int p_lo = rank * (kTileN / 2) / C, p_hi = (rank + 1) * (kTileN / 2) / C;
-    const int np = p_hi - p_lo;
-    const int rows = static_cast<int>(M < 8 * NJ ? M : 8 * NJ);
+    // ranges that keep the columns of a pair (a gate and what it multiplies)
+    // together, in neighbouring lanes; every lane of a warp takes every turn
+    const int c_lo = 2 * (rank * (kTileN / 2) / C), c_hi = 2 * ((rank + 1) * (kTileN / 2) / C);
+    const int nc = c_hi - c_lo, rows = static_cast<int>(M < 8 * NJ ? M : 8 * NJ);
     const uint32_t red0 = smem_addr(red);
-    for (int i = threadIdx.x; i < rows * np; i += GvShape<NJ>::Threads) {
-      const int m = i / np, col = 2 * (p_lo + (i - m * np));
-      float v[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int64_t n = n0 + col + e;
-        const uint32_t local = red0 + static_cast<uint32_t>(m * kTileN + col + e) * 4;
-        uint32_t parts[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (q < C) parts[q] = ld_dsmem(dsmem_addr(local, static_cast<uint32_t>(q)));
-        float af = __uint_as_float(parts[0]);
-        int32_t ai = static_cast<int32_t>(parts[0]);
-#pragma unroll
-        for (int q = 1; q < 16; ++q)
-          if (q < C) {
-            af += __uint_as_float(parts[q]);
-            ai += static_cast<int32_t>(parts[q]);
-          }
-        v[e] = n < N ? ep_value<MODE>(args, m, n, af, ai) : 0.f;
+    auto element = [&](int i, int& m, int& col) {
+      m = i / nc;
+      col = c_lo + (i - m * nc);
+      return i < rows * nc && n0 + col < N;
+    };
+    ep_wait(args);
+    int m, col;
+    bool ok = element(threadIdx.x, m, col);
+    float side = ep_side<MODE>(args, m, n0 + col, ok);  // in flight across the barrier
+    cluster_sync();
+    for (int i0 = 0; i0 < rows * nc; i0 += GvShape<NJ>::Threads) {
+      if (i0 > 0) {
+        ok = element(i0 + threadIdx.x, m, col);
+        side = ep_side<MODE>(args, m, n0 + col, ok);
       }
-      const int64_t n = n0 + col;
-      if (n >= N) continue;
-      if (args.gated) {
-        const int64_t o = m * (N >> 1) + (n >> 1);
-        ep_store<MODE>(args, o, ep_act(v[0], args.act) * v[1] + ep_residual<MODE>(args, o));
-      } else {
+      const uint32_t local = red0 + static_cast<uint32_t>(ok ? m * kTileN + col : 0) * 4;
+      uint32_t parts[16];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (n + e >= N) break;
-          const int64_t o = m * N + n + e;
-          ep_store<MODE>(args, o, ep_act(v[e], args.act) + ep_residual<MODE>(args, o));
+      for (int q = 0; q < 16; ++q)
+        if (q < C) parts[q] = ld_dsmem(dsmem_addr(local, static_cast<uint32_t>(q)));
+      float af = __uint_as_float(parts[0]);
+      int32_t ai = static_cast<int32_t>(parts[0]);
+#pragma unroll
+      for (int q = 1; q < 16; ++q)
+        if (q < C) {
+          af += __uint_as_float(parts[q]);
+          ai += static_cast<int32_t>(parts[q]);
         }
-      }
+      store_lane<MODE, 1>(args, m, n0 + col, ok, af, ai, side, 0xffffffffu);
     }
   } else {
+    cluster_sync();
     const int c_lo = rank * kTileN / C, c_hi = (rank + 1) * kTileN / C;
     const int nc = c_hi - c_lo;
     const int rows = static_cast<int>(M < 8 * NJ ? M : 8 * NJ);

@@ -173,8 +173,8 @@ __global__ void simt_w4a16_kernel(const T* __restrict__ a, Args args) {
         acc = fmaf(to_f(a[m * K + k0 + j]), to_f(w), acc);
       }
     }
-    store_lane<std::is_same<T, __half>::value ? kW4A16_F16 : kW4A16_BF16, 1>(args, m, n, true, acc,
-                                                                            0, live);
+    constexpr int MODE = std::is_same<T, __half>::value ? kW4A16_F16 : kW4A16_BF16;
+    store_lane<MODE, 1>(args, m, n, true, acc, 0, ep_side<MODE>(args, m, n, true), live);
   }
 }
 
@@ -198,7 +198,7 @@ __global__ void simt_w4a8_kernel(const int8_t* __restrict__ a, Args args) {
         acc += static_cast<int32_t>(a[m * K + k0 + j]) * v * mul;
       }
     }
-    store_lane<kW4A8, 1>(args, m, n, true, 0.f, acc, live);
+    store_lane<kW4A8, 1>(args, m, n, true, 0.f, acc, ep_side<kW4A8>(args, m, n, true), live);
   }
 }
 
@@ -222,7 +222,7 @@ __global__ void simt_w4a8f8_kernel(const __nv_fp8_storage_t* __restrict__ a, Arg
         acc = fmaf(__half2float(h), v, acc);
       }
     }
-    store_lane<kW4A8F8, 1>(args, m, n, true, acc, 0, live);
+    store_lane<kW4A8F8, 1>(args, m, n, true, acc, 0, ep_side<kW4A8F8>(args, m, n, true), live);
   }
 }
 

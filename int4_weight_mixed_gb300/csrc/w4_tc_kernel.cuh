@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr uint32_t WB = F8 ? 8192u : 4096u;
   constexpr int CPB = BK / kChunkK;  // 32-K chunks per block
   constexpr int NCTA = PAIR ? 2 : 1;
+  constexpr bool EP = std::is_same<Args, EpArgs>::value;  // an epilogue of its own
   if constexpr (PAIR) {
     // launched without its two-CTA clusters: nothing may run
     if (cluster_size() != 2) {
@@ -997,6 +998,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
+          // An epilogue of its own: the residual too, which another grid may
+          // just have written
+          [[maybe_unused]] const bool writes = final_ev && !(split && !reducer);
+          if constexpr (EP) {
+            if (writes) {
+              ep_wait(args);
+              for (int bb = grp; bb < NT * nblk; bb += kConvGroups) {
+                const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
+                ep_prefetch8(args, m0 + cc, n0 + t * kTileN + q * 32);
+              }
+            }
+          }
           if (!__all_sync(0xffffffffu, mbar_wait<true>(sm.dfull, ev & 1, abort, args.status))) {
             return false;
           }
@@ -1021,8 +1034,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // further on, so that each 16-byte access of a warp covers 512
           // contiguous bytes; partial sums otherwise: row r of the block
           // holds its 8 columns contiguously at r * 8.
+          [[maybe_unused]] uint4 side_next = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (EP) {
+            if (writes) {
+              const int t = LEAN ? 0 : grp / nblk;
+              if (grp < NT * nblk)
+                side_next = ep_side8<MODE>(args, m0 + (grp - t * nblk) * 8, n0 + t * kTileN + q * 32);
+            }
+          }
           for (int bb = grp; bb < NT * nblk; bb += kConvGroups) {
             const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
+            // this block's residual has been asked for one block ago
+            [[maybe_unused]] const uint4 side = side_next;
+            if constexpr (EP) {
+              const int nb = bb + kConvGroups, nt2 = LEAN ? 0 : nb / nblk;
+              if (writes && nb < NT * nblk)
+                side_next = ep_side8<MODE>(args, m0 + (nb - nt2 * nblk) * 8,
+                                           n0 + nt2 * kTileN + q * 32);
+            }
             const uint32_t dcol = tmem + lane_base + t * BM + cc;
             const int64_t nrow = n0 + t * kTileN + r;  // output column
             const size_t goff = static_cast<size_t>(bb) * 1024 + q * 256 + lane * 4;
@@ -1089,8 +1118,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int i = 0; i < 8; ++i) d[i] = acc[i];
             }
             // outputs
-            if constexpr (std::is_same<Args, EpArgs>::value) {
-              store_block8<MODE>(args, m0 + cc, nrow, d);
+            if constexpr (EP) {
+              store_block8<MODE>(args, m0 + cc, n0 + t * kTileN + q * 32, d, side);
             } else {
   #pragma unroll
               for (int i = 0; i < 8; ++i) {
