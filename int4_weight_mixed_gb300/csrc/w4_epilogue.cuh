@@ -105,6 +105,25 @@ __device__ __forceinline__ float ep_act(float v, int act) {
   }
 }
 
+// act of each of n values: one branch for all of them
+template <int N>
+__device__ __forceinline__ void ep_act_n(float (&v)[N], int act) {
+  switch (act) {
+#define W4_ACT_CASE(A)                              \
+  case A:                                           \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) { \
+      v[i] = ep_act(v[i], A);                       \
+    }                                               \
+    break;
+    W4_ACT_CASE(kActRelu)
+    W4_ACT_CASE(kActSilu)
+    W4_ACT_CASE(kActGelu)
+    W4_ACT_CASE(kActGeluTanh)
+#undef W4_ACT_CASE
+    default: break;
+  }
+}
+
 // output element o = m * columns + column from its value before the residual
 template <int MODE>
 __device__ __forceinline__ float ep_residual(const EpArgs& args, int64_t o) {
@@ -272,18 +291,20 @@ __device__ __forceinline__ void store_block8(const EpArgs& args, int64_t m0, int
   const uint32_t r[4] = {side.x, side.y, side.z, side.w};
   uint32_t o[4];
   if (args.gated) {
+    float g[4] = {v[0], v[2], v[4], v[6]};
+    ep_act_n(g, args.act);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float2 p = ep_pair<T16>(r[i]);
-      o[i] = ep_pack<T16>(ep_act(v[4 * i], args.act) * v[4 * i + 1] + p.x,
-                          ep_act(v[4 * i + 2], args.act) * v[4 * i + 3] + p.y);
+      o[i] = ep_pack<T16>(g[2 * i] * v[4 * i + 1] + p.x, g[2 * i + 1] * v[4 * i + 3] + p.y);
     }
     o[2] = o[3] = 0u;
   } else {
+    ep_act_n(v, args.act);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 p = ep_pair<T16>(r[i]);
-      o[i] = ep_pack<T16>(ep_act(v[2 * i], args.act) + p.x, ep_act(v[2 * i + 1], args.act) + p.y);
+      o[i] = ep_pack<T16>(v[2 * i] + p.x, v[2 * i + 1] + p.y);
     }
   }
   T16* const out = static_cast<T16*>(args.out) + ep_offset(args, m, n);

@@ -1034,23 +1034,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // further on, so that each 16-byte access of a warp covers 512
           // contiguous bytes; partial sums otherwise: row r of the block
           // holds its 8 columns contiguously at r * 8.
-          [[maybe_unused]] uint4 side_next = make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (EP) {
-            if (writes) {
-              const int t = LEAN ? 0 : grp / nblk;
-              if (grp < NT * nblk)
-                side_next = ep_side8<MODE>(args, m0 + (grp - t * nblk) * 8, n0 + t * kTileN + q * 32);
+          // the residuals of this warp's next blocks, kSideAhead of them asked
+          // for ahead
+          constexpr int kSideAhead = 3;
+          [[maybe_unused]] uint4 sides[kSideAhead];
+          [[maybe_unused]] auto side_of = [&](int b) {
+            if constexpr (EP) {
+              const int t = LEAN ? 0 : b / nblk;
+              if (writes && b < NT * nblk)
+                return ep_side8<MODE>(args, m0 + (b - t * nblk) * 8, n0 + t * kTileN + q * 32);
             }
+            return make_uint4(0u, 0u, 0u, 0u);
+          };
+          if constexpr (EP) {
+#pragma unroll
+            for (int i = 0; i < kSideAhead; ++i) sides[i] = side_of(grp + i * kConvGroups);
           }
           for (int bb = grp; bb < NT * nblk; bb += kConvGroups) {
             const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
-            // this block's residual has been asked for one block ago
-            [[maybe_unused]] const uint4 side = side_next;
+            [[maybe_unused]] uint4 side;
             if constexpr (EP) {
-              const int nb = bb + kConvGroups, nt2 = LEAN ? 0 : nb / nblk;
-              if (writes && nb < NT * nblk)
-                side_next = ep_side8<MODE>(args, m0 + (nb - nt2 * nblk) * 8,
-                                           n0 + nt2 * kTileN + q * 32);
+              side = sides[0];
+#pragma unroll
+              for (int i = 1; i < kSideAhead; ++i) sides[i - 1] = sides[i];
+              sides[kSideAhead - 1] = side_of(bb + kSideAhead * kConvGroups);
             }
             const uint32_t dcol = tmem + lane_base + t * BM + cc;
             const int64_t nrow = n0 + t * kTileN + r;  // output column
