@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(128 * NJ) ds_prep_kernel(const void* __restric
 template <int MODE, int NJ, class Args>
 __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
     ds_gemm_kernel(const DsPlan p, const Args args, const uint8_t* __restrict__ prep) {
+  constexpr bool EP = std::is_same<Args, EpArgs>::value;  // an epilogue of its own
   constexpr int kDsRP = DsShape<NJ>::RP, kDsCols = DsShape<NJ>::Cols;
   constexpr int kDsConsumers = DsShape<NJ>::Consumers;
   constexpr int kDsWProd = DsShape<NJ>::WProd, kDsAProd = DsShape<NJ>::AProd;
@@ -410,9 +411,8 @@ __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
   const int fold_blocks =
       pc ? (MODE == kW4A8 ? 64 : (1 << 30)) : static_cast<int>(args.group_size / kBlkK);
   auto store = [&](int64_t m, int64_t n, float vf, int32_t vi) {
-    // lanes 4 apart hold neighbouring weight columns of the same rows
-    const bool ok = m < M && n < N;
-    store_lane<MODE, 4>(args, m, n, ok, vf, vi, ep_side<MODE>(args, m, n, ok), 0xffffffffu);
+    if (m >= M || n >= N) return;
+    if constexpr (!EP) store_out<MODE>(args, m, n, vf, vi);
   };
 
   uint32_t it = 0, cs = 0, cph = 0;  // stage count, it % S, (it / S) & 1
@@ -588,8 +588,10 @@ __global__ void __launch_bounds__(DsShape<NJ>::Threads, ds_ctas_per_sm(NJ))
     if (!ok) break;
 
     // ---- this tile's result: the output, or a partial slot for ds_reduce
-    if (u.nslots == 1) {
-      ep_wait(args);
+    // (An epilogue of its own is left to ds_reduce for every tile: in this
+    // kernel its code costs the main loop registers.  W4A8 M=32 N=8192
+    // K=21760: %% us with it here, %% there.)
+    if (!EP && u.nslots == 1) {
 #pragma unroll
       for (int R = 0; R < kDsRP; ++R)
 #pragma unroll
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(kDsRedThreads) ds_reduce_kernel(const DsPlan p
   const int64_t cf = ds_owner(static_cast<int64_t>(tile) * p.kblocks, T, G);
   const int64_t cl = ds_owner((static_cast<int64_t>(tile) + 1) * p.kblocks - 1, T, G);
   const int nslots = static_cast<int>(cl - cf + 1);
-  if (nslots == 1) return;
+  if (!std::is_same<Args, EpArgs>::value && nslots == 1) return;  // ds_gemm stored it
   const size_t slot_elems = static_cast<size_t>(8 * NJ) * kTileN;
   auto slot_base = [&](int sl) -> unsigned long long {
     const int64_t cpr = cf + sl;

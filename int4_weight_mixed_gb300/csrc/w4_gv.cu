@@ -210,6 +210,7 @@ template <int MODE, int NJ, class Args>
 __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
     gv_gemm_kernel(const __grid_constant__ CUtensorMap amap, const GvPlan p, const Args args) {
   constexpr int RP = GvShape<NJ>::RP, Cols = GvShape<NJ>::Cols;
+  constexpr bool EP = std::is_same<Args, EpArgs>::value;  // an epilogue of its own
   constexpr int Consumers = GvShape<NJ>::Consumers, Prod = GvShape<NJ>::Prod;
   constexpr bool F16 = MODE == kW4A16_F16;
   using T16 = typename std::conditional<F16, __half, __nv_bfloat16>::type;
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
     (void)ok;
     // ---- this CTA's sums of its K range: the output (C == 1), or the
     // partial-sum tile of the cluster reduction
-    if (C == 1) {
-      ep_wait(args);
+    // (An epilogue of its own has one place, the reduction, whatever C.)
+    if (!EP && C == 1) {
 #pragma unroll
       for (int R = 0; R < RP; ++R)
 #pragma unroll
@@ -515,10 +516,8 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
           for (int e = 0; e < 4; ++e) {
             const int64_t m = j * 8 + 2 * t + (e & 1);
             const int64_t n = n0 + Cols * w + 16 * R + g + 8 * (e >> 1);
-            // lanes 4 apart hold neighbouring weight columns of the same rows
-            const bool ok = m < M && n < N;
-            store_lane<MODE, 4>(args, m, n, ok, res[R][j][e], ires[R][j][e],
-                                ep_side<MODE>(args, m, n, ok), 0xffffffffu);
+            if constexpr (!EP)
+              if (m < M && n < N) store_out<MODE>(args, m, n, res[R][j][e], ires[R][j][e]);
           }
     } else {
 #pragma unroll
@@ -534,10 +533,10 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
           }
     }
   }
-  if (C == 1) return;
+  if (!EP && C == 1) return;
 
   // ---- cluster reduction: CTA `rank` owns columns [c_lo, c_hi) of the tile
-  if constexpr (std::is_same<Args, EpArgs>::value) {
+  if constexpr (EP) {
     // ranges that keep the columns of a pair (a gate and what it multiplies)
     // together, in neighbouring lanes; every lane of a warp takes every turn
     const int c_lo = 2 * (rank * (kTileN / 2) / C), c_hi = 2 * ((rank + 1) * (kTileN / 2) / C);
