@@ -557,19 +557,25 @@ __global__ void __launch_bounds__(GvShape<NJ>::Threads, gv_ctas_per_sm(NJ))
         ok = element(i0 + threadIdx.x, m, col);
         side = ep_side<MODE>(args, m, n0 + col, ok);
       }
-      const uint32_t local = red0 + static_cast<uint32_t>(ok ? m * kTileN + col : 0) * 4;
-      uint32_t parts[16];
+      if (i0 + static_cast<int>(threadIdx.x & ~31u) >= rows * nc) break;  // none in this warp
+      float af = 0.f;
+      int32_t ai = 0;
+      if (ok) {
+        const uint32_t local = red0 + static_cast<uint32_t>(m * kTileN + col) * 4;
+        uint32_t parts[16];
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (q < C) parts[q] = ld_dsmem(dsmem_addr(local, static_cast<uint32_t>(q)));
-      float af = __uint_as_float(parts[0]);
-      int32_t ai = static_cast<int32_t>(parts[0]);
+        for (int q = 0; q < 16; ++q)
+          if (q < C) parts[q] = ld_dsmem(dsmem_addr(local, static_cast<uint32_t>(q)));
+        af = __uint_as_float(parts[0]);
+        ai = static_cast<int32_t>(parts[0]);
 #pragma unroll
-      for (int q = 1; q < 16; ++q)
-        if (q < C) {
-          af += __uint_as_float(parts[q]);
-          ai += static_cast<int32_t>(parts[q]);
-        }
+        for (int q = 1; q < 16; ++q)
+          if (q < C) {
+            af += __uint_as_float(parts[q]);
+            ai += static_cast<int32_t>(parts[q]);
+          }
+      }
+      __syncwarp();
       store_lane<MODE, 1>(args, m, n0 + col, ok, af, ai, side, 0xffffffffu);
     }
   } else {
