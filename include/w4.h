@@ -207,8 +207,10 @@ typedef enum w4_act {
  *   residual  array of out's type and shape, or NULL.  It may be out itself
  *             (the residual stream updated in place).
  * With act NONE, gated 0 and residual NULL this is exactly w4_gemm_bias.
- * The schedules, workspace and heuristic are those of w4_gemm for the same
- * M, N and K.  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
+ * The schedules and workspace are those of w4_gemm for the same M, N and K,
+ * and a given schedule sums in the same order; beyond 16 rows the default
+ * one is chosen by a rule of its own (the least estimated time; overrides
+ * come first).  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
  * an odd N with gated, an epilogue on the raw int32 output, a residual not
  * aligned to 2 bytes or one that overlaps out without being out.  With
  * K == 0 the product is 0. */

@@ -513,6 +513,114 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
   return 0;
 }
 
+// ---------------------------------------------------------------------------
+// The schedule of a product with an epilogue of its own, beyond 16 rows: the
+// one whose plan has the least estimated time.  (Up to 16 rows the rule above
+// is within 1% of the fastest.  The plain product keeps that rule at every
+// size, and with it the order of its sums; an epilogue's schedules, sums and
+// plans are otherwise the plain product's.)
+//
+// A tensor-core plan takes a fixed time, one time per pipeline stage of its
+// busiest CTA, one per tile that CTA drains (more with taller tiles) and one
+// per partial-sum slot that the last contributor of a split tile adds; W4A8
+// also the pass that stages its activations.  The constants (microseconds)
+// are fitted to timings of every schedule at 8200 shapes (fp16 / bf16 g128
+// and per-channel, int8 per-channel and g128, E4M3; M 1..4096, N 256..57344,
+// K 512..28672).  On 2700 other shapes, drawn over the logarithm of each size,
+// the pick is within 1.5-2.3% of the fastest schedule in the geometric mean of
+// each type (at most 1.53 times, on a product of 18 us), where the rule above
+// is 23-34% off, mostly on products of few tiles (M=200 N=992 K=4608 int8
+// g128: tc256p_sk 92 us, 18 contributors a tile; tc64_sk 23).
+enum CostClass { kCost16 = 0, kCostS8 = 1, kCostS8G = 2, kCostF8 = 3 };
+struct TcCost {
+  double fixed;
+  double stage[7];  // tiles of 16, 32, 64, 128, 256 rows, pairs of 128, 256
+  double drain_row, staging;
+};
+constexpr TcCost kTcCost[4] = {
+    {2.29, {1.10, 1.12, 1.16, 0.69, 0.51, 0.57, 0.29}, 0.026, 0.0},
+    {2.21, {1.04, 1.04, 1.06, 0.63, 0.44, 0.59, 0.31}, 0.040, 7.1e-7},
+    {1.85, {1.61, 1.66, 1.80, 1.09, 0.86, 1.01, 0.66}, 0.026, 7.1e-7},
+    {1.56, {1.50, 1.55, 0.88, 0.91, 0.68, 0.74, 0.39}, 0.026, 0.0}};
+constexpr double kTcDrain = 3.1, kTcSlot = 0.52, kTcSlotRow = 0.0147;
+// streamed at 32 rows: fixed, per 128-K block of the busiest CTA, per slot
+constexpr double kDs32Cost[3][3] = {{5.25, 0.643, 0.084}, {5.55, 0.571, 0.103}, {5.27, 0.805, 0.105}};
+// clustered at 32 rows: fixed, per 128-K block of the busiest CTA
+constexpr double kGv32Cost[4][2] = {{3.85, 1.50}, {3.93, 1.33}, {3.77, 1.57}, {4.04, 1.10}};
+
+double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
+  const Schedule& sc = kSchedules[si];
+  const int cls = mode == kW4A8 ? (gs < K ? kCostS8G : kCostS8) : mode == kW4A8F8 ? kCostF8 : kCost16;
+  if (sc.engine == kEngineGv) {
+    const GvPlan p = make_gv_plan(si, mode, M, N, K);
+    if (p.grid > sm_count() * gv_ctas_per_sm(p.nj)) return 1e30;  // more than one wave
+    return kGv32Cost[cls][0] + kGv32Cost[cls][1] * ((p.kblocks + p.cluster - 1) / p.cluster);
+  }
+  if (sc.engine == kEngineDs) {
+    const DsPlan p = make_ds_plan(si, mode, M, N, K);
+    const int64_t T = static_cast<int64_t>(p.n_tiles) * p.kblocks, per = (T + p.grid - 1) / p.grid;
+    const int64_t least = std::max<int64_t>(T / p.grid, 1);
+    return kDs32Cost[cls][0] + kDs32Cost[cls][1] * per +
+           kDs32Cost[cls][2] * ((p.kblocks + least - 1) / least);
+  }
+  const TcPlan p = make_plan(si, mode, M, N, K, gs);
+  const TcCost& c = kTcCost[cls];
+  const int units = p.grid / (p.pair ? 2 : 1);
+  const int row = p.pair ? (p.bm == 128 ? 5 : 6)
+                         : p.bm == 16 ? 0 : p.bm == 32 ? 1 : p.bm == 64 ? 2 : p.bm == 128 ? 3 : 4;
+  double stages, drains, slots = 0;
+  if (p.decomp == kDataParallel) {
+    drains = (p.tiles + units - 1) / units;
+    stages = drains * p.kb_total;
+  } else {
+    const int64_t T = static_cast<int64_t>(p.tiles) * p.kb_total, it = (T + units - 1) / units;
+    stages = static_cast<double>(it);
+    drains = static_cast<double>(it) / p.kb_total + 1;
+    slots = it < p.kb_total ? static_cast<double>((p.kb_total + it - 1) / it)
+                            : (T % units != 0 || it % p.kb_total != 0 ? 1 : 0);
+  }
+  return c.fixed + stages * c.stage[row] + drains * (kTcDrain + c.drain_row * p.bm) +
+         slots * (kTcSlot + kTcSlotRow * p.bm) + c.staging * static_cast<double>(M) * K;
+}
+
+int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
+  const int plain = default_schedule_impl(mode, M, N, K, gs, has_sg);
+  if (M <= 16 || kSchedules[plain].engine == kEngineSimt || override_for(mode, M, N, K, gs) == plain)
+    return plain;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  const auto key = std::make_tuple(mode, M, N, K, gs, has_sg, dev);
+  static std::mutex mu;
+  static std::map<decltype(key), int> cache;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+  }
+  int best = plain;
+  double best_us = 1e30;
+  for (int si = 1; si < kNumSchedules; ++si) {
+    const Schedule& sc = kSchedules[si];
+    // one weight tile a CTA, stream-K or data-parallel; or 32-row decode
+    const bool takes = sc.engine == kEngineTc
+                           ? sc.nt == 1 && sc.decomp != kSplitK
+                           : sc.bm == 32 && (sc.engine == kEngineGv || sc.engine == kEngineDs);
+    if (!takes || !schedule_fits(si, mode, M, N, K, gs, has_sg)) continue;
+    const double us = estimated_us(si, mode, M, N, K, gs);
+    if (us < best_us) {
+      best_us = us;
+      best = si;
+    }
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache.size() >= 4096) cache.clear();
+  cache.emplace(key, best);
+  return best;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -837,7 +945,9 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
   }
   int si = schedule;
   const bool forced = schedule >= 0;
-  if (!forced) si = default_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg);
+  if (!forced)
+    si = ep.any() ? epilogue_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg)
+                  : default_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg);
   if (!schedule_fits(si, pr.mode, M, N, K, pr.gs, pr.has_sg))
     return fail(W4_ERR_UNSUPPORTED, "schedule %s cannot run this shape", kSchedules[si].name);
   const bool ptrs_ok = aligned16(a) && aligned16(b_packed) && aligned16(b_scales) &&
@@ -1063,7 +1173,7 @@ struct DynLayout {
   bool prestage;    // tensor-core int8: the quantizer writes the bf16 copy
   size_t gemm_ws, codes, stok, total;
 };
-DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs) {
+DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs, bool epilogue) {
   DynLayout d{};
   Problem pr{};
   pr.mode = mode_of(act_type);
@@ -1072,7 +1182,8 @@ DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs) 
   pr.K = K;
   pr.gs = gs;
   pr.has_sg = gs != K;
-  d.si = default_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg);
+  d.si = epilogue ? epilogue_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg)
+                  : default_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg);
   d.prestage = pr.mode == kW4A8 && kSchedules[d.si].engine == kEngineTc && K % 8 == 0 &&
                K <= 32768;
   // the GEMM part always spans the status word and the split-K counters
@@ -1097,7 +1208,7 @@ size_t w4_gemm_dynamic_workspace_size(int64_t M, int64_t N, int64_t K, int act_t
   if (act_type == W4_E4M3 && K % 128 != 0) return kWsHeader;
   // the largest over the schedules the call may take (the default one),
   // with room for any schedule an override may name
-  const DynLayout d = dyn_layout(act_type, M, N, K, gs);
+  const DynLayout d = dyn_layout(act_type, M, N, K, gs, false);
   const size_t any = w4_gemm_workspace_size(M, N, K, act_type, group_size);
   const size_t extra = d.total - d.gemm_ws;
   return (any > d.gemm_ws ? align256(any) : d.gemm_ws) + extra;
@@ -1128,7 +1239,7 @@ w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const vo
   if (K == 0 || K % kStageK != 0 || (act_type == W4_E4M3 && K % 128 != 0))
     return fail(W4_ERR_UNSUPPORTED, "K must be a positive multiple of 64 (128 for fp8)");
   if (!workspace || !aligned16(workspace)) return fail(W4_ERR_WORKSPACE, "workspace is null or not 16-byte aligned");
-  const DynLayout d = dyn_layout(act_type, M, N, K, gs);
+  const DynLayout d = dyn_layout(act_type, M, N, K, gs, ep.any());
   if (workspace_bytes < d.total)
     return fail(W4_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, d.total);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
