@@ -140,7 +140,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // The rows' reductions: sum and A of each row's blockDim.x threads (a power
 // of two up to 32, or a multiple of 32), in an order that depends on
-// blockDim.x alone; red: [2][kNormMaxThreads / 32].
+// blockDim.x alone, which every launch takes from K: the bits of a row do not
+// depend on how many rows there are.  red: [2][kNormMaxThreads / 32].
 template <int OUT>
 __device__ __forceinline__ void reduce_row(float& sum, float& A, float (*red)[kNormMaxThreads / 32]) {
   const int tpr = blockDim.x;
@@ -219,9 +220,15 @@ __device__ __forceinline__ uint4 pack8(const float (&h)[8]) {
 // of 16 bytes, all loads issued before the first is used, so x and r are read
 // once.  h is stored as soon as it is formed, y once the row's statistics are
 // known; every element is read and written by one thread, so an output may
-// take the place of x or r.  CLUSTER: a row is split over the CTAs of a
-// cluster, which exchange their sums through distributed shared memory.
-// Bound by HBM: 4 bytes read and 3 or 4 written per element.
+// take the place of x or r.  64 registers a thread leave 1024 threads and up
+// to 128 KB of loads in flight on an SM.  Bound by HBM, with a residual 4
+// bytes read and 3 or 4 written per element: 16384 x 8192 fp16 to int8 133 us
+// (104% of the copy bandwidth), 16384 x 4096 bf16 77 us (103%).
+// CLUSTER: a row of more than 8192 values is split over the CTAs of a
+// cluster, which exchange their sums through distributed shared memory: 4096 x
+// 28672 to int8 139 us (87%), 1024 x 21760 to E4M3 30 us (77%, two and a half
+// waves).  One CTA of the whole row took 147 and 35.5 us in registers (one CTA
+// an SM at 64 registers x 704 threads), 147 and 36 staged in shared memory.
 template <typename T, int OUT, int NV, bool CLUSTER>
 __global__ void __launch_bounds__(kNormThreads, 4)
     norm_held_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K, float eps,
@@ -296,12 +303,12 @@ __global__ void __launch_bounds__(kNormThreads, 4)
 // x and of r, copied to shared memory in 16-byte pieces whatever the rows' own
 // alignment (x and r start at 16-byte boundaries; what is left at the arrays'
 // end by element).  A CTA takes every gridDim.x-th block and copies the next
-// one while it works on this one, element by element, NV values of a row held by
-// each of its threads (16: 10782 x 6165 with a residual to E4M3 143 us against
-// 155 with 32, whose registers leave fewer warps; 16384 x 8191 16 bits without
-// one 158 against 148).  Bound by instruction issue.
-// A piece that two blocks' rows share is read by
-// both, each using its own values.
+// one while it works on this one, element by element, NV values of a row held
+// by each of its threads.  A piece that two blocks' rows share is read by
+// both, each using its own values.  Bound by instruction issue (78% of the
+// slots, about 37 a value), at 48-50% of the copy bandwidth: 10782 x 6165 bf16
+// with a residual to E4M3 143 us, 16384 x 8191 fp16 without one 158.  NV 32
+// made them 155 and 148: its registers leave fewer warps.
 template <typename T, int OUT, bool RES, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads ? 3 : 1)
     norm_ragged_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K,
@@ -491,6 +498,7 @@ cudaError_t launch_held(const NormArgs& a, int tpr, cudaStream_t s) {
 template <typename T, int OUT, int NV>
 cudaError_t launch_split(const NormArgs& a, int64_t n, cudaStream_t s) {
   const int C = static_cast<int>((n + NV * kNormThreads - 1) / (NV * kNormThreads));
+  if (a.M > 0x7fffffff / C) return cudaErrorInvalidValue;  // more CTAs than a grid has
   const int tpr = static_cast<int>((n + NV * C * 32 - 1) / (NV * C * 32)) * 32;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
