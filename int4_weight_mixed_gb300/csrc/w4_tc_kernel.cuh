@@ -885,7 +885,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint8_t* sst = sm.s + st_idx * NS * 256;
           const uint8_t* zst = sm.z + st_idx * NS * 256;
           const uint32_t tcol = tmem + lane_base + p.acol + (ts * NT + t) * NS * 32;
-          const bool row_ok = n0 + t * kTileN + r < N;
+          // (Rows past N hold whatever their slot held: a row of A meets its
+          // own row of D alone, and those are not stored.  Zeroing them was a
+          // select per register: 1-2% of every tensor-core schedule.)
           for (int qq = 0; qq < nv; ++qq) {
             if constexpr (F8) {
               // four 32-K chunks -> 32 columns of E4M3 bytes (no scales)
@@ -894,10 +896,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int c = 0; c < 4; ++c)
                 convert_chunk_f8(*reinterpret_cast<const uint4*>(wst + qq * WB + c * 2048 + r * 16),
                                  args.wbias, v + 8 * c);
-              if (!row_ok) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0;
-              }
               tmem_st32(tcol + qq * 32, v);
               continue;
             }
@@ -927,10 +925,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t (&v1)[16] = *reinterpret_cast<uint32_t(*)[16]>(&v[16]);
             convert_chunk<MODE>(w0, s2, nz2, args.zeros != nullptr, has_s, args.wbias, v0);
             convert_chunk<MODE>(w1, s2, nz2, args.zeros != nullptr, has_s, args.wbias, v1);
-            if (!row_ok) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0;
-            }
             tmem_st32(tcol + qq * 32, v);
           }
         }
