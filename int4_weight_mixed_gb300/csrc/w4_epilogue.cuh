@@ -88,6 +88,32 @@ __device__ __forceinline__ float ep_value(const EpArgs& args, int64_t m, int64_t
   }
 }
 
+// GELU, v * (1 + erf(v / sqrt 2)) / 2 = max(v, 0) - q with
+//   q = |v| erfc(|v| / sqrt 2) / 2 = |v| t P(t) e^(-v^2 / 2),
+//   t = 1 / (1 + |v| / (2 sqrt 2)),
+// so that the tail keeps its relative accuracy.  P is the minimax polynomial
+// of degree 8 (relative error 0.5 * 2^-24) of erfc(z) e^(z^2) / (2 t) over
+// z = |v| / sqrt 2 in [0, 14], found by linear programming on 5500 points;
+// the whole is within (2 v^2 + 12) 2^-24 of GELU.  (E4M3 1024 x 8192 x 21760
+// with bias 155 us; 162 with erfcf.)
+__device__ __forceinline__ float ep_gelu(float v) {
+  const float a = fabsf(v);
+  const float t = __fdividef(1.f, fmaf(0.35355339f, a, 1.f));
+  float p = -0.0301823653f;
+  p = fmaf(p, t, 0.145287484f);
+  p = fmaf(p, t, -0.249470085f);
+  p = fmaf(p, t, 0.145345181f);
+  p = fmaf(p, t, -0.0173700731f);
+  p = fmaf(p, t, 0.102930456f);
+  p = fmaf(p, t, 0.121185437f);
+  p = fmaf(p, t, 0.141233012f);
+  p = fmaf(p, t, 0.141040921f);
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(v * v * -0.72134752f));
+  const float q = a * t * p * e;
+  return fmaxf(v, 0.f) - (a >= 100.f ? 0.f : q);  // (infinities: q is 0; NaN stays)
+}
+
 // act(v).  The logistic and the tanh go through one exponential; each is
 // exact to a few units of fp32, far below the output's 11 or 8 bits.  (The
 // fast division gives 0 for a quotient by more than 2^126: SiLU and the tanh
@@ -96,7 +122,7 @@ __device__ __forceinline__ float ep_act(float v, int act) {
   switch (act) {
     case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
     case kActSilu: return __fdividef(v, 1.f + __expf(-v));
-    case kActGelu: return 0.5f * v * erfcf(v * -0.70710678f);  // exact in the tail too
+    case kActGelu: return ep_gelu(v);
     case kActGeluTanh: {  // (1 + tanh(u)) / 2 = 1 / (1 + e^-2u)
       const float u2 = 1.5957691f * fmaf(0.044715f * v * v, v, v);
       return __fdividef(v, 1.f + __expf(-u2));
