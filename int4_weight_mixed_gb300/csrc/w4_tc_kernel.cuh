@@ -942,7 +942,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       // drain the accumulator at the end of an exact chunk or of the unit
       // (every converter warp); false when a wait gave up
-      auto drain = [&](bool final_ev) -> bool {
+      auto drain = [&](auto last) -> bool {
+          bool final_ev;
+          if constexpr (std::is_same<decltype(last), bool>::value) final_ev = last;
+          else final_ev = decltype(last)::value;
           // ------------------------------------------------ drain an event
           const bool split = final_ev && u.nslots > 1;
           const size_t slot_elems = static_cast<size_t>(NT) * kTileN * BM;
@@ -1054,7 +1057,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               sides[kSideAhead - 1] = side_of(bb + kSideAhead * kConvGroups);
             }
             const uint32_t dcol = tmem + lane_base + t * BM + cc;
-            const int64_t nrow = n0 + t * kTileN + r;  // output column
+            [[maybe_unused]] const int64_t nrow = n0 + t * kTileN + r;  // output column
             const size_t goff = static_cast<size_t>(bb) * 1024 + q * 256 + lane * 4;
             const size_t coff = LEAN ? goff : static_cast<size_t>(t * BM + cc) * kTileN + r * 8;
             uint32_t d[8];
@@ -1147,6 +1150,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         return true;
       };
+      // with an epilogue of its own, the drains between a unit's exact chunks
+      // are code apart from the last one's
+      auto drain_at = [&](bool last) -> bool {
+        if constexpr (EP && MODE == kW4A8) {
+          if (!last) return drain(std::false_type{});
+          return drain(std::true_type{});
+        } else {
+          return drain(last);
+        }
+      };
       if constexpr (kOwnStages) {
         // Exact chunks (W4A8) or the whole unit, each ended by a drain;
         // within a chunk this group visits only its own stages (every
@@ -1192,7 +1205,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (!ok) break;
-          if (!drain(c1 == nkb)) {
+          if (!drain_at(c1 == nkb)) {
             ok = false;
             break;
           }
@@ -1224,7 +1237,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             pph ^= 1u;
           }
           if (--cleft != 0) continue;
-          if (!drain(j == nkb - 1)) {
+          if (!drain_at(j == nkb - 1)) {
             ok = false;
             break;
           }
