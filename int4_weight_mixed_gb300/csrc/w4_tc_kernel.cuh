@@ -1150,10 +1150,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         return true;
       };
-      // with an epilogue of its own, the drains between a unit's exact chunks
-      // are code apart from the last one's
+      // W4A8: the drains between a unit's exact chunks are code apart from the
+      // last one's (g128 1000 x 8192 x 21760 455 -> 436 us, with a residual
+      // 473 -> 425; per-channel M=1024 238 -> 232; the single-CTA kernels
+      // without an epilogue of their own were 1% slower with it)
       auto drain_at = [&](bool last) -> bool {
-        if constexpr (EP && MODE == kW4A8) {
+        if constexpr (MODE == kW4A8 && (EP || PAIR)) {
           if (!last) return drain(std::false_type{});
           return drain(std::true_type{});
         } else {
