@@ -206,6 +206,10 @@ typedef enum w4_act {
  * scales, zero-points, channel scales and bias; N is even.
  *   residual  array of out's type and shape, or NULL.  It may be out itself
  *             (the residual stream updated in place).
+ * The tensor-core schedules' epilogue wants out, residual, bias and
+ * ch_scales 16-byte aligned: without that the default rule runs the
+ * CUDA-core schedule in their place, and an explicit one returns
+ * UNSUPPORTED.
  * With act NONE, gated 0 and residual NULL this is exactly w4_gemm_bias.
  * The schedules and workspace are those of w4_gemm for the same M, N and K,
  * and a given schedule sums in the same order; beyond 16 rows the default

@@ -897,6 +897,13 @@ w4_status check_epilogue(const Epilogue& ep, int64_t M, int64_t N, const void* o
   return W4_OK;
 }
 
+// The tensor-core schedules' epilogue reads and writes 16 bytes at a time.
+bool epilogue_aligned(const Epilogue& ep, const void* out, const void* bias,
+                      const float* ch_scales) {
+  return !ep.any() ||
+         (aligned16(out) && aligned16(ep.residual) && aligned16(bias) && aligned16(ch_scales));
+}
+
 // prestaged: W4A8 on the tensor-core schedule with its bf16 activation copy
 // already in the workspace (the dynamic-quantization entry point writes it)
 w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
@@ -957,6 +964,13 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
       return fail(W4_ERR_UNSUPPORTED, "tensor-core schedules need 16-byte aligned inputs");
     si = 0;
   }
+  if (kSchedules[si].engine == kEngineTc && !epilogue_aligned(ep, out, bias, ch_scales)) {
+    if (forced)
+      return fail(W4_ERR_UNSUPPORTED,
+                  "the tensor-core schedules' epilogue needs 16-byte aligned out, residual, bias "
+                  "and channel scales");
+    si = 0;
+  }
   if (!workspace) return fail(W4_ERR_WORKSPACE, "workspace is null");
   if (!aligned16(workspace)) return fail(W4_ERR_WORKSPACE, "workspace is not 16-byte aligned");
   const size_t need = ws_needed(si, pr);
@@ -988,7 +1002,6 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
     ea.residual = ep.residual;
     ea.act = ep.act;
     ea.gated = ep.gated;
-    ea.vec = aligned16(out) && aligned16(ep.residual) && aligned16(bias) && aligned16(ch_scales);
     return launch(ea);
   };
 
@@ -1261,7 +1274,8 @@ w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const vo
   void* qdst = codes;
   int qout = act_type == W4_E4M3 ? 2 : 0;
   // the bf16 form is written from rows held in registers (16-byte loads)
-  const bool prestage = d.prestage && aligned16(a);
+  const bool prestage =
+      d.prestage && aligned16(a) && epilogue_aligned(ep, out, bias, ch_scales);
   if (prestage) {
     const TcPlan plan = make_plan(d.si, kW4A8, M, N, K, gs);
     qdst = ws + plan.ws_act;

@@ -281,8 +281,8 @@ __global__ void epilogue_rows_kernel(EpArgs args) {
        o += (int64_t)gridDim.x * blockDim.x) {
     const int64_t m = o / cols, j = o - m * cols, n = args.gated ? 2 * j : j;
     float r = ep_act(ep_value<MODE>(args, m, n, 0.f, 0), args.act);
-    if (args.gated) r *= ep_value<MODE>(args, m, n + 1, 0.f, 0);
-    ep_store<MODE>(args, o, r + ep_residual<MODE>(args, o));
+    if (args.gated) r = __fmul_rn(r, ep_value<MODE>(args, m, n + 1, 0.f, 0));
+    ep_store<MODE>(args, o, __fadd_rn(r, ep_residual<MODE>(args, o)));
   }
 }
 

@@ -995,17 +995,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          // An epilogue of its own: the residual too, which another grid may
-          // just have written
+          // An epilogue of its own: the residuals of this warp's next blocks,
+          // kSideAhead of them asked for ahead, the first ones now (another
+          // grid may just have written them)
           [[maybe_unused]] const bool writes = final_ev && !(split && !reducer);
-          if constexpr (EP) {
-            if (writes) {
-              ep_wait(args);
-              for (int bb = grp; bb < NT * nblk; bb += kConvGroups) {
-                const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
-                ep_prefetch8(args, m0 + cc, n0 + t * kTileN + q * 32);
-              }
+          constexpr int kSideAhead = 3;
+          [[maybe_unused]] uint4 sides[kSideAhead];
+          [[maybe_unused]] auto side_of = [&](int b) {
+            if constexpr (EP) {
+              const int t = LEAN ? 0 : b / nblk;
+              if (writes && b < NT * nblk)
+                return ep_side8<MODE>(args, m0 + (b - t * nblk) * 8, n0 + t * kTileN + q * 32);
             }
+            return make_uint4(0u, 0u, 0u, 0u);
+          };
+          if constexpr (EP) {
+            if (writes) ep_wait(args);
+#pragma unroll
+            for (int i = 0; i < kSideAhead; ++i) sides[i] = side_of(grp + i * kConvGroups);
           }
           if (!__all_sync(0xffffffffu, mbar_wait<true>(sm.dfull, ev & 1, abort, args.status))) {
             return false;
@@ -1031,22 +1038,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // further on, so that each 16-byte access of a warp covers 512
           // contiguous bytes; partial sums otherwise: row r of the block
           // holds its 8 columns contiguously at r * 8.
-          // the residuals of this warp's next blocks, kSideAhead of them asked
-          // for ahead
-          constexpr int kSideAhead = 3;
-          [[maybe_unused]] uint4 sides[kSideAhead];
-          [[maybe_unused]] auto side_of = [&](int b) {
-            if constexpr (EP) {
-              const int t = LEAN ? 0 : b / nblk;
-              if (writes && b < NT * nblk)
-                return ep_side8<MODE>(args, m0 + (b - t * nblk) * 8, n0 + t * kTileN + q * 32);
-            }
-            return make_uint4(0u, 0u, 0u, 0u);
-          };
-          if constexpr (EP) {
-#pragma unroll
-            for (int i = 0; i < kSideAhead; ++i) sides[i] = side_of(grp + i * kConvGroups);
-          }
           for (int bb = grp; bb < NT * nblk; bb += kConvGroups) {
             const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
             [[maybe_unused]] uint4 side;

@@ -324,6 +324,47 @@ def test_activations_far_out(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 24, 40, 300])
+@pytest.mark.parametrize("gated", [False, True])
+def test_arrays_off_a_16_byte_boundary(gpu_lib, M, gated):
+    """out, residual, bias and channel scales aligned to their elements only:
+    the same values by the default rule, a refusal by a tensor-core schedule."""
+    N, K = 256, 512
+    n = N // 2 if gated else N
+
+    def off(shape, dt, by=1):
+        flat = torch.empty(math.prod(shape) + 8, dtype=dt, device=DEV)
+        return flat[by:by + math.prod(shape)].view(shape)
+
+    for mode in ("bf16", "int8", "e4m3"):
+        c = Case(mode, M, N, K, seed=13)
+        a, b, kw = c.device()
+        bias, r = gen(c.g, N, dt=c.dt), gen(c.g, M, n, dt=c.dt)
+        ref, err = reference(c.prod, bias, "silu", gated, r)
+        names = ["out", "residual", "bias"] + (["channel_scales"] if mode != "bf16" else [])
+        for name in names:
+            k2 = dict(kw, bias=bias.to(DEV), residual=r.to(DEV), out=torch.empty(M, n, dtype=c.dt,
+                                                                                   device=DEV))
+            t = off(tuple(k2[name].shape), k2[name].dtype)
+            t.copy_(k2[name])
+            k2[name] = t
+            out = w4.gemm(a, b, c.wtype, N, act=w4.ACT_SILU, gated=gated, **k2)
+            check(out, ref, err, c.fmt(), (mode, name))
+            with pytest.raises(w4.W4Error) as e:
+                w4.gemm(a, b, c.wtype, N, act=w4.ACT_SILU, gated=gated, schedule=sched("tc64_sk"),
+                        **k2)
+            assert e.value.status == w4.ERR_UNSUPPORTED
+            if mode == "int8":
+                x = torch.randn(M, K, device=DEV).half()
+                k3 = {k: v for k, v in k2.items() if k not in ("token_scales", "group_size")}
+                k4 = dict(k3)
+                k4[name] = k4[name].clone() if name != "out" else torch.empty_like(t)
+                two = w4.gemm_dynamic(x, b, c.wtype, N, act=w4.ACT_SILU, gated=gated, **k4)
+                one = w4.gemm_dynamic(x, b, c.wtype, N, act=w4.ACT_SILU, gated=gated, **k3)
+                assert torch.equal(one, two)
+
+
+@pytest.mark.gpu
 def test_nan_and_infinite_activations_stay_in_their_rows(gpu_lib):
     c = Case("bf16", 20, 256, 1024, seed=8)
     a, b, kw = c.device()
