@@ -995,12 +995,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          // An epilogue of its own: the residuals of this warp's next blocks,
-          // kSideAhead of them asked for ahead, the first ones now (another
-          // grid may just have written them)
+          // An epilogue of its own: the residuals (another grid may just have
+          // written them).  CTA pairs ask for those of a warp's next three
+          // blocks ahead, the first ones now (E4M3 1024 x 8192 x 21760 162 us
+          // with one ahead, 154 with three); the other kernels, whose warps
+          // have two to four blocks and no registers to spare, when a block
+          // needs them (int8 M=64 54 us, 57 with three ahead).
           [[maybe_unused]] const bool writes = final_ev && !(split && !reducer);
-          constexpr int kSideAhead = 3;
-          [[maybe_unused]] uint4 sides[kSideAhead];
+          constexpr int kSideAhead = PAIR ? 3 : 0;
+          [[maybe_unused]] uint4 sides[kSideAhead + 1];
           [[maybe_unused]] auto side_of = [&](int b) {
             if constexpr (EP) {
               const int t = LEAN ? 0 : b / nblk;
@@ -1042,10 +1045,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int t = LEAN ? 0 : bb / nblk, cc = (bb - t * nblk) * 8;
             [[maybe_unused]] uint4 side;
             if constexpr (EP) {
+              sides[kSideAhead] = side_of(bb + kSideAhead * kConvGroups);
               side = sides[0];
 #pragma unroll
-              for (int i = 1; i < kSideAhead; ++i) sides[i - 1] = sides[i];
-              sides[kSideAhead - 1] = side_of(bb + kSideAhead * kConvGroups);
+              for (int i = 1; i <= kSideAhead; ++i) sides[i - 1] = sides[i];
             }
             const uint32_t dcol = tmem + lane_base + t * BM + cc;
             [[maybe_unused]] const int64_t nrow = n0 + t * kTileN + r;  // output column
