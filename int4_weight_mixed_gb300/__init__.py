@@ -291,15 +291,27 @@ def interleave_columns(gate: torch.Tensor, up: torch.Tensor, dim: int = -1) -> t
     return torch.stack((gate, up), dim=dim + 1).flatten(dim, dim + 1).contiguous()
 
 
-def _check_epilogue(M, N, gated, bias, residual, out, out_dtype):
-    """The types and sizes of what the epilogue reads and writes."""
-    cols = N // 2 if gated else N
-    if bias is not None and (bias.dtype != out_dtype or bias.numel() != N):
-        raise ValueError(f"bias must be [{N}] of {out_dtype}")
-    if out.dtype != out_dtype or out.numel() != M * cols:
-        raise ValueError(f"out must be [{M}, {cols}] of {out_dtype}")
-    if residual is not None and (residual.dtype != out_dtype or residual.numel() != M * cols):
-        raise ValueError(f"residual must be [{M}, {cols}] of {out_dtype}")
+def _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales, channel_scales,
+                    gated, bias, residual, out, out_dtype):
+    """The types and sizes of what a product with an epilogue reads and
+    writes (the library sees addresses alone)."""
+    def held(name, t, n, dtype):
+        if t is not None and (t.numel() != n or t.dtype is not dtype):
+            raise ValueError(f"{name} must hold {n} values of {dtype} (got {t.numel()} of "
+                             f"{t.dtype})")
+
+    n_out = M * (N // 2 if gated else N)
+    groups = 1 if group_size == -1 or K == 0 else K // group_size if group_size > 0 else 0
+    if M and b_packed.numel() * b_packed.element_size() < (N + 127) // 128 * 64 * K:
+        raise ValueError(f"b_packed is smaller than the prepacked {K} x {N} weight")
+    if scales is not None:
+        held("scales", scales, groups * N, scales.dtype)
+    held("zeros", zeros, groups * N, out_dtype)
+    held("token_scales", token_scales, M, torch.float32)
+    held("channel_scales", channel_scales, N, torch.float32)
+    held("bias", bias, N, out_dtype)
+    held("residual", residual, n_out, out_dtype)
+    held("out", out, n_out, out_dtype)
 
 
 def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
@@ -340,7 +352,8 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
         ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
     if act != ACT_NONE or gated or residual is not None:
-        _check_epilogue(M, N, gated, bias, residual, out, out_dtype)
+        _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales,
+                        channel_scales, gated, bias, residual, out, out_dtype)
         st = lib.w4_gemm_epilogue(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                                   scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                                   _ptr(channel_scales), _ptr(bias), act, int(gated),
@@ -387,7 +400,8 @@ def gemm_dynamic(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
         ws = workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, code, group_size)))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else S8
     if act != ACT_NONE or gated or residual is not None:
-        _check_epilogue(M, N, gated, bias, residual, out, torch.float16)
+        _check_epilogue(M, N, K, b_packed, scales, None, group_size, token_scales_out,
+                        channel_scales, gated, bias, residual, out, torch.float16)
         _check(lib.w4_gemm_dynamic_epilogue(
             _ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N, _ptr(scales), scale_code,
             group_size, _ptr(channel_scales), code, _ptr(bias), act, int(gated), _ptr(residual),

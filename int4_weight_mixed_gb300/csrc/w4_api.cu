@@ -527,9 +527,9 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
 // are fitted to timings of every schedule at 8200 shapes (fp16 / bf16 g128
 // and per-channel, int8 per-channel and g128, E4M3; M 1..4096, N 256..57344,
 // K 512..28672).  On 2700 other shapes, drawn over the logarithm of each size,
-// the pick is within 1.5-2.3% of the fastest schedule in the geometric mean of
-// each type (at most 1.53 times, on a product of 18 us), where the rule above
-// is 23-34% off, mostly on products of few tiles (M=200 N=992 K=4608 int8
+// the pick is within 1.6-2.3% of the fastest schedule in the geometric mean of
+// each type (at most 1.5 times, on products of 10-20 us), where the rule above
+// is 27-37% off, mostly on products of few tiles (M=200 N=992 K=4608 int8
 // g128: tc256p_sk 92 us, 18 contributors a tile; tc64_sk 23).
 enum CostClass { kCost16 = 0, kCostS8 = 1, kCostS8G = 2, kCostF8 = 3 };
 struct TcCost {
@@ -538,15 +538,15 @@ struct TcCost {
   double drain_row, staging;
 };
 constexpr TcCost kTcCost[4] = {
-    {2.29, {1.10, 1.12, 1.16, 0.69, 0.51, 0.57, 0.29}, 0.026, 0.0},
-    {2.21, {1.04, 1.04, 1.06, 0.63, 0.44, 0.59, 0.31}, 0.040, 7.1e-7},
-    {1.85, {1.61, 1.66, 1.80, 1.09, 0.86, 1.01, 0.66}, 0.026, 7.1e-7},
-    {1.56, {1.50, 1.55, 0.88, 0.91, 0.68, 0.74, 0.39}, 0.026, 0.0}};
-constexpr double kTcDrain = 3.1, kTcSlot = 0.52, kTcSlotRow = 0.0147;
+    {2.40, {1.06, 1.07, 1.10, 0.65, 0.49, 0.57, 0.30}, 0.025, 0.0},
+    {2.42, {1.01, 0.99, 1.01, 0.61, 0.42, 0.59, 0.30}, 0.036, 6.8e-7},
+    {2.25, {1.44, 1.45, 1.55, 0.94, 0.73, 0.91, 0.60}, 0.025, 6.8e-7},
+    {1.71, {1.44, 1.46, 0.81, 0.84, 0.66, 0.75, 0.38}, 0.025, 0.0}};
+constexpr double kTcDrain = 2.6, kTcSlot = 0.49, kTcSlotRow = 0.0148;
 // streamed at 32 rows: fixed, per 128-K block of the busiest CTA, per slot
-constexpr double kDs32Cost[3][3] = {{5.25, 0.643, 0.084}, {5.55, 0.571, 0.103}, {5.27, 0.805, 0.105}};
+constexpr double kDs32Cost[3][3] = {{5.26, 0.643, 0.084}, {5.56, 0.572, 0.104}, {5.29, 0.807, 0.104}};
 // clustered at 32 rows: fixed, per 128-K block of the busiest CTA
-constexpr double kGv32Cost[4][2] = {{3.85, 1.50}, {3.93, 1.33}, {3.77, 1.57}, {4.04, 1.10}};
+constexpr double kGv32Cost[4][2] = {{3.85, 1.52}, {3.91, 1.33}, {3.77, 1.57}, {4.03, 1.10}};
 
 double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
   const Schedule& sc = kSchedules[si];

@@ -537,6 +537,35 @@ def test_dynamic_epilogue_refusals(lib):
     assert call(residual=0x800001) == BAD
 
 
+def test_default_rule_fits_in_the_published_workspaces(lib):
+    """Whatever schedule the epilogue's own rule takes, its need is within
+    w4_gemm_workspace_size and w4_gemm_dynamic_workspace_size (read from the
+    WORKSPACE error of a workspace that is too small; host only)."""
+    import re
+    rng = np.random.default_rng(1)
+    need = lambda: int(re.search(r"(\d+) bytes", lib.w4_last_error().decode()).group(1))
+    for _ in range(400):
+        at = int(rng.choice([w4.F16, w4.BF16, w4.S8, w4.E4M3]))
+        M = int(np.exp(rng.uniform(0, np.log(5000))))
+        N = 2 * int(np.exp(rng.uniform(0, np.log(30000))))
+        K = 128 * int(rng.integers(1, 120))
+        gs = -1 if at == w4.E4M3 else int(rng.choice([g for g in (-1, 64, 128, 256) if K % g == 0]))
+        w8 = at in (w4.S8, w4.E4M3)
+        sg = 0x300000 if at == w4.S8 and gs not in (-1, K) else 0 if w8 else 0x300000
+        st = lib.w4_gemm_epilogue(
+            P, at, M, K, 0x200000, w4.INT4 if w8 else w4.UINT4B8, N, sg, at, 0, gs,
+            0x500000 if w8 else 0, 0x600000 if w8 else 0, 0, w4.ACT_SILU, 1, 0, 0x40000000,
+            w4.F16 if w8 else at, 0x400000, 16, None, -1)
+        assert st == w4.ERR_WORKSPACE, (M, N, K, at, gs, st, lib.w4_last_error())
+        assert need() <= lib.w4_gemm_workspace_size(M, N, K, at, gs), (M, N, K, at, gs)
+        if w8:
+            st = lib.w4_gemm_dynamic_epilogue(
+                P, w4.F16, M, K, 0x200000, w4.INT4, N, sg, w4.S8, gs, 0x600000, at, 0, w4.ACT_SILU,
+                1, 0, 0x40000000, 0, 0x400000, 16, None)
+            assert st == w4.ERR_WORKSPACE, (M, N, K, at, gs, st, lib.w4_last_error())
+            assert need() <= lib.w4_gemm_dynamic_workspace_size(M, N, K, at, gs), (M, N, K, at, gs)
+
+
 @pytest.mark.gpu
 def test_binding_refusals(gpu_lib):
     c = Case("bf16", 4, 64, 128)
@@ -548,9 +577,22 @@ def test_binding_refusals(gpu_lib):
                 dict(gated=True, out=torch.zeros(4, 64, **f)),
                 dict(act=w4.ACT_SILU, bias=torch.zeros(63, **f)),
                 dict(residual=torch.zeros(4, 64, dtype=torch.bfloat16)),
-                dict(residual=torch.zeros(4, 128, **f)[:, ::2])):
+                dict(residual=torch.zeros(4, 128, **f)[:, ::2]),
+                dict(act=w4.ACT_SILU, scales=kw["scales"][:, :32].contiguous()),
+                dict(act=w4.ACT_SILU, zeros=kw["scales"].float())):
         with pytest.raises(ValueError):
-            w4.gemm(a, b, c.wtype, c.N, **kw, **bad)
+            w4.gemm(a, b, c.wtype, c.N, **{**kw, **bad})
+    with pytest.raises(ValueError, match="b_packed"):
+        w4.gemm(a, b[:64], c.wtype, c.N, act=w4.ACT_SILU, **kw)
+    c8 = Case("int8", 4, 64, 128)
+    a8, b8, kw8 = c8.device()
+    for name in ("token_scales", "channel_scales"):
+        for t in (kw8[name][1:].clone(), kw8[name].half()):
+            with pytest.raises(ValueError, match=name):
+                w4.gemm(a8, b8, c8.wtype, c8.N, act=w4.ACT_SILU, **{**kw8, name: t})
+    with pytest.raises(ValueError, match="channel_scales"):
+        w4.gemm_dynamic(torch.zeros(4, 128, dtype=torch.float16, device=DEV), b8, c8.wtype, c8.N,
+                        channel_scales=kw8["channel_scales"][1:].clone(), act=w4.ACT_SILU)
     with pytest.raises(w4.W4Error):
         w4.gemm(a, b, c.wtype, c.N, act=9, **kw)
 
