@@ -516,7 +516,7 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
 // ---------------------------------------------------------------------------
 // The schedule of a product with an epilogue of its own, beyond 16 rows: the
 // one whose plan has the least estimated time.  (Up to 16 rows the rule above
-// is within 1% of the fastest.  The plain product keeps that rule at every
+// is within 1.0-1.7% of the fastest.  The plain product keeps that rule at every
 // size, and with it the order of its sums; an epilogue's schedules, sums and
 // plans are otherwise the plain product's.)
 //
@@ -527,8 +527,8 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
 // are fitted to timings of every schedule at 8200 shapes (fp16 / bf16 g128
 // and per-channel, int8 per-channel and g128, E4M3; M 1..4096, N 256..57344,
 // K 512..28672).  On 2700 other shapes, drawn over the logarithm of each size,
-// the pick is within 1.6-2.3% of the fastest schedule in the geometric mean of
-// each type (at most 1.5 times, on products of 10-20 us), where the rule above
+// the pick is within 1.6-2.2% of the fastest schedule in the geometric mean of
+// each type (at most 1.41 times, on products of 10-20 us), where the rule above
 // is 27-37% off, mostly on products of few tiles (M=200 N=992 K=4608 int8
 // g128: tc256p_sk 92 us, 18 contributors a tile; tc64_sk 23).
 enum CostClass { kCost16 = 0, kCostS8 = 1, kCostS8G = 2, kCostF8 = 3 };
@@ -543,10 +543,18 @@ constexpr TcCost kTcCost[4] = {
     {2.25, {1.44, 1.45, 1.55, 0.94, 0.73, 0.91, 0.60}, 0.025, 6.8e-7},
     {1.71, {1.44, 1.46, 0.81, 0.84, 0.66, 0.75, 0.38}, 0.025, 0.0}};
 constexpr double kTcDrain = 2.6, kTcSlot = 0.49, kTcSlotRow = 0.0148;
-// streamed at 32 rows: fixed, per 128-K block of the busiest CTA, per slot
-constexpr double kDs32Cost[3][3] = {{5.26, 0.643, 0.084}, {5.56, 0.572, 0.104}, {5.29, 0.807, 0.104}};
-// clustered at 32 rows: fixed, per 128-K block of the busiest CTA
-constexpr double kGv32Cost[4][2] = {{3.85, 1.52}, {3.91, 1.33}, {3.77, 1.57}, {4.03, 1.10}};
+// streamed at 32 rows: fixed, per 128-K block of the busiest CTA, per slot, and
+// per 128 columns for the reduction (without which M=32 N=8192 K=21760 int8 was
+// taken for 47.1 us against 46.9 on tc32_sk: 43 and 52 measured)
+constexpr double kDs32Cost[3][4] = {{4.80, 0.561, 0.150, 0.0317},
+                                    {5.05, 0.491, 0.173, 0.0326},
+                                    {4.84, 0.717, 0.172, 0.0323}};
+// clustered at 32 rows: fixed, per 128-K block of the busiest CTA, per CTA,
+// per block of the average SM
+constexpr double kGv32Cost[4][4] = {{3.58, 0.775, 0.0095, 0.565},
+                                    {3.71, 0.593, 0.0089, 0.567},
+                                    {3.55, 0.798, 0.0091, 0.586},
+                                    {4.03, 1.10, 0.0, 0.0}};
 
 double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
   const Schedule& sc = kSchedules[si];
@@ -554,14 +562,16 @@ double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t g
   if (sc.engine == kEngineGv) {
     const GvPlan p = make_gv_plan(si, mode, M, N, K);
     if (p.grid > sm_count() * gv_ctas_per_sm(p.nj)) return 1e30;  // more than one wave
-    return kGv32Cost[cls][0] + kGv32Cost[cls][1] * ((p.kblocks + p.cluster - 1) / p.cluster);
+    const int per = (p.kblocks + p.cluster - 1) / p.cluster;
+    const double* g = kGv32Cost[cls];
+    return g[0] + g[1] * per + g[2] * p.grid + g[3] * per * p.grid / sm_count();
   }
   if (sc.engine == kEngineDs) {
     const DsPlan p = make_ds_plan(si, mode, M, N, K);
     const int64_t T = static_cast<int64_t>(p.n_tiles) * p.kblocks, per = (T + p.grid - 1) / p.grid;
     const int64_t least = std::max<int64_t>(T / p.grid, 1);
-    return kDs32Cost[cls][0] + kDs32Cost[cls][1] * per +
-           kDs32Cost[cls][2] * ((p.kblocks + least - 1) / least);
+    const double* d = kDs32Cost[cls];
+    return d[0] + d[1] * per + d[2] * ((p.kblocks + least - 1) / least) + d[3] * p.n_tiles;
   }
   const TcPlan p = make_plan(si, mode, M, N, K, gs);
   const TcCost& c = kTcCost[cls];
