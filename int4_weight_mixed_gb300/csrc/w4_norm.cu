@@ -164,6 +164,37 @@ __device__ __forceinline__ void reduce_row(float& sum, float& A, float (*red)[kN
   }
 }
 
+// The same for the kernels that take any K, the warps' sums added by shuffles
+// (at most P warps a row, a power of two; a longer butterfly over zeros adds
+// the same numbers).
+template <int OUT, int P>
+__device__ __forceinline__ void reduce_any_row(float& sum, float& A,
+                                               float (*red)[kNormMaxThreads / 32]) {
+  const int tpr = blockDim.x;
+  auto add = [&](int o) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (OUT != kNorm16) A = max_nan(A, __shfl_xor_sync(0xffffffffu, A, o));
+  };
+  if (tpr < 32) {
+    for (int o = tpr / 2; o > 0; o >>= 1) add(o);
+    return;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) add(o);
+  if (tpr == 32) return;
+  const int nw = tpr / 32, w0 = threadIdx.y * nw, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    red[0][w0 + threadIdx.x / 32] = sum;
+    if (OUT != kNorm16) red[1][w0 + threadIdx.x / 32] = A;
+  }
+  __syncthreads();
+  const int i = lane & (P - 1);
+  sum = i < nw ? red[0][w0 + i] : 0.f;
+  if (OUT != kNorm16) A = i < nw ? red[1][w0 + i] : 0.f;
+#pragma unroll
+  for (int o = P / 2; o > 0; o >>= 1) add(o);
+}
+
 // The same over the CTAs of a row's cluster: every CTA writes its sums into
 // each CTA's array, and adds them in the order of the ranks.
 template <int OUT>
@@ -299,112 +330,192 @@ __global__ void __launch_bounds__(kNormThreads, 4)
   }
 }
 
-// Any K up to MAXT * NV.  A block of blockDim.y rows is a contiguous range of
-// x and of r, copied to shared memory in 16-byte pieces whatever the rows' own
-// alignment (x and r start at 16-byte boundaries; what is left at the arrays'
-// end by element).  A CTA takes every gridDim.x-th block and copies the next
-// one while it works on this one, element by element, NV values of a row held
-// by each of its threads.  A piece that two blocks' rows share is read by
-// both, each using its own values.  Bound by instruction issue (78% of the
-// slots, about 37 a value), at 48-50% of the copy bandwidth: 10782 x 6165 bf16
-// with a residual to E4M3 143 us, 16384 x 8191 fp16 without one 158.  NV 32
-// made them 155 and 148: its registers leave fewer warps.
+// 16 bytes from byte n (0..15) of two neighbouring 16-byte pieces.
+__device__ __forceinline__ uint4 bytes_from(const uint4& lo, const uint4& hi, uint32_t n) {
+  const bool two = n & 8, one = n & 4;
+  const uint32_t a0 = two ? lo.z : lo.x, a1 = two ? lo.w : lo.y, a2 = two ? hi.x : lo.z,
+                 a3 = two ? hi.y : lo.w, a4 = two ? hi.z : hi.x, a5 = two ? hi.w : hi.y;
+  const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? a4 : a3,
+                 b4 = one ? a5 : a4;
+  const uint32_t bits = (n & 3) * 8;
+  return make_uint4(__funnelshift_r(b0, b1, bits), __funnelshift_r(b1, b2, bits),
+                    __funnelshift_r(b2, b3, bits), __funnelshift_r(b3, b4, bits));
+}
+
+// `count` elements from shared memory (16-byte aligned) to any place of an
+// array, by the `n` threads of a row: whole 16-byte pieces of the array, and
+// what is left at the two ends by element.  Shared memory is read up to 16
+// bytes past the elements.  At most NV * n pieces.
+template <int NV, typename E>
+__device__ __forceinline__ void copy_out(const uint4* from, E* to, int count, int t, int n) {
+  constexpr int kPer = 16 / sizeof(E);
+  const int head =
+      min(static_cast<int>((0 - reinterpret_cast<uintptr_t>(to)) & 15) / static_cast<int>(sizeof(E)), count);
+  const int pieces = (count - head) / kPer, tail = head + pieces * kPer;
+  uint4* const to16 = reinterpret_cast<uint4*>(to + head);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int p = t + v * n;
+    if (p < pieces) to16[p] = bytes_from(from[p], from[p + 1], head * sizeof(E));
+  }
+  const E* const src = reinterpret_cast<const E*>(from);
+#pragma unroll 1
+  for (int e = t; e < head; e += n) to[e] = src[e];
+#pragma unroll 1
+  for (int e = tail + t; e < count; e += n) to[e] = src[e];
+}
+
+// Any K from 9 to MAXT * NV * 8.  A block of blockDim.y rows is a contiguous
+// range of x and of r, copied to shared memory in 16-byte pieces whatever the
+// rows' own alignment (x and r start at 16-byte boundaries; what is left at
+// the arrays' end by element).  A CTA takes every gridDim.x-th block and copies
+// the next one while it works on this one.  A thread holds NV vectors of eight
+// columns, each put together from the two pieces that it lies in; the outputs
+// go back through the stage their inputs came from, so that they too leave in
+// 16-byte pieces.  A piece that two blocks' rows share is read by both, each
+// using its own values, and written by element.
+// Bound by instruction issue (25 a value, two thirds of the slots) and by the
+// barriers between its steps: 10782 x 6165 bf16 with a residual to E4M3 116 us
+// (59% of the copy bandwidth), 16384 x 8191 fp16 without one 123 (64%), 16384 x
+// 1111 bf16 with one 33 (65%).  Element by element from the same stages it was
+// 37 instructions a value: 143, 160 and 41 us.  More than 16384 columns take 32
+// values a thread, some of them spilled: 4096 x 20001 fp16 to int8 161 us (52%).
 template <typename T, int OUT, bool RES, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads ? 3 : 1)
+__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads ? 4 : 1)
     norm_ragged_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K,
                        float eps, T* h_out, void* y, float* scales, uint32_t range) {
   extern __shared__ __align__(16) uint8_t raw[];  // [2][x range, r range]
   __shared__ float red[2][kNormMaxThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int R = blockDim.y, tpr = blockDim.x;
+  const int R = blockDim.y, tpr = blockDim.x, n = (K + 7) / 8;
   const int t = threadIdx.y * tpr + threadIdx.x, nt = tpr * R;
   const int64_t blocks = (M + R - 1) / R;
   const uint32_t stage = RES ? 2 * range : range;
   auto copy = [&](int64_t b, uint32_t at) {  // block b to the stage at byte `at`
-    const int64_t m0 = b * R, m1 = m0 + R < M ? m0 + R : M;
-    const int64_t g0 = m0 * K / 8, e1 = m1 * K;         // first piece, end of the range
-    const int64_t g1 = m1 == M ? e1 / 8 : (e1 + 7) / 8;  // end of the whole pieces
+    const int64_t e0 = b * R * K;  // the block's first element; its last row may be the array's
+    const bool last = (b + 1) * R >= M;
+    const int len = static_cast<int>(last ? M * K - e0 : static_cast<int64_t>(R) * K);
+    const int off = static_cast<int>(e0) & 7;
+    const int pieces = last ? (off + len) / 8 : (off + len + 7) / 8;
     const uint32_t sx = smem_addr(raw) + at;
-    const int pieces = static_cast<int>(g1 - g0);
-    const uint4* px = reinterpret_cast<const uint4*>(x) + g0;
-    const uint4* pr = reinterpret_cast<const uint4*>(r) + g0;
-    for (int g = t; g < pieces; g += nt) {
-      cp_async16(sx + g * 16, px + g);
-      if (RES) cp_async16(sx + range + g * 16, pr + g);
+    const T* const px = x + (e0 - off);
+    const T* const pr = RES ? r + (e0 - off) : nullptr;
+#pragma unroll
+    for (int v = 0; v <= NV; ++v) {  // up to R * n + 1 pieces
+      const int g = v < NV ? t + v * nt : NV * nt;
+      if (g < pieces && (v < NV || t == 0)) {
+        cp_async16(sx + g * 16, px + g * 8);
+        if (RES) cp_async16(sx + range + g * 16, pr + g * 8);
+      }
     }
-    T* const tx = reinterpret_cast<T*>(raw + at);
-    T* const tr = reinterpret_cast<T*>(raw + at + range);
-    for (int64_t e = g1 * 8 + t; e < e1; e += nt) {
-      tx[e - g0 * 8] = x[e];
-      if (RES) tr[e - g0 * 8] = r[e];
+    if (last) {
+      T* const tx = reinterpret_cast<T*>(raw + at);
+      T* const tr = reinterpret_cast<T*>(raw + at + range);
+#pragma unroll 1
+      for (int e = pieces * 8 + t; e < off + len; e += nt) {
+        tx[e] = px[e];
+        if (RES) tr[e] = pr[e];
+      }
     }
   };
   uint32_t at = 0;
   if (blockIdx.x < blocks) copy(blockIdx.x, 0);
   cp_async_commit();
-  T wv[NV];  // a thread has the same columns in every row
+  // This thread's vectors of a row: threadIdx.x + v * tpr.  Only its last one
+  // can lie past the row's end (the host gives a row enough vectors for
+  // that); it takes the row's last vector instead, with the columns masked.
+  const int i_last = threadIdx.x + (NV - 1) * tpr;
+  const int left = K - i_last * 8;  // columns from there on
+  uint32_t mask[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    mask[j] = left >= 2 * j + 2 ? 0xffffffffu : left == 2 * j + 1 ? 0xffffu : 0u;
+  auto vec = [&](int v) { return v < NV - 1 ? static_cast<int>(threadIdx.x) + v * tpr : min(i_last, n - 1); };
+  uint4 wv[NV];  // a thread has the same columns in every row
+  const bool w16 = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int k = threadIdx.x + v * tpr;
-    wv[v] = w && k < K ? w[k] : ep_round<T>(1.f);
+    const int k = vec(v) * 8;
+    if (w && w16 && k + 8 <= K) {
+      wv[v] = __ldg(reinterpret_cast<const uint4*>(w + k));
+    } else {
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = w && k + e < K ? ep_f32(w[k + e]) : 1.f;
+      wv[v] = pack8<T>(u);
+    }
   }
+  const float inv_k = __frcp_rn(static_cast<float>(K));
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, at ^= stage) {
+    cp_async_wait<0>();
+    __syncthreads();  // everyone's copies of this block; the other stage has been read
     if (b + gridDim.x < blocks) copy(b + gridDim.x, at ^ stage);
     cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();  // everyone's copies of this block
     const int64_t m = b * R + threadIdx.y;
-    const bool live = m < M;
-    const int len = live ? K : 0;
-    // (rows beyond the last read this block's first one and store nothing)
-    const int shift = static_cast<int>((live ? m : b * R) * K - b * R * K / 8 * 8) + threadIdx.x;
-    const T* const xr = reinterpret_cast<const T*>(raw + at) + shift;
-    const T* const rr = reinterpret_cast<const T*>(raw + at + range) + shift;
-    T* const hr = RES && h_out ? h_out + m * K + threadIdx.x : nullptr;
-    float u[NV];
+    const bool live = m < M;  // other rows take the block's first one and store nothing
+    const int64_t e0 = b * R * K;
+    const int first = (static_cast<int>(e0) & 7) + (live ? static_cast<int>(threadIdx.y) * K : 0);
+    uint4* const xs = reinterpret_cast<uint4*>(raw + at);
+    uint4* const rs = reinterpret_cast<uint4*>(raw + at + range);
+    const uint32_t off = (first & 7) * 2;
+    float hw[NV * 8];
+    uint4 hp[NV];
     float sum = 0.f, A = 0.f;
-    // without branches: what lies past the row (its threads' last values, in
-    // shared memory all the same) counts as zero
-    auto take = [&](int v, T* h_to) {
-      const bool in = static_cast<int>(threadIdx.x) + v * tpr < len;
-      float h = ep_f32(xr[v * tpr]);
-      if (RES) h = __fadd_rn(h, ep_f32(rr[v * tpr]));
-      h = in ? h : 0.f;
-      if (RES && h_to && in) h_to[v * tpr] = ep_round<T>(h);
-      sum = fmaf(h, h, sum);
-      u[v] = __fmul_rn(h, ep_f32(wv[v]));
-      if (OUT != kNorm16) A = max_nan(A, fabsf(u[v]));
-    };
-    if (hr) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) take(v, hr);
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) take(v, nullptr);
-    }
-    reduce_row<OUT>(sum, A, red);
-    const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(K)) + eps);
-    float by = rstd;
-    if (OUT != kNorm16) {
-      const RowCode c = row_code<OUT>(sum, A, rstd);
-      if (live && threadIdx.x == 0) scales[m] = c.scale;
-      by = c.inv;
-      if (!plain_codes(c)) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) u[v] = fit_code(u[v], c);
-      }
-    }
-    T* const y16 = static_cast<T*>(y) + (OUT == kNorm16 ? m * K + threadIdx.x : 0);
-    uint8_t* const y8 = static_cast<uint8_t*>(y) + m * K + threadIdx.x;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (static_cast<int>(threadIdx.x) + v * tpr < len) {
-        if constexpr (OUT == kNorm16) y16[v * tpr] = ep_round<T>(__fmul_rn(u[v], by));
-        else y8[v * tpr] = static_cast<uint8_t>(code_of<OUT>(u[v], by));
+      const int p = (first >> 3) + vec(v);
+      auto piece = [&](const uint4* from) {
+        uint4 q = bytes_from(from[p], from[p + 1], off);
+        if (v == NV - 1) {
+          q.x &= mask[0];
+          q.y &= mask[1];
+          q.z &= mask[2];
+          q.w &= mask[3];
+        }
+        return q;
+      };
+      float h[8], u[8];
+      const uint4 xv = piece(xs);
+      add8<T>(xv, RES ? piece(rs) : xv, RES, h);
+      unpack<T>(wv[v], u);
+      if (RES) hp[v] = pack8<T>(h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(h[e], h[e], sum);
+        hw[v * 8 + e] = __fmul_rn(h[e], u[e]);
+        if (OUT != kNorm16) A = max_nan(A, fabsf(hw[v * 8 + e]));
       }
     }
-    __syncthreads();  // before the stage and the sums are written again
+    reduce_any_row<OUT, MAXT / 32>(sum, A, red);
+    if (tpr <= 32) __syncthreads();  // the stage has been read, as after a longer row's sums
+    const float rstd = rsqrtf(fmaf(sum, inv_k, eps));
+    RowCode c{};
+    if (OUT != kNorm16) {
+      c = row_code<OUT>(sum, A, rstd);
+      if (live && threadIdx.x == 0) scales[m] = c.scale;
+      if (!plain_codes(c)) {
+#pragma unroll
+        for (int e = 0; e < NV * 8; ++e) hw[e] = fit_code(hw[e], c);
+      }
+    }
+    uint4* const ys = xs + threadIdx.y * n;
+    uint4* const hs = rs + threadIdx.y * n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (v == NV - 1 && left <= 0) continue;
+      store8<T, OUT>(hw + v * 8, rstd, c.inv, ys, 0, vec(v));
+      if (RES && h_out) hs[vec(v)] = hp[v];
+    }
+    __syncthreads();
+    if (live) {
+      const int64_t row = e0 + static_cast<int64_t>(threadIdx.y) * K;
+      if constexpr (OUT == kNorm16)
+        copy_out<NV>(ys, static_cast<T*>(y) + row, K, threadIdx.x, tpr);
+      else
+        copy_out<(NV + 1) / 2>(ys, static_cast<uint8_t*>(y) + row, K, threadIdx.x, tpr);
+      if (RES && h_out) copy_out<NV>(hs, h_out + row, K, threadIdx.x, tpr);
+    }
   }
 }
 
@@ -431,23 +542,24 @@ __global__ void __launch_bounds__(kNormMaxThreads)
   auto hw_at = [&](uint32_t k, float h) { return w ? __fmul_rn(h, ep_f32(w[k])) : h; };
   float sum = 0.f, A = 0.f;
   if (live) {
-#pragma unroll 4
-    for (uint32_t k = threadIdx.x; k < K; k += tpr) {
-      const float h = h_at(k);
-      sum = fmaf(h, h, sum);
-      if (OUT != kNorm16) A = max_nan(A, fabsf(hw_at(k, h)));
+    for (uint32_t k = threadIdx.x * 8; k < K; k += tpr * 8) {
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        const float h = k + e < K ? h_at(k + e) : 0.f;
+        sum = fmaf(h, h, sum);
+        if (OUT != kNorm16 && k + e < K) A = max_nan(A, fabsf(hw_at(k + e, h)));
+      }
     }
   }
-  reduce_row<OUT>(sum, A, red);
+  reduce_any_row<OUT, kNormMaxThreads / 32>(sum, A, red);
   if (!live) return;
-  const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(K)) + eps);
+  const float rstd = rsqrtf(fmaf(sum, __frcp_rn(static_cast<float>(K)), eps));
   RowCode c{};
   if (OUT != kNorm16) {
     c = row_code<OUT>(sum, A, rstd);
     if (threadIdx.x == 0) scales[m] = c.scale;
   }
-#pragma unroll 2
-  for (uint32_t k = threadIdx.x; k < K; k += tpr) {
+  auto put = [&](uint32_t k) {
     const float h = h_at(k), hw = hw_at(k, h);
     if (h_out) h_out[m * K + k] = ep_round<T>(h);
     if constexpr (OUT == kNorm16)
@@ -455,7 +567,9 @@ __global__ void __launch_bounds__(kNormMaxThreads)
     else
       static_cast<uint8_t*>(y)[m * K + k] =
           static_cast<uint8_t>(code_of<OUT>(fit_code(hw, c), c.inv));
-  }
+  };
+#pragma unroll 2
+  for (uint32_t k = threadIdx.x; k < K; k += tpr) put(k);
 }
 
 cudaLaunchConfig_t norm_config(dim3 grid, dim3 block, cudaLaunchAttribute* attr, cudaStream_t s) {
@@ -523,18 +637,18 @@ cudaError_t allow_smem(Fn* fn, size_t bytes) {
 }
 
 // Shared memory of a CTA of the ragged kernel: two stages of x and r, each
-// from one 16-byte boundary to another, and what a row's threads read past
-// its end.
+// from one 16-byte boundary to another or the rows' outputs, each row's from a
+// boundary on, with a piece beyond.
 size_t ragged_range(const NormArgs& a, int rows) {
-  return (static_cast<size_t>(rows) * a.K * 2 + 31) / 16 * 16;
+  return (static_cast<size_t>(rows) * ((a.K + 7) / 8) + 2) * 16;
 }
-size_t ragged_bytes(const NormArgs& a, int tpr, int rows, int nv) {
-  return ragged_range(a, rows) * (a.residual ? 4 : 2) + static_cast<size_t>(nv * tpr - a.K) * 2;
+size_t ragged_bytes(const NormArgs& a, int rows) {
+  return ragged_range(a, rows) * (a.residual ? 4 : 2);
 }
 
 template <typename T, int OUT, int NV, int MAXT>
 cudaError_t launch_ragged(const NormArgs& a, int tpr, int rows, cudaStream_t s) {
-  const size_t bytes = ragged_bytes(a, tpr, rows, NV);
+  const size_t bytes = ragged_bytes(a, rows);
   auto* fn = a.residual ? &norm_ragged_kernel<T, OUT, true, NV, MAXT>
                         : &norm_ragged_kernel<T, OUT, false, NV, MAXT>;
   cudaError_t e = allow_smem(fn, bytes);
@@ -569,14 +683,15 @@ cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s) {
     if (n <= 1024) return launch_held<T, OUT, 4>(a, row_threads(n, 4), s);
     if (n <= 4 * kNormThreads * kNormMaxCluster) return launch_split<T, OUT, 4>(a, n, s);
   }
-  // values of a row a thread: by K alone, as the order of a row's sum
-  const int nv = a.K <= 16 * kNormMaxThreads ? 16 : 32;
-  const int tpr = row_threads(a.K, nv), rows = cta_rows(tpr);
-  if (in16 && a.K <= nv * kNormMaxThreads && ragged_bytes(a, tpr, rows, nv) <= kNormMaxSmem) {
+  // vectors of a row a thread: by K alone, as the order of a row's sum
+  const int64_t all = (a.K + 7) / 8;
+  const int nv = all <= 2 * kNormMaxThreads ? 2 : 4;
+  const int tpr = row_threads(all, nv), rows = cta_rows(tpr);
+  if (in16 && a.K > 8 && all <= nv * kNormMaxThreads && ragged_bytes(a, rows) <= kNormMaxSmem) {
     constexpr int kLow = kNormThreads, kHigh = kNormMaxThreads;
-    if (nv == 32) return launch_ragged<T, OUT, 32, kHigh>(a, tpr, rows, s);
-    return tpr <= kLow ? launch_ragged<T, OUT, 16, kLow>(a, tpr, rows, s)
-                       : launch_ragged<T, OUT, 16, kHigh>(a, tpr, rows, s);
+    if (nv == 4) return launch_ragged<T, OUT, 4, kHigh>(a, tpr, rows, s);
+    return tpr <= kLow ? launch_ragged<T, OUT, 2, kLow>(a, tpr, rows, s)
+                       : launch_ragged<T, OUT, 2, kHigh>(a, tpr, rows, s);
   }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
