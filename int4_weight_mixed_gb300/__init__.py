@@ -295,23 +295,30 @@ def _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales, 
                     gated, bias, residual, out, out_dtype):
     """The types and sizes of what a product with an epilogue reads and
     writes (the library sees addresses alone)."""
-    def held(name, t, n, dtype):
-        if t is not None and (t.numel() != n or t.dtype is not dtype):
-            raise ValueError(f"{name} must hold {n} values of {dtype} (got {t.numel()} of "
-                             f"{t.dtype})")
-
     n_out = M * (N // 2 if gated else N)
-    groups = 1 if group_size == -1 or K == 0 else K // group_size if group_size > 0 else 0
+    n_groups = N * (1 if group_size == -1 or K == 0 else K // group_size if group_size > 0 else 0)
+    f32 = torch.float32
     if M and b_packed.numel() * b_packed.element_size() < (N + 127) // 128 * 64 * K:
         raise ValueError(f"b_packed is smaller than the prepacked {K} x {N} weight")
-    if scales is not None:
-        held("scales", scales, groups * N, scales.dtype)
-    held("zeros", zeros, groups * N, out_dtype)
-    held("token_scales", token_scales, M, torch.float32)
-    held("channel_scales", channel_scales, N, torch.float32)
-    held("bias", bias, N, out_dtype)
-    held("residual", residual, n_out, out_dtype)
-    held("out", out, n_out, out_dtype)
+    if scales is not None and scales.numel() != n_groups:
+        _not_held("scales", scales, n_groups, scales.dtype)
+    if zeros is not None and (zeros.numel() != n_groups or zeros.dtype is not out_dtype):
+        _not_held("zeros", zeros, n_groups, out_dtype)
+    if token_scales is not None and (token_scales.numel() != M or token_scales.dtype is not f32):
+        _not_held("token_scales", token_scales, M, f32)
+    if channel_scales is not None and (channel_scales.numel() != N or
+                                       channel_scales.dtype is not f32):
+        _not_held("channel_scales", channel_scales, N, f32)
+    if bias is not None and (bias.numel() != N or bias.dtype is not out_dtype):
+        _not_held("bias", bias, N, out_dtype)
+    if residual is not None and (residual.numel() != n_out or residual.dtype is not out_dtype):
+        _not_held("residual", residual, n_out, out_dtype)
+    if out.numel() != n_out or out.dtype is not out_dtype:
+        _not_held("out", out, n_out, out_dtype)
+
+
+def _not_held(name, t, n, dtype):
+    raise ValueError(f"{name} must hold {n} values of {dtype} (got {t.numel()} of {t.dtype})")
 
 
 def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
@@ -348,19 +355,29 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
         out_dtype = torch.float16 if a.dtype in (torch.int8, torch.float8_e4m3fn) else a.dtype
     if out is None:
         out = torch.empty((M, N // 2 if gated else N), dtype=out_dtype, device=dev)
-    if ws is None:  # (a given workspace is checked against the plan by the library)
-        ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
     if act != ACT_NONE or gated or residual is not None:
         _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales,
                         channel_scales, gated, bias, residual, out, out_dtype)
-        st = lib.w4_gemm_epilogue(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
-                                  scale_code, _ptr(zeros), group_size, _ptr(token_scales),
-                                  _ptr(channel_scales), _ptr(bias), act, int(gated),
-                                  _ptr(residual), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
-                                  ws.numel(), _stream(dev), schedule)
-        _check(st, "w4_gemm_epilogue")
-    elif bias is None:
+        args = (a.data_ptr(), a_code, M, K, b_packed.data_ptr(), wtype, N, _ptr(scales),
+                scale_code, _ptr(zeros), group_size, _ptr(token_scales), _ptr(channel_scales),
+                _ptr(bias), act, int(gated), _ptr(residual), out.data_ptr(),
+                _DTYPE_CODE[out_dtype])
+        # The library checks the workspace against its plan before it launches
+        # anything: the stream's cached one is tried as it is, and its size
+        # asked for when it is too small (1 us less a call on the host).
+        given = ws if ws is not None else workspace(dev, 0)
+        st = lib.w4_gemm_epilogue(*args, given.data_ptr(), given.numel(), _stream(dev), schedule)
+        if st == ERR_WORKSPACE and ws is None:
+            given = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
+            st = lib.w4_gemm_epilogue(*args, given.data_ptr(), given.numel(), _stream(dev),
+                                      schedule)
+        if st:
+            _check(st, "w4_gemm_epilogue")
+        return out
+    if ws is None:  # (a given workspace is checked against the plan by the library)
+        ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
+    if bias is None:
         st = lib.w4_gemm_ex(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                             scale_code, _ptr(zeros), group_size, _ptr(token_scales),
                             _ptr(channel_scales), _ptr(out), _DTYPE_CODE[out_dtype], _ptr(ws),
