@@ -678,7 +678,8 @@ cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s) {
   const int64_t n = a.K / 8;
   if (a.K % 8 == 0 && in16 && at(a.weight, 16) && at(a.h_out, 16) &&
       at(a.y, OUT == kNorm16 ? 16 : 8)) {
-    if (n <= 32) return launch_held<T, OUT, 1>(a, row_threads(n, 1), s);
+    // two vectors a thread (65536 x 256 fp16 to int8 with a residual 25.5 us with
+    // one, 19.4 with two, 18.7 with four; one row 1.26, 1.37 and 1.66)
     if (n <= 512) return launch_held<T, OUT, 2>(a, row_threads(n, 2), s);
     if (n <= 1024) return launch_held<T, OUT, 4>(a, row_threads(n, 4), s);
     if (n <= 4 * kNormThreads * kNormMaxCluster) return launch_split<T, OUT, 4>(a, n, s);
