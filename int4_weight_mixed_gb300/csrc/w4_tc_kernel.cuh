@@ -308,6 +308,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int CPB = BK / kChunkK;  // 32-K chunks per block
   constexpr int NCTA = PAIR ? 2 : 1;
   constexpr bool EP = std::is_same<Args, EpArgs>::value;  // an epilogue of its own
+  // Split tiles of a product with an epilogue are left to tc_reduce_kernel:
+  // always (one CTA a tile), or where the launch says so (CTA pairs).
+  constexpr bool kReduceAfter = EP && !PAIR;
+  bool reduce_after = kReduceAfter;
+  if constexpr (EP && PAIR) reduce_after = args.reduce != 0;
   if constexpr (PAIR) {
     // launched without its two-CTA clusters: nothing may run
     if (cluster_size() != 2) {
@@ -401,6 +406,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool stage_in_group = sub_per_group >= NS;
   const int grow_shift = sub_per_group >= 2 ? 1 : 0;
   const int esz = MODE == kW4A8 ? 1 : 2;
+
+  if constexpr (EP) {
+    // tc_reduce_kernel may launch, and waits for this grid
+    if (args.reduce) asm volatile("griddepcontrol.launch_dependents;");
+  }
 
   if (warp >= kConvWarps) {
   // W4A16 with one MMA issuer: the fifth warpgroup (producers, MMA) gives
@@ -955,13 +965,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // The last to arrive adds the others' partial sums to its own
           // accumulator; the others write theirs and then count themselves as
           // written (high half), which the last one waits for.
+          // (reduce_after: every contributor writes, tc_reduce_kernel adds.)
           int* ctr = args.counters + (static_cast<size_t>(u.tile) * NCTA + rank) * kConvWarps + cw;
           bool reducer = false;
-          if (split) {
-            int prev_count = 0;
-            if (lane == 0) prev_count = atomicAdd(ctr, 1);
-            prev_count = __shfl_sync(0xffffffffu, prev_count, 0);
-            reducer = (prev_count & 0xffff) == u.nslots - 1;
+          if constexpr (!kReduceAfter) {
+            if (split && !reduce_after) {
+              int prev_count = 0;
+              if (lane == 0) prev_count = atomicAdd(ctr, 1);
+              prev_count = __shfl_sync(0xffffffffu, prev_count, 0);
+              reducer = (prev_count & 0xffff) == u.nslots - 1;
+            }
           }
           // position of this unit among the tile's contributors (K order), and
           // the slot of contributor sl held by lane sl (<= 32 contributors)
@@ -1134,13 +1147,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             else mbar_arrive(sm.dempty);
           }
           first_chunk = false;
-          if (split && !reducer) {
-            // partial sums visible device-wide, then counted as written
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) atomicAdd(ctr, 0x10000);
-          } else if (reducer) {
-            if (lane == 0) *ctr = 0;  // leave the counter at zero for the next call
+          if constexpr (!kReduceAfter) {
+            if (split && !reducer && !reduce_after) {
+              // partial sums visible device-wide, then counted as written
+              __threadfence();
+              __syncwarp();
+              if (lane == 0) atomicAdd(ctr, 0x10000);
+            } else if (reducer) {
+              if (lane == 0) *ctr = 0;  // leave the counter at zero for the next call
+            }
           }
         return true;
       };
