@@ -15,14 +15,15 @@ constexpr int kRedAhead = 8;  // slots whose loads are in flight together
 
 // Split tiles: the sum of their contributors' partial sums, in K order (the
 // plain product's), and the epilogue.  A warp has a block of eight rows by 32
-// columns, laid out as the main kernel's drain leaves it.  The plain product's
+// columns, laid out as the main kernel's drain leaves it (CTA pairs: the LEAN
+// one's).  The plain product's
 // kernels let the last contributor of a tile add the others', slot by slot;
 // here the whole GPU does, eight slots in flight a warp, and the main kernel is
 // rid of that code, whose registers its main loop spilled (M=64 4096 x 14336
 // bf16 g128 with a residual 31.4 -> 25.2 us, M=100 1024 x 8192 int8 on 128-row
 // tiles 52 -> 17, M=64 28672 x 4096 48.0 -> 45.9).  Bound by latency: a launch
 // and one or two rounds of loads from L2.
-template <int MODE, bool PAIR, bool LEAN>
+template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(32 * kRedWarps)
     tc_reduce_kernel(const TcPlan p, const EpArgs args) {
   constexpr int NCTA = PAIR ? 2 : 1;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(32 * kRedWarps)
       ((static_cast<int64_t>(nt) * NCTA + rank) * p.nt + t) * kTileN + q * 32;
   if (m0 >= args.M || n0 >= args.N) return;
   const size_t slot_elems = static_cast<size_t>(p.nt) * kTileN * p.bm;
-  const size_t off = LEAN ? static_cast<size_t>(b) * 1024 + q * 256 + lane * 4
+  const size_t off = PAIR ? static_cast<size_t>(b) * 1024 + q * 256 + lane * 4
                           : static_cast<size_t>(t * p.bm + cc) * kTileN + (q * 32 + lane) * 8;
   // lane l: the slot of contributor s0 + l of the 32 from s0 on
   auto slot_of = [&](int sl) {
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(32 * kRedWarps)
       const size_t at = static_cast<size_t>(__shfl_sync(
           0xffffffffu, static_cast<unsigned long long>(held), (s0 + j) & 31));
       if (s0 + j < u.nslots) {
-        if (LEAN) ld_cg_halves(part + at, 128, x[j]);
+        if (PAIR) ld_cg_halves(part + at, 128, x[j]);
         else ld_cg_v8(part + at, x[j]);
       }
     }
@@ -106,13 +107,8 @@ cudaError_t launch_reduce(const TcPlan& plan, const EpArgs& args, cudaStream_t s
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (!plan.pair) return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, false, false>, plan, args);
-  // the pair kernels' layout of the partial sums (see launch_tc_t)
-  if constexpr (MODE == kW4A8) {
-    if (!tc_grouped(plan))
-      return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, true, false>, plan, args);
-  }
-  return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, true, true>, plan, args);
+  if (!plan.pair) return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, false>, plan, args);
+  return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, true>, plan, args);
 }
 
 // Whether tc_reduce_kernel adds the split tiles of a plan.  CTA pairs: where a

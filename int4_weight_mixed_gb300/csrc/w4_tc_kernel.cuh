@@ -1307,6 +1307,11 @@ cudaError_t launch_tc_mode(const TcPlan& plan, const CUtensorMap& amap, const CU
   return cudaLaunchKernelEx(&cfg, fn, amap, smap, zmap, plan, args);
 }
 
+// W4A8 on CTA pairs: LEAN with group scales, and where every tile is split and
+// left to tc_reduce_kernel
+inline bool tc_pair_lean(const TcPlan& p, const TcArgs&) { return tc_grouped(p); }
+inline bool tc_pair_lean(const TcPlan& p, const EpArgs& a) { return tc_grouped(p) || a.reduce; }
+
 // fp8 activations are read by TMA straight from the caller's buffer; W4A8
 // int8 from the workspace's bf16 copy; W4A16 from the caller's buffer.
 template <bool MMA2, bool PAIR, class Args>
@@ -1320,7 +1325,7 @@ cudaError_t launch_tc_t(const TcPlan& plan, const CUtensorMap& amap, const CUten
       return launch_tc_mode<kW4A16_BF16, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
     case kW4A8F8: return launch_tc_mode<kW4A8F8, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
     default:
-      if (PAIR && tc_grouped(plan))
+      if (PAIR && tc_pair_lean(plan, args))
         return launch_tc_mode<kW4A8, MMA2, PAIR, PAIR, Args>(plan, amap, smap, zmap, args, s);
       return launch_tc_mode<kW4A8, MMA2, PAIR, false, Args>(plan, amap, smap, zmap, args, s);
   }
