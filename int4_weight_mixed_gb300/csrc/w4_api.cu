@@ -521,16 +521,17 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
 // plans are otherwise the plain product's.)
 //
 // A tensor-core plan takes a fixed time, one time per pipeline stage of its
-// busiest CTA, one per tile that CTA drains (more with taller tiles) and one
-// per partial-sum slot that the last contributor of a split tile adds; W4A8
-// also the pass that stages its activations.  The constants (microseconds)
-// are fitted to timings of every schedule at 8200 shapes (fp16 / bf16 g128
-// and per-channel, int8 per-channel and g128, E4M3; M 1..4096, N 256..57344,
-// K 512..28672).  On 2700 other shapes, drawn over the logarithm of each size,
-// the pick is within 1.6-2.2% of the fastest schedule in the geometric mean of
-// each type (at most 1.41 times, on products of 10-20 us), where the rule above
-// is 27-37% off, mostly on products of few tiles (M=200 N=992 K=4608 int8
-// g128: tc256p_sk 92 us, 18 contributors a tile; tc64_sk 23).
+// busiest CTA, one per tile that CTA drains, and what its split tiles cost:
+// where their last contributor adds the others' partial sums, a time per slot
+// (and drains that take longer with taller tiles); where tc_reduce_kernel adds
+// them, its launch, a time per slot and one per megabyte of partial sums.
+// W4A8 also takes the pass that stages its activations.  The constants
+// (microseconds) are fitted to timings of every schedule at 7000 shapes (bf16
+// g128 and per-channel, int8 per-channel and g128, E4M3; M 17..4096, N
+// 256..57344, K 512..28672).  On 1750 other shapes of more than 16 rows, drawn
+// over the logarithm of each size, the pick is within 2.1-2.6% of the fastest
+// schedule in the geometric mean of each type (at most 1.41 times), where the
+// rule above is 13-23% off.
 enum CostClass { kCost16 = 0, kCostS8 = 1, kCostS8G = 2, kCostF8 = 3 };
 struct TcCost {
   double fixed;
@@ -538,11 +539,12 @@ struct TcCost {
   double drain_row, staging;
 };
 constexpr TcCost kTcCost[4] = {
-    {2.40, {1.06, 1.07, 1.10, 0.65, 0.49, 0.57, 0.30}, 0.025, 0.0},
-    {2.42, {1.01, 0.99, 1.01, 0.61, 0.42, 0.59, 0.30}, 0.036, 6.8e-7},
-    {2.25, {1.44, 1.45, 1.55, 0.94, 0.73, 0.91, 0.60}, 0.025, 6.8e-7},
-    {1.71, {1.44, 1.46, 0.81, 0.84, 0.66, 0.75, 0.38}, 0.025, 0.0}};
-constexpr double kTcDrain = 2.6, kTcSlot = 0.49, kTcSlotRow = 0.0148;
+    {2.35, {1.12, 1.07, 1.08, 0.654, 0.469, 0.562, 0.306}, 0.0293, 0.0},
+    {3.08, {1.14, 1.12, 1.11, 0.639, 0.429, 0.579, 0.313}, 0.0395, 5.4e-7},
+    {2.47, {1.57, 1.55, 1.59, 0.942, 0.713, 0.905, 0.608}, 0.0283, 5.4e-7},
+    {2.42, {1.56, 1.54, 0.842, 0.883, 0.699, 0.752, 0.407}, 0.0297, 0.0}};
+constexpr double kTcDrain = 1.16, kTcSlot = 3.16, kTcSlotRow = 0.0091;
+constexpr double kTcSplitDrain = 2.74, kTcReduce = 1.81, kTcReduceSlot = 0.153, kTcReduceMB = 0.397;
 // streamed at 32 rows: fixed, per 128-K block of the busiest CTA, per slot, and
 // per 128 columns for the reduction (without which M=32 N=8192 K=21760 int8 was
 // taken for 47.1 us against 46.9 on tc32_sk: 43 and 52 measured)
@@ -554,7 +556,7 @@ constexpr double kDs32Cost[3][4] = {{4.80, 0.561, 0.150, 0.0317},
 constexpr double kGv32Cost[4][4] = {{3.58, 0.775, 0.0095, 0.565},
                                     {3.71, 0.593, 0.0089, 0.567},
                                     {3.55, 0.798, 0.0091, 0.586},
-                                    {4.03, 1.10, 0.0, 0.0}};
+                                    {3.74, 0.512, 0.0085, 0.430}};
 
 double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
   const Schedule& sc = kSchedules[si];
@@ -578,19 +580,20 @@ double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t g
   const int units = p.grid / (p.pair ? 2 : 1);
   const int row = p.pair ? (p.bm == 128 ? 5 : 6)
                          : p.bm == 16 ? 0 : p.bm == 32 ? 1 : p.bm == 64 ? 2 : p.bm == 128 ? 3 : 4;
-  double stages, drains, slots = 0;
+  double us = c.fixed + c.staging * static_cast<double>(M) * K;
+  const double drain = kTcDrain + c.drain_row * p.bm;
   if (p.decomp == kDataParallel) {
-    drains = (p.tiles + units - 1) / units;
-    stages = drains * p.kb_total;
-  } else {
-    const int64_t T = static_cast<int64_t>(p.tiles) * p.kb_total, it = (T + units - 1) / units;
-    stages = static_cast<double>(it);
-    drains = static_cast<double>(it) / p.kb_total + 1;
-    slots = it < p.kb_total ? static_cast<double>((p.kb_total + it - 1) / it)
-                            : (T % units != 0 || it % p.kb_total != 0 ? 1 : 0);
+    const int drains = (p.tiles + units - 1) / units;
+    return us + drains * (p.kb_total * c.stage[row] + drain);
   }
-  return c.fixed + stages * c.stage[row] + drains * (kTcDrain + c.drain_row * p.bm) +
-         slots * (kTcSlot + kTcSlotRow * p.bm) + c.staging * static_cast<double>(M) * K;
+  const int64_t T = static_cast<int64_t>(p.tiles) * p.kb_total, it = (T + units - 1) / units;
+  const double drains = static_cast<double>(it) / p.kb_total + 1;
+  const int64_t slots = it < p.kb_total ? (p.kb_total + it - 1) / it
+                                        : T % units != 0 || it % p.kb_total != 0;
+  us += it * c.stage[row];
+  if (!tc_reduces(p)) return us + drains * drain + slots * (kTcSlot + kTcSlotRow * p.bm);
+  const double mb = (p.tiles + units) * (p.bm * kTileN * 4e-6) * (p.pair ? 2 : 1);
+  return us + drains * kTcSplitDrain + kTcReduce + (slots + 1) * kTcReduceSlot + mb * kTcReduceMB;
 }
 
 int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {

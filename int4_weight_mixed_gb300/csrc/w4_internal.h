@@ -99,6 +99,21 @@ inline bool tc_mma2(const TcPlan& p) { return p.bm <= 128 && !p.pair; }
 // W4A8 with group scales: exact chunks of 1024 K (16384 K per-channel)
 inline bool tc_grouped(const TcPlan& p) { return p.chunk_stages * kStageK * p.nsub < 16384; }
 
+// Whether tc_reduce_kernel (w4_tc_ep.cu) adds the split tiles of a plan of a
+// product with an epilogue.  CTA pairs: where a
+// tile has two contributors or more on average (M=512 4096 x 4096 bf16 41.9 ->
+// 33.5 us, M=200 2048 x 8192 E4M3 63 -> 20); with more tiles than that most of
+// the time is not the split tiles', and the partial sums of tiles of 256 x 256
+// are many bytes (M=1024 8192 x 21760 E4M3 151 us, 170 with them all written).
+inline bool tc_reduces(const TcPlan& p) {
+  if (p.decomp == kDataParallel) return false;
+  if (p.decomp == kSplitK) return p.ksplit > 1;
+  const int units = p.pair ? p.grid / 2 : p.grid;
+  if (p.pair) return 2 * p.tiles <= units;
+  const int64_t T = static_cast<int64_t>(p.tiles) * p.kb_total;
+  return T % units != 0 || T / units % p.kb_total != 0;
+}
+
 struct TcArgs {
   const uint8_t* b_packed;
   const void* scales;      // W4A16 [G][N] 16-bit; W4A8 int8 sg [G][N] or null

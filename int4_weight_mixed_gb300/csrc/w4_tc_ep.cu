@@ -111,26 +111,12 @@ cudaError_t launch_reduce(const TcPlan& plan, const EpArgs& args, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, &tc_reduce_kernel<MODE, true>, plan, args);
 }
 
-// Whether tc_reduce_kernel adds the split tiles of a plan.  CTA pairs: where a
-// tile has two contributors or more on average (M=512 4096 x 4096 bf16 41.9 ->
-// 33.5 us, M=200 2048 x 8192 E4M3 63 -> 20); with more tiles than that most of
-// the time is not the split tiles', and the partial sums of tiles of 256 x 256
-// are many bytes (M=1024 8192 x 21760 E4M3 151 us, 170 with them all written).
-bool reduces(const TcPlan& p) {
-  if (p.decomp == kDataParallel) return false;
-  if (p.decomp == kSplitK) return p.ksplit > 1;
-  const int units = p.pair ? p.grid / 2 : p.grid;
-  if (p.pair) return 2 * p.tiles <= units;
-  const int64_t T = static_cast<int64_t>(p.tiles) * p.kb_total;
-  return T % units != 0 || T / units % p.kb_total != 0;
-}
-
 }  // namespace
 
 cudaError_t launch_tc(const TcPlan& plan, const CUtensorMap& amap, const CUtensorMap& smap,
                       const CUtensorMap& zmap, const EpArgs& given, cudaStream_t s) {
   EpArgs args = given;
-  args.reduce = reduces(plan);
+  args.reduce = tc_reduces(plan);
   const cudaError_t e = plan.pair ? launch_tc_pair(plan, amap, smap, zmap, args, s)
                         : tc_mma2(plan) ? launch_tc_t<true, false>(plan, amap, smap, zmap, args, s)
                                         : launch_tc_t<false, false>(plan, amap, smap, zmap, args, s);
