@@ -262,6 +262,50 @@ def test_zero_residual_keeps_the_product(gpu_lib, name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,mode,M,N,K,gs", [
+    # every tile split: 2, 9, 33 and more contributors; the last tile ragged
+    ("tc16_sk", "bf16", 16, 392, 4096, 128), ("tc64_sk", "bf16", 64, 136, 28672, 128),
+    ("tc32_sk", "int8", 20, 256, 21760, -1), ("tc128_sk", "fp16", 77, 2056, 4096, 64),
+    ("tc64_sk", "e4m3", 100, 1000, 8192, -1), ("tc256_sk", "int8", 300, 272, 8192, 128),
+    # some tiles split, some whole; none split
+    ("tc64_sk", "bf16", 64, 20000, 2048, 128), ("tc128_sk", "int8", 513, 5000, 1024, -1),
+    ("tc16_sk", "bf16", 16, 19456, 1024, 128),
+    # two weight tiles a CTA, K splits
+    ("tc128x2_sk", "fp16", 130, 520, 4096, 128), ("tc256_kp", "e4m3", 260, 1032, 8192, -1),
+    ("tc128x2_kp", "int8", 130, 520, 8192, -1),
+    # CTA pairs: two contributors a tile and more, fewer; exact chunks in a unit
+    ("tc256p_sk", "bf16", 512, 4096, 2048, 128), ("tc256p_sk", "int8", 300, 1000, 8192, -1),
+    ("tc128p_sk", "int8", 100, 1040, 8192, 128), ("tc256p_sk", "e4m3", 200, 2056, 4096, -1),
+    ("tc256p_sk", "int8", 1000, 8192, 1024, -1), ("tc128p_sk", "fp16", 300, 6000, 1024, 128),
+    ("tc256p_sk", "int8", 300, 4864, 40960, -1)])
+def test_split_tiles_keep_the_product(gpu_lib, name, mode, M, N, K, gs):
+    """Tiles that several CTAs share are added in the order of the plain
+    product's kernels, however many share one: the same bits."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+    b = w4.prepack_B(torch.randint(-2**31, 2**31 - 1, (K // 8, N), generator=g, device=DEV,
+                                   dtype=torch.int32), w4.INT4, w4.KN_SEQ, K, N)
+    G = 1 if gs == -1 else K // gs
+    kw = dict(group_size=gs, schedule=sched(name))
+    a = torch.randn(M, K, generator=g, device=DEV)
+    if mode in ("bf16", "fp16"):
+        a = a.to(torch.bfloat16 if mode == "bf16" else torch.float16)
+        kw["scales"] = ((torch.rand(G, N, generator=g, device=DEV) + 0.5) / 256).to(a.dtype)
+    else:
+        a = (a * 30).to(torch.float8_e4m3fn) if mode == "e4m3" else (a * 30).clamp(-127, 127).to(
+            torch.int8)
+        if G > 1:
+            kw["scales"] = torch.randint(1, 17, (G, N), generator=g, device=DEV, dtype=torch.int8)
+        kw["token_scales"] = (torch.rand(M, generator=g, device=DEV) + 0.5) / 4096
+        kw["channel_scales"] = (torch.rand(N, generator=g, device=DEV) + 0.5) / 64
+    plain = w4.gemm(a, b, w4.INT4, N, **kw)
+    assert plain.isfinite().all()
+    out = w4.gemm(a, b, w4.INT4, N, residual=torch.zeros_like(plain), **kw)
+    assert torch.equal(plain, out)
+    for _ in range(3):  # and call after call
+        assert torch.equal(out, w4.gemm(a, b, w4.INT4, N, residual=torch.zeros_like(plain), **kw))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("name", SCHEDULES)
 @pytest.mark.parametrize("gated", [False, True])
 def test_residual_in_place(gpu_lib, name, gated):

@@ -113,6 +113,29 @@ def test_norm_matches_the_definition(gpu_lib, M, K, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("K", [9, 10, 15, 17, 23, 255, 257, 1111, 2049, 4100, 8191, 16385, 20001])
+def test_norm_rows_start_and_end_anywhere(gpu_lib, K, dt):
+    """Rows whose first and last values lie anywhere between two 16-byte
+    boundaries, several blocks of them a CTA: as the definition, and the same
+    bits wherever in the array a row stands."""
+    x, r, w = _inputs(min(700, 3_000_000 // K), K, dt, seed=5)
+    _all(x, r, w, what=K)
+    x, r, w = (t.to(DEV) for t in (x, r, w))
+    x[8:16] = x[:8]
+    r[8:16] = r[:8]
+    x[19:27] = x[:8]
+    r[19:27] = r[:8]
+    for residual in (None, r):
+        for out in (w4.rmsnorm(x, w, residual=residual),
+                    w4.rmsnorm_quant(x, w, residual=residual),
+                    w4.rmsnorm_quant(x, w, residual=residual, act_dtype=torch.float8_e4m3fn)):
+            for t in out if isinstance(out, tuple) else (out,):
+                t = t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
+                assert torch.equal(t[:8], t[8:16]) and torch.equal(t[:8], t[19:27])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,K", [(2000, 128), (3000, 520), (1500, 4096), (700, 8192)])
 def test_norm_many_rows(gpu_lib, M, K):
     x, r, w = _inputs(M, K, torch.float16, seed=3)
