@@ -15,6 +15,7 @@ b_scales, b_group_size, and an optional schedule).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -30,9 +31,11 @@ OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT 
 
 _DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.int8: S8, torch.int32: S32,
                torch.float8_e4m3fn: E4M3}
+_CODES8 = {torch.int8: S8, torch.float8_e4m3fn: E4M3}
 _CODE_DTYPE = {v: k for k, v in _DTYPE_CODE.items()}
 
 _lib = None
+_host = None  # the extension module (csrc/w4_host.cpp)
 _lock = threading.Lock()
 _ws_cache: dict = {}
 
@@ -53,7 +56,7 @@ def build(force: bool = False) -> str:
 
 
 def load():
-    """Load libw4.so (raises if it has not been built)."""
+    """Load libw4.so and the extension module (raises if not built)."""
     global _lib
     if _lib is not None:
         return _lib
@@ -111,8 +114,23 @@ def load():
         lib.w4_status_string.argtypes = [i32]
         lib.w4_status_string.restype = ctypes.c_char_p
         lib.w4_last_error.restype = ctypes.c_char_p
+        _load_host()
         _lib = lib
         return lib
+
+
+def _load_host():
+    global _host
+    path = _build_lib.HOST
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"w4_host.so not found at {path}: the binding's extension module is missing; "
+            "run __graft_entry__.build() or python -m int4_weight_mixed_gb300._build_lib")
+    spec = importlib.util.spec_from_file_location("w4_host", path)
+    host = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(host)
+    host.init(_ws_cache, workspace, _check)
+    _host = host
 
 
 def status_string(status: int) -> str:
@@ -342,41 +360,27 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     act(even column) * odd column (see interleave_columns).  residual: an
     array of out's type and shape, added last; it may be out itself.
     """
+    if act != ACT_NONE or gated or residual is not None:
+        if _host is None:
+            load()
+        return _host.gemm(a, b_packed, wtype, N, scales, zeros, group_size, token_scales,
+                          channel_scales, -1 if out_dtype is None else _DTYPE_CODE[out_dtype], out,
+                          ws, schedule, bias, act, gated, residual)
     lib = load()
     dev = a.device
-    if not _is_dense(dev, a, b_packed, scales, zeros, token_scales, channel_scales, out, ws, bias,
-                     residual):
+    if not _is_dense(dev, a, b_packed, scales, zeros, token_scales, channel_scales, out, ws, bias):
         _dense_on(dev, a=a, b_packed=b_packed, scales=scales, zeros=zeros,
                   token_scales=token_scales, channel_scales=channel_scales, out=out, ws=ws,
-                  bias=bias, residual=residual)
+                  bias=bias)
     M, K = a.shape
     a_code = _DTYPE_CODE[a.dtype]
     if out_dtype is None:
         out_dtype = torch.float16 if a.dtype in (torch.int8, torch.float8_e4m3fn) else a.dtype
     if out is None:
-        out = torch.empty((M, N // 2 if gated else N), dtype=out_dtype, device=dev)
-    scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
-    if act != ACT_NONE or gated or residual is not None:
-        _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales,
-                        channel_scales, gated, bias, residual, out, out_dtype)
-        args = (a.data_ptr(), a_code, M, K, b_packed.data_ptr(), wtype, N, _ptr(scales),
-                scale_code, _ptr(zeros), group_size, _ptr(token_scales), _ptr(channel_scales),
-                _ptr(bias), act, int(gated), _ptr(residual), out.data_ptr(),
-                _DTYPE_CODE[out_dtype])
-        # The library checks the workspace against its plan before it launches
-        # anything: the stream's cached one is tried as it is, and its size
-        # asked for when it is too small (1 us less a call on the host).
-        given = ws if ws is not None else workspace(dev, 0)
-        st = lib.w4_gemm_epilogue(*args, given.data_ptr(), given.numel(), _stream(dev), schedule)
-        if st == ERR_WORKSPACE and ws is None:
-            given = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
-            st = lib.w4_gemm_epilogue(*args, given.data_ptr(), given.numel(), _stream(dev),
-                                      schedule)
-        if st:
-            _check(st, "w4_gemm_epilogue")
-        return out
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
     if ws is None:  # (a given workspace is checked against the plan by the library)
         ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
+    scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
     if bias is None:
         st = lib.w4_gemm_ex(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
                             scale_code, _ptr(zeros), group_size, _ptr(token_scales),
@@ -472,32 +476,6 @@ def quantize_per_token_fp8(a: torch.Tensor, out: torch.Tensor | None = None,
     return out, scales
 
 
-def _norm_call(x, weight, eps, residual, y, scales, residual_out):
-    """w4_rmsnorm after the checks that need tensors: device, contiguity,
-    types and sizes."""
-    dev, dt, shape = x.device, x.dtype, x.shape
-    if not _is_dense(dev, x, weight, residual, y, scales, residual_out):
-        _dense_on(dev, x=x, weight=weight, residual=residual, out=y, scales=scales,
-                  residual_out=residual_out)
-    if not shape:
-        raise ValueError("x needs at least one dimension")
-    if dt is not torch.float16 and dt is not torch.bfloat16:
-        raise ValueError(f"x must be fp16 or bf16 (got {dt})")
-    K, n = shape[-1], x.numel()
-    M = n // K if K else shape[:-1].numel()
-    if weight is not None and (weight.dtype is not dt or weight.numel() != K):
-        raise ValueError(f"weight must hold {K} values of {dt}")
-    if residual is not None and (residual.dtype is not dt or residual.numel() != n):
-        raise ValueError(f"residual must hold {n} values of {dt}")
-    if residual_out is not None and (residual_out.dtype is not dt or residual_out.numel() != n):
-        raise ValueError(f"residual_out must hold {n} values of {dt}")
-    st = load().w4_rmsnorm(x.data_ptr(), _DTYPE_CODE[dt], M, K, _ptr(residual), _ptr(weight), eps,
-                           _ptr(residual_out), y.data_ptr(), _DTYPE_CODE[y.dtype], _ptr(scales),
-                           _stream(dev))
-    if st:
-        _check(st, "w4_rmsnorm")
-
-
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
             residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
             residual_out: torch.Tensor | None = None):
@@ -506,14 +484,9 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e
     product.  Returns out, or (out, residual_out) when a residual is given:
     residual_out is x + residual, the residual stream after this addition.
     out and residual_out may be x or residual (in place)."""
-    if out is None:
-        out = torch.empty_like(x)
-    elif out.dtype != x.dtype or out.shape != x.shape:
-        raise ValueError("out must have x's type and shape")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    _norm_call(x, weight, eps, residual, out, None, residual_out)
-    return out if residual is None else (out, residual_out)
+    if _host is None:
+        load()
+    return _host.norm(x, weight, eps, residual, out, None, residual_out, -1)
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -524,20 +497,12 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
     or E4M3 (torch.float8_e4m3fn) codes and one fp32 scale per row, the `a`
     and `token_scales` of a W4A8 gemm.  Returns (codes, scales), or (codes,
     scales, residual_out) when a residual is given."""
-    if act_dtype not in (torch.int8, torch.float8_e4m3fn):
+    code = _CODES8.get(act_dtype)
+    if code is None:
         raise ValueError("act_dtype must be torch.int8 or torch.float8_e4m3fn")
-    if out is None:
-        out = torch.empty(x.shape, dtype=act_dtype, device=x.device)
-    elif out.dtype != act_dtype or out.shape != x.shape:
-        raise ValueError(f"out must be {act_dtype} of x's shape")
-    if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    elif scales.dtype != torch.float32 or scales.shape != x.shape[:-1]:
-        raise ValueError("scales must be fp32, one per row of x")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    _norm_call(x, weight, eps, residual, out, scales, residual_out)
-    return (out, scales) if residual is None else (out, scales, residual_out)
+    if _host is None:
+        load()
+    return _host.norm(x, weight, eps, residual, out, scales, residual_out, code)
 
 
 def check_status(ws: torch.Tensor) -> int:

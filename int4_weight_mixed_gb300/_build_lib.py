@@ -1,18 +1,23 @@
-"""Build libw4.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Build libw4.so in-tree with nvcc for sm_103a (no cmake), and the binding's
+extension module w4_host.so beside it.
 
-The translation units compile in parallel; the shared library lands in
-int4_weight_mixed_gb300/_build/libw4.so.
+The translation units compile in parallel; both land in
+int4_weight_mixed_gb300/_build/.  libw4 knows nothing of torch or Python; the
+extension module links against it and torch's libraries.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libw4.so")
+HOST = os.path.join(BUILD, "w4_host.so")
+HOST_SOURCE = os.path.join(CSRC, "w4_host.cpp")
 SOURCES = ["w4_api.cu", "w4_kernels.cu", "w4_tc.cu", "w4_tc2.cu", "w4_tc3.cu", "w4_dk.cu", "w4_noalloc.cu",
            "w4_ds.cu", "w4_quant.cu", "w4_gv.cu", "w4_norm.cu",
            "w4_tc_ep.cu", "w4_tc_ep2.cu"]
@@ -30,20 +35,44 @@ def _nvcc() -> str:
 
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
-    return max(os.path.getmtime(p) for p in paths)
+    return max(os.path.getmtime(p) for p in paths + [HOST_SOURCE])
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _host_compile(nvcc: str, obj: str) -> list:
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+            "-I" + sysconfig.get_paths()["include"], "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+            "-c", HOST_SOURCE, "-o", obj]
+
+
+def _host_link(obj: str, out: str) -> list:
+    lib = os.path.join(_torch_dir(), "lib")
+    return [shutil.which("g++") or "g++", "-shared", "-o", out, obj, "-L" + BUILD, "-l:libw4.so",
+            "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, HOST)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     procs = []
     objs = []
+    host_obj = os.path.join(BUILD, "w4_host.o")
+    jobs = [("w4_host.cpp", _host_compile(nvcc, host_obj))]
     for src in SOURCES:
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        objs.append(obj)
-        cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        objs.append(os.path.join(BUILD, src.replace(".cu", ".o")))
+        jobs.append((src, [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", objs[-1]]))
+    for src, cmd in jobs:
         if verbose:
             print(" ".join(cmd))
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
@@ -57,6 +86,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + ".tmp.%d" % os.getpid()
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    tmp = HOST + ".tmp.%d" % os.getpid()
+    subprocess.check_call(_host_link(host_obj, tmp))
+    os.replace(tmp, HOST)
     return LIB
 
 
