@@ -194,7 +194,7 @@ typedef enum w4_act {
   W4_ACT_GELU_TANH = 4
 } w4_act;
 
-/* w4_gemm_bias with the step after the product in the same launch.  With
+/* w4_gemm_bias with the step after the product in its own kernels.  With
  * v[m][n] the fp32 value of w4_gemm_bias before its rounding (product,
  * scales, bias), and act a w4_act:
  *   gated == 0: out[m][n] = round(act(v[m][n]) + residual[m][n])   [M, N]

@@ -309,36 +309,6 @@ def interleave_columns(gate: torch.Tensor, up: torch.Tensor, dim: int = -1) -> t
     return torch.stack((gate, up), dim=dim + 1).flatten(dim, dim + 1).contiguous()
 
 
-def _check_epilogue(M, N, K, b_packed, scales, zeros, group_size, token_scales, channel_scales,
-                    gated, bias, residual, out, out_dtype):
-    """The types and sizes of what a product with an epilogue reads and
-    writes (the library sees addresses alone)."""
-    n_out = M * (N // 2 if gated else N)
-    n_groups = N * (1 if group_size == -1 or K == 0 else K // group_size if group_size > 0 else 0)
-    f32 = torch.float32
-    if M and b_packed.numel() * b_packed.element_size() < (N + 127) // 128 * 64 * K:
-        raise ValueError(f"b_packed is smaller than the prepacked {K} x {N} weight")
-    if scales is not None and scales.numel() != n_groups:
-        _not_held("scales", scales, n_groups, scales.dtype)
-    if zeros is not None and (zeros.numel() != n_groups or zeros.dtype is not out_dtype):
-        _not_held("zeros", zeros, n_groups, out_dtype)
-    if token_scales is not None and (token_scales.numel() != M or token_scales.dtype is not f32):
-        _not_held("token_scales", token_scales, M, f32)
-    if channel_scales is not None and (channel_scales.numel() != N or
-                                       channel_scales.dtype is not f32):
-        _not_held("channel_scales", channel_scales, N, f32)
-    if bias is not None and (bias.numel() != N or bias.dtype is not out_dtype):
-        _not_held("bias", bias, N, out_dtype)
-    if residual is not None and (residual.numel() != n_out or residual.dtype is not out_dtype):
-        _not_held("residual", residual, n_out, out_dtype)
-    if out.numel() != n_out or out.dtype is not out_dtype:
-        _not_held("out", out, n_out, out_dtype)
-
-
-def _not_held(name, t, n, dtype):
-    raise ValueError(f"{name} must hold {n} values of {dtype} (got {t.numel()} of {t.dtype})")
-
-
 def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
          scales: torch.Tensor | None = None, zeros: torch.Tensor | None = None,
          group_size: int = -1, token_scales: torch.Tensor | None = None,
@@ -410,25 +380,22 @@ def gemm_dynamic(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     (act_dtype torch.int8) or E4M3 (torch.float8_e4m3fn) inside the call,
     then the W4A8 product; fp16 out [M, N].  act, gated and residual as in
     gemm()."""
+    if act != ACT_NONE or gated or residual is not None:
+        if _host is None:
+            load()
+        return _host.gemm_dynamic(a, b_packed, wtype, N, _DTYPE_CODE[act_dtype], scales, group_size,
+                                  channel_scales, bias, out, token_scales_out, ws, act, gated,
+                                  residual)
     lib = load()
     _dense_on(a.device, a=a, b_packed=b_packed, scales=scales, channel_scales=channel_scales,
-              bias=bias, out=out, token_scales_out=token_scales_out, ws=ws, residual=residual)
+              bias=bias, out=out, token_scales_out=token_scales_out, ws=ws)
     M, K = a.shape
     code = _DTYPE_CODE[act_dtype]
     if out is None:
-        out = torch.empty((M, N // 2 if gated else N), dtype=torch.float16, device=a.device)
+        out = torch.empty((M, N), dtype=torch.float16, device=a.device)
     if ws is None:  # (a given workspace is checked against the plan by the library)
         ws = workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, code, group_size)))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else S8
-    if act != ACT_NONE or gated or residual is not None:
-        _check_epilogue(M, N, K, b_packed, scales, None, group_size, token_scales_out,
-                        channel_scales, gated, bias, residual, out, torch.float16)
-        _check(lib.w4_gemm_dynamic_epilogue(
-            _ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N, _ptr(scales), scale_code,
-            group_size, _ptr(channel_scales), code, _ptr(bias), act, int(gated), _ptr(residual),
-            _ptr(out), _ptr(token_scales_out), _ptr(ws), ws.numel(), _stream(a.device)),
-            "w4_gemm_dynamic_epilogue")
-        return out
     _check(lib.w4_gemm_dynamic(_ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N,
                                _ptr(scales), scale_code, group_size, _ptr(channel_scales), code,
                                _ptr(bias), _ptr(out), _ptr(token_scales_out), _ptr(ws),

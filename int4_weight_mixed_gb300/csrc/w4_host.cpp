@@ -197,6 +197,47 @@ at::Tensor workspace(PyObject* a, c10::Device dev, void* stream, int64_t bytes) 
   return t;
 }
 
+// The sizes and types of a product's arrays (the library sees addresses alone).
+struct Product {
+  const at::Tensor *a, *b, *scales, *zeros, *s_tok, *s_ch, *out, *ws, *bias, *residual;
+  int64_t N, gs;
+  at::ScalarType ot;  // of the output
+  int gated;
+  int64_t M, K, cols;
+  c10::Device dev = c10::Device(c10::kCPU);
+
+  void devices() {
+    dev = a->device();
+    dense(a, dev, "a");
+    dense(b, dev, "b_packed");
+    dense(scales, dev, "scales");
+    dense(zeros, dev, "zeros");
+    dense(s_tok, dev, "token_scales");
+    dense(s_ch, dev, "channel_scales");
+    dense(out, dev, "out");
+    dense(ws, dev, "ws");
+    dense(bias, dev, "bias");
+    dense(residual, dev, "residual");
+    if (a->dim() != 2) bad_value("a must be [M, K]");
+    M = a->size(0);
+    K = a->size(1);
+    cols = gated ? N / 2 : N;
+  }
+  void sizes() const {
+    const int64_t n_groups = N * (gs == -1 || K == 0 ? 1 : gs > 0 ? K / gs : 0);
+    if (M && static_cast<int64_t>(b->nbytes()) < (N + 127) / 128 * 64 * K)
+      bad_value("b_packed is smaller than the prepacked " + std::to_string(K) + " x " +
+                std::to_string(N) + " weight");
+    if (scales) holds(scales, n_groups, scales->scalar_type(), "scales");
+    holds(zeros, n_groups, ot, "zeros");
+    holds(s_tok, M, at::kFloat, "token_scales");
+    holds(s_ch, N, at::kFloat, "channel_scales");
+    holds(bias, N, ot, "bias");
+    holds(residual, M * cols, ot, "residual");
+    holds(out, M * cols, ot, "out");
+  }
+};
+
 // gemm(a, b_packed, wtype, N, scales, zeros, group_size, token_scales,
 // channel_scales, out_code (-1: by a), out, ws, schedule, bias, act, gated,
 // residual)
@@ -217,37 +258,18 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     const int act = static_cast<int>(integer(v[14]));
     const int gated = PyObject_IsTrue(v[15]);
     if (gated < 0) throw Bad();
-    const c10::Device dev = a->device();
-    dense(a, dev, "a");
-    dense(b, dev, "b_packed");
-    dense(scales, dev, "scales");
-    dense(zeros, dev, "zeros");
-    dense(s_tok, dev, "token_scales");
-    dense(s_ch, dev, "channel_scales");
-    dense(out, dev, "out");
-    dense(ws, dev, "ws");
-    dense(bias, dev, "bias");
-    dense(residual, dev, "residual");
-    if (a->dim() != 2) bad_value("a must be [M, K]");
-    const int64_t M = a->size(0), K = a->size(1);
+    Product p{a, b, scales, zeros, s_tok, s_ch, out, ws, bias, residual, N, gs, at::kHalf, gated};
+    p.devices();
     const int a_code = code_of(a->scalar_type());
     const at::ScalarType ot = out_code >= 0 ? type_of(static_cast<int>(out_code))
                               : a_code == W4_S8 || a_code == W4_E4M3 ? at::kHalf
                                                                      : a->scalar_type();
-    const int64_t cols = gated ? N / 2 : N;
-    const int64_t n_groups = N * (gs == -1 || K == 0 ? 1 : gs > 0 ? K / gs : 0);
-    if (M && static_cast<int64_t>(b->nbytes()) < (N + 127) / 128 * 64 * K)
-      bad_value("b_packed is smaller than the prepacked " + std::to_string(K) + " x " +
-                std::to_string(N) + " weight");
-    if (scales) holds(scales, n_groups, scales->scalar_type(), "scales");
-    holds(zeros, n_groups, ot, "zeros");
-    holds(s_tok, M, at::kFloat, "token_scales");
-    holds(s_ch, N, at::kFloat, "channel_scales");
-    holds(bias, N, ot, "bias");
-    holds(residual, M * cols, ot, "residual");
-    holds(out, M * cols, ot, "out");
+    p.ot = ot;
+    p.sizes();
+    const int64_t M = p.M, K = p.K;
+    const c10::Device dev = p.dev;
     at::Tensor o_new;
-    if (!out) out = &(o_new = empty({M, cols}, ot, dev));
+    if (!out) out = &(o_new = empty({M, p.cols}, ot, dev));
     void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     const int s_code = scales ? code_of(scales->scalar_type()) : a_code, o_code = code_of(ot);
     const void *pa = ptr(a), *pb = ptr(b), *ps = ptr(scales), *pz = ptr(zeros);
@@ -279,6 +301,57 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// gemm_dynamic(a, b_packed, wtype, N, act_code, scales, group_size,
+// channel_scales, bias, out, token_scales_out, ws, act, gated, residual)
+PyObject* gemm_dynamic(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  try {
+    if (nargs != 15) bad(PyExc_TypeError, "gemm_dynamic takes 15 arguments");
+    const at::Tensor *a = tensor(v[0], "a"), *b = tensor(v[1], "b_packed");
+    if (!a || !b) bad(PyExc_TypeError, "a and b_packed must be tensors");
+    const int wtype = static_cast<int>(integer(v[2])), code = static_cast<int>(integer(v[4]));
+    const int64_t N = integer(v[3]), gs = integer(v[6]);
+    const at::Tensor *scales = tensor(v[5], "scales"), *s_ch = tensor(v[7], "channel_scales");
+    const at::Tensor *bias = tensor(v[8], "bias"), *out = tensor(v[9], "out");
+    const at::Tensor *s_tok = tensor(v[10], "token_scales_out"), *ws = tensor(v[11], "ws");
+    const at::Tensor* residual = tensor(v[14], "residual");
+    const int act = static_cast<int>(integer(v[12]));
+    const int gated = PyObject_IsTrue(v[13]);
+    if (gated < 0) throw Bad();
+    Product p{a, b, scales, nullptr, s_tok, s_ch, out, ws, bias, residual, N, gs, at::kHalf, gated};
+    p.devices();
+    p.sizes();
+    const int64_t M = p.M, K = p.K;
+    at::Tensor o_new, w_new;
+    if (!out) out = &(o_new = empty({M, p.cols}, at::kHalf, p.dev));
+    void* const stream = c10::cuda::getCurrentCUDAStream(p.dev.index()).stream();
+    const int a_code = code_of(a->scalar_type());
+    const int s_code = scales ? code_of(scales->scalar_type()) : W4_S8;
+    const void *pa = ptr(a), *pb = ptr(b), *ps = ptr(scales), *pbias = ptr(bias), *pr = ptr(residual);
+    const float* pc = static_cast<const float*>(ptr(s_ch));
+    float* const pt = static_cast<float*>(out_ptr(s_tok));
+    void* const po = out_ptr(out);
+    int st;
+    for (int64_t bytes = 0;; bytes = static_cast<int64_t>(
+                                 w4_gemm_dynamic_workspace_size(M, N, K, code, gs))) {
+      if (!ws) w_new = workspace(v[0], p.dev, stream, bytes);
+      const at::Tensor& w = ws ? *ws : w_new;
+      void* const pw = out_ptr(&w);
+      const size_t nw = static_cast<size_t>(w.numel());
+      Py_BEGIN_ALLOW_THREADS
+      st = w4_gemm_dynamic_epilogue(pa, a_code, M, K, pb, wtype, N, ps, s_code, gs, pc, code, pbias,
+                                    act, gated, pr, po, pt, pw, nw, stream);
+      Py_END_ALLOW_THREADS
+      if (st != W4_ERR_WORKSPACE || ws || bytes) break;
+    }
+    check(st, "w4_gemm_dynamic_epilogue");
+    return result(v[9], *out);
+  } catch (const Bad&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 // init(ws_cache, workspace, check)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (nargs != 3) {
@@ -296,6 +369,8 @@ PyMethodDef methods[] = {
     {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(init)), METH_FASTCALL, nullptr},
     {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm)), METH_FASTCALL, nullptr},
     {"gemm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm)), METH_FASTCALL, nullptr},
+    {"gemm_dynamic", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm_dynamic)),
+     METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "w4_host", nullptr, -1, methods};
 

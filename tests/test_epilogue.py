@@ -648,3 +648,58 @@ def test_interleave_columns_on_the_host():
                                                           [13, 14, 15]]
     with pytest.raises(ValueError):
         w4.interleave_columns(g, u[:1])
+
+
+def test_binding_refuses_what_is_no_tensor(lib):
+    """Errors of the host's part, before anything of the device's."""
+    x = torch.zeros(2, 64, dtype=torch.float16)
+    for call in (lambda: w4.rmsnorm(None), lambda: w4.rmsnorm([1.0]), lambda: w4.rmsnorm(x, [1.0]),
+                 lambda: w4.rmsnorm(x, None, "eps"), lambda: w4.rmsnorm_quant(x, residual=3),
+                 lambda: w4.gemm(None, x, w4.INT4, 64, act=w4.ACT_SILU),
+                 lambda: w4.gemm(x, x, w4.INT4, 64, gated=True, bias=1.0),
+                 lambda: w4.gemm(x, x, w4.INT4, 2.5, act=w4.ACT_SILU),
+                 lambda: w4.gemm_dynamic(x, None, w4.INT4, 64, act=w4.ACT_SILU)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: w4.gemm(x, x, w4.INT4, 64, act=w4.ACT_SILU),
+                 lambda: w4.gemm_dynamic(x, x, w4.INT4, 64, residual=x)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
+
+
+@pytest.mark.gpu
+def test_binding_workspace_grows_and_capture_is_refused(gpu_lib):
+    """The stream's cached workspace is taken as it is when it is large
+    enough, replaced when not, and a call under capture wants its own."""
+    small, large = Case("int8", 4, 64, 128), Case("int8", 300, 1032, 4096)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        key = (torch.device(DEV).index or 0, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        w4._ws_cache.pop(key, None)  # (a pooled stream another test has used)
+        sizes = []
+        for c in (small, large, small):
+            a, b, kw = c.device()
+            torch.cuda.current_stream().synchronize()
+            out = w4.gemm(a, b, c.wtype, c.N, act=w4.ACT_RELU, **kw)
+            sizes.append(w4._ws_cache[key].numel())
+            plain = w4.gemm(a, b, c.wtype, c.N, ws=torch.zeros(
+                w4.workspace_size(c.M, c.N, c.K, a.dtype, kw["group_size"]), dtype=torch.uint8,
+                device=DEV), act=w4.ACT_RELU, **kw)
+            assert torch.equal(out, plain)
+        assert sizes[0] < sizes[1] == sizes[2]
+        ws = w4._ws_cache.pop(key)  # (the stream and its workspace go with this test)
+        torch.cuda.current_stream().synchronize()
+        assert w4.check_status(ws) == w4.OK
+    a, b, kw = small.device()
+    ws = torch.zeros(w4.workspace_size(4, 64, 128, a.dtype, kw["group_size"]), dtype=torch.uint8,
+                     device=DEV)
+    ref = w4.gemm(a, b, small.wtype, 64, act=w4.ACT_RELU, ws=ws, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError, match="capture"):
+            w4.gemm(a, b, small.wtype, 64, act=w4.ACT_RELU, **kw)
+        out = w4.gemm(a, b, small.wtype, 64, act=w4.ACT_RELU, ws=ws, **kw)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
