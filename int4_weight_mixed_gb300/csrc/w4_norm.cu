@@ -374,14 +374,16 @@ __device__ __forceinline__ void copy_out(const uint4* from, E* to, int count, in
 // go back through the stage their inputs came from, so that they too leave in
 // 16-byte pieces.  A piece that two blocks' rows share is read by both, each
 // using its own values, and written by element.
-// Bound by instruction issue (25 a value, two thirds of the slots) and by the
-// barriers between its steps: 10782 x 6165 bf16 with a residual to E4M3 116 us
-// (59% of the copy bandwidth), 16384 x 8191 fp16 without one 123 (64%), 16384 x
-// 1111 bf16 with one 33 (65%).  Element by element from the same stages it was
-// 37 instructions a value: 143, 160 and 41 us.  More than 16384 columns take 32
-// values a thread, some of them spilled: 4096 x 20001 fp16 to int8 161 us (52%).
+// Bound by instruction issue and by the barriers between its steps: 10782 x
+// 6165 bf16 with a residual to E4M3 101 us (68% of the copy bandwidth), 16384 x
+// 8191 fp16 without one 105 (75%), 32768 x 2001 bf16 with one 94 (82%).  Four
+// vectors a thread beyond 4096 columns: with two, whose rows take more threads,
+// the first two were 117 and 123 us.  Element by element from the same stages
+// they were 143 and 160.  Beyond 16384 columns the registers of a CTA of more
+// than 512 threads do not hold four vectors without spilling: 4096 x 20001 fp16
+// to int8 161 us (52%); with eight vectors a thread 165.
 template <typename T, int OUT, bool RES, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads ? 4 : 1)
+__global__ void __launch_bounds__(MAXT, MAXT > kNormThreads ? 1 : NV == 2 ? 4 : 2)
     norm_ragged_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K,
                        float eps, T* h_out, void* y, float* scales, uint32_t range) {
   extern __shared__ __align__(16) uint8_t raw[];  // [2][x range, r range]
@@ -686,13 +688,16 @@ cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s) {
   }
   // vectors of a row a thread: by K alone, as the order of a row's sum
   const int64_t all = (a.K + 7) / 8;
-  const int nv = all <= 2 * kNormMaxThreads ? 2 : 4;
+  const int nv = all <= 2 * kNormThreads ? 2 : 4;
   const int tpr = row_threads(all, nv), rows = cta_rows(tpr);
-  if (in16 && a.K > 8 && all <= nv * kNormMaxThreads && ragged_bytes(a, rows) <= kNormMaxSmem) {
-    constexpr int kLow = kNormThreads, kHigh = kNormMaxThreads;
-    if (nv == 4) return launch_ragged<T, OUT, 4, kHigh>(a, tpr, rows, s);
-    return tpr <= kLow ? launch_ragged<T, OUT, 2, kLow>(a, tpr, rows, s)
-                       : launch_ragged<T, OUT, 2, kHigh>(a, tpr, rows, s);
+  // (the second condition holds for every K from 9 on: a thread's vectors but
+  // its last lie in the row)
+  if (in16 && a.K > 8 && (nv - 1) * tpr < all && all <= nv * tpr &&
+      ragged_bytes(a, rows) <= kNormMaxSmem) {
+    if (nv == 2) return launch_ragged<T, OUT, 2, kNormThreads>(a, tpr, rows, s);
+    if (tpr <= kNormThreads) return launch_ragged<T, OUT, 4, kNormThreads>(a, tpr, rows, s);
+    if (tpr <= 512) return launch_ragged<T, OUT, 4, 512>(a, tpr, rows, s);
+    return launch_ragged<T, OUT, 4, kNormMaxThreads>(a, tpr, rows, s);
   }
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
