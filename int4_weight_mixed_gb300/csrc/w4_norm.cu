@@ -376,14 +376,15 @@ __device__ __forceinline__ void copy_out(const uint4* from, E* to, int count, in
 // using its own values, and written by element.
 // Bound by instruction issue and by the barriers between its steps: 10782 x
 // 6165 bf16 with a residual to E4M3 101 us (68% of the copy bandwidth), 16384 x
-// 8191 fp16 without one 105 (75%), 32768 x 2001 bf16 with one 94 (82%).  Four
+// 8191 fp16 without one 98 (80%), 32768 x 2001 bf16 with one 94 (82%).  Four
 // vectors a thread beyond 4096 columns: with two, whose rows take more threads,
-// the first two were 117 and 123 us.  Element by element from the same stages
+// the first two were 117 and 123 us.  Two CTAs of four vectors an SM with a
+// residual, three without: three spill with one (115 us), two were 105 without.  Element by element from the same stages
 // they were 143 and 160.  Beyond 16384 columns the registers of a CTA of more
 // than 512 threads do not hold four vectors without spilling: 4096 x 20001 fp16
 // to int8 161 us (52%); with eight vectors a thread 165.
 template <typename T, int OUT, bool RES, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT > kNormThreads ? 1 : NV == 2 ? 4 : 2)
+__global__ void __launch_bounds__(MAXT, MAXT > kNormThreads ? 1 : NV == 2 ? 4 : RES ? 2 : 3)
     norm_ragged_kernel(const T* x, const T* r, const T* __restrict__ w, int64_t M, int K,
                        float eps, T* h_out, void* y, float* scales, uint32_t range) {
   extern __shared__ __align__(16) uint8_t raw[];  // [2][x range, r range]
