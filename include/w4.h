@@ -114,7 +114,9 @@ w4_status w4_unprepack_B(const void* b_packed, int wtype, int out_layout, int64_
  * counters and partial sums, and (W4A8) a bf16 copy of the activations.
  * It must be zero-filled before its first use; every call leaves its
  * counters at zero again.  Calls that share a workspace must not overlap
- * on the GPU. */
+ * on the GPU: one stream runs them (or the caller orders the streams).  Host
+ * threads may make such calls on one stream at the same time: the launches of
+ * a call are enqueued together, under a lock by the workspace's address. */
 size_t w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size);
 
 /* out = a x dequant(W)  ([MR] Overview and API; [QQQ]; [PT]).

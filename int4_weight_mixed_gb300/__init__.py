@@ -218,11 +218,12 @@ def workspace_size(M: int, N: int, K: int, a_dtype: torch.dtype, group_size: int
 def workspace(device, nbytes: int) -> torch.Tensor:
     """A zero-filled workspace of at least nbytes, cached per (device, stream).
 
-    Calls on the same stream are ordered, so sharing is safe; the library
-    leaves its counters at zero after every call.  Not available while the
-    stream is capturing a CUDA graph: an allocation there would come from the
-    graph's private pool and its zero-fill would be recorded into the graph,
-    so callers that capture pass a workspace allocated beforehand."""
+    Calls on the same stream are ordered, and the library enqueues the
+    launches of a call together whatever other host threads call, so sharing
+    is safe; it leaves its counters at zero after every call.  Not available
+    while the stream is capturing a CUDA graph: an allocation there would come
+    from the graph's private pool and its zero-fill would be recorded into the
+    graph, so callers that capture pass a workspace allocated beforehand."""
     dev = device if isinstance(device, torch.device) else torch.device(device)
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("w4: pass ws= (allocated before capture) to calls captured in a "

@@ -910,6 +910,17 @@ w4_status check_epilogue(const Epilogue& ep, int64_t M, int64_t N, const void* o
   return W4_OK;
 }
 
+// Held from a call's first launch to its last.  What a launch leaves in the
+// workspace for the call's next one (partial sums, staged activations, codes)
+// would be overwritten if another host thread's call with the same workspace
+// enqueued a launch between them.  One of a few locks by the workspace's
+// address: calls with different workspaces seldom wait for each other.
+std::mutex& enqueue_mutex(const void* workspace) {
+  static std::mutex mu[64];
+  const uintptr_t p = reinterpret_cast<uintptr_t>(workspace);
+  return mu[(p >> 8 ^ p >> 14 ^ p >> 21) % 64];
+}
+
 // The tensor-core schedules' epilogue reads and writes 16 bytes at a time.
 bool epilogue_aligned(const Epilogue& ep, const void* out, const void* bias,
                       const float* ch_scales) {
@@ -917,6 +928,7 @@ bool epilogue_aligned(const Epilogue& ep, const void* out, const void* bias,
          (aligned16(out) && aligned16(ep.residual) && aligned16(bias) && aligned16(ch_scales));
 }
 
+// The caller holds the workspace's enqueue_mutex.
 // prestaged: W4A8 on the tensor-core schedule with its bf16 activation copy
 // already in the workspace (the dynamic-quantization entry point writes it)
 w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void* b_packed,
@@ -1284,6 +1296,7 @@ w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const vo
     if (st != W4_OK) return st;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> together(enqueue_mutex(workspace));
   void* qdst = codes;
   int qout = act_type == W4_E4M3 ? 2 : 0;
   // the bf16 form is written from rows held in registers (16-byte loads)
@@ -1331,6 +1344,7 @@ w4_status w4_gemm_ex(const void* a, int a_type, int64_t M, int64_t K, const void
                      const void* b_zeros, int64_t group_size, const float* a_token_scales,
                      const float* ch_scales, void* out, int out_type, void* workspace,
                      size_t workspace_bytes, void* stream, int schedule) {
+  std::lock_guard<std::mutex> together(enqueue_mutex(workspace));
   return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
                    group_size, a_token_scales, ch_scales, nullptr, Epilogue{}, out, out_type,
                    workspace, workspace_bytes, stream, schedule);
@@ -1341,6 +1355,7 @@ w4_status w4_gemm_bias(const void* a, int a_type, int64_t M, int64_t K, const vo
                        const void* b_zeros, int64_t group_size, const float* a_token_scales,
                        const float* ch_scales, const void* bias, void* out, int out_type,
                        void* workspace, size_t workspace_bytes, void* stream, int schedule) {
+  std::lock_guard<std::mutex> together(enqueue_mutex(workspace));
   return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
                    group_size, a_token_scales, ch_scales, bias, Epilogue{}, out, out_type,
                    workspace, workspace_bytes, stream, schedule);
@@ -1352,6 +1367,7 @@ w4_status w4_gemm_epilogue(const void* a, int a_type, int64_t M, int64_t K, cons
                            const float* ch_scales, const void* bias, int act, int gated,
                            const void* residual, void* out, int out_type, void* workspace,
                            size_t workspace_bytes, void* stream, int schedule) {
+  std::lock_guard<std::mutex> together(enqueue_mutex(workspace));
   return gemm_impl(a, a_type, M, K, b_packed, wtype, N, b_scales, scale_type, b_zeros,
                    group_size, a_token_scales, ch_scales, bias,
                    Epilogue{act, gated != 0 ? 1 : 0, residual}, out, out_type, workspace,
