@@ -42,6 +42,8 @@
  *     returns W4_ERR_UNSUPPORTED.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Work is enqueued on it; calls return after enqueue.
+ *   - The device of the stream and the arrays is the calling thread's current
+ *     device (cudaSetDevice): calls plan for it and launch on it.
  *   - Argument errors are reported synchronously, before anything is
  *     enqueued; w4_last_error() then holds a one-line message.  The library
  *     never aborts the process and its kernels never trap.

@@ -129,7 +129,7 @@ def _load_host():
     spec = importlib.util.spec_from_file_location("w4_host", path)
     host = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(host)
-    host.init(_ws_cache, workspace, _check)
+    host.init(_ws_cache, _workspace, _check)
     _host = host
 
 
@@ -155,6 +155,17 @@ def _stream(device) -> int:
     if _raw_stream is not None and device.index is not None:
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+# The library plans for and launches on the current device: a call on tensors of
+# another GPU makes that one current for its time.
+_current_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _there(device, call, args):
+    """call(*args) with `device` the current one."""
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _is_dense(device, *tensors) -> bool:
@@ -193,6 +204,8 @@ def prepack_B(w_q: torch.Tensor, wtype: int, layout: int, K: int, N: int,
     lib = load()
     assert w_q.dtype == torch.int32 and w_q.is_cuda and w_q.is_contiguous()
     _dense_on(w_q.device, out=out)
+    if w_q.device.index != _current_index():
+        return _there(w_q.device, prepack_B, (w_q, wtype, layout, K, N, out))
     nbytes = prepacked_size(K, N)
     if out is None:
         out = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=w_q.device)
@@ -204,6 +217,8 @@ def prepack_B(w_q: torch.Tensor, wtype: int, layout: int, K: int, N: int,
 def unprepack_B(b_packed: torch.Tensor, wtype: int, layout: int, K: int, N: int) -> torch.Tensor:
     lib = load()
     _dense_on(b_packed.device, b_packed=b_packed)
+    if b_packed.device.index != _current_index():
+        return _there(b_packed.device, unprepack_B, (b_packed, wtype, layout, K, N))
     shape = (K // 8, N) if layout == KN_SEQ else (N, K // 8)
     w_q = torch.empty(shape, dtype=torch.int32, device=b_packed.device)
     _check(lib.w4_unprepack_B(_ptr(b_packed), wtype, layout, K, N, _ptr(w_q),
@@ -225,6 +240,13 @@ def workspace(device, nbytes: int) -> torch.Tensor:
     from the graph's private pool and its zero-fill would be recorded into the
     graph, so callers that capture pass a workspace allocated beforehand."""
     dev = device if isinstance(device, torch.device) else torch.device(device)
+    if dev.index is not None and dev.index != _current_index():
+        return _there(dev, _workspace, (dev, nbytes))
+    return _workspace(dev, nbytes)
+
+
+def _workspace(dev, nbytes: int) -> torch.Tensor:
+    """workspace() of the current device."""
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("w4: pass ws= (allocated before capture) to calls captured in a "
                            "CUDA graph")
@@ -268,6 +290,9 @@ def autotune(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int, instal
     make the fastest the default for exactly this shape (w4_override_schedule
     for this M).  Returns {schedule name: microseconds per call}.  The calls
     write `out` (or a scratch output) and use `ws` (or the cached workspace)."""
+    if a.is_cuda and a.device.index != _current_index():
+        with torch.cuda.device(a.device):
+            return autotune(a, b_packed, wtype, N, install, reps, **kw)
     M, K = a.shape
     names = schedule_names()
     kw = dict(kw)
@@ -334,15 +359,20 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     if act != ACT_NONE or gated or residual is not None:
         if _host is None:
             load()
-        return _host.gemm(a, b_packed, wtype, N, scales, zeros, group_size, token_scales,
-                          channel_scales, -1 if out_dtype is None else _DTYPE_CODE[out_dtype], out,
-                          ws, schedule, bias, act, gated, residual)
+        args = (a, b_packed, wtype, N, scales, zeros, group_size, token_scales, channel_scales,
+                -1 if out_dtype is None else _DTYPE_CODE[out_dtype], out, ws, schedule, bias, act,
+                gated, residual)
+        done = _host.gemm(*args)
+        return done if done is not NotImplemented else _there(a.device, _host.gemm, args)
     lib = load()
     dev = a.device
     if not _is_dense(dev, a, b_packed, scales, zeros, token_scales, channel_scales, out, ws, bias):
         _dense_on(dev, a=a, b_packed=b_packed, scales=scales, zeros=zeros,
                   token_scales=token_scales, channel_scales=channel_scales, out=out, ws=ws,
                   bias=bias)
+    if dev.index != _current_index():
+        return _there(dev, gemm, (a, b_packed, wtype, N, scales, zeros, group_size, token_scales,
+                                  channel_scales, out_dtype, out, ws, schedule, bias))
     M, K = a.shape
     a_code = _DTYPE_CODE[a.dtype]
     if out_dtype is None:
@@ -350,7 +380,7 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     if ws is None:  # (a given workspace is checked against the plan by the library)
-        ws = workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
+        ws = _workspace(dev, workspace_size(M, N, K, a.dtype, group_size))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else a_code
     if bias is None:
         st = lib.w4_gemm_ex(_ptr(a), a_code, M, K, _ptr(b_packed), wtype, N, _ptr(scales),
@@ -384,18 +414,23 @@ def gemm_dynamic(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     if act != ACT_NONE or gated or residual is not None:
         if _host is None:
             load()
-        return _host.gemm_dynamic(a, b_packed, wtype, N, _DTYPE_CODE[act_dtype], scales, group_size,
-                                  channel_scales, bias, out, token_scales_out, ws, act, gated,
-                                  residual)
+        args = (a, b_packed, wtype, N, _DTYPE_CODE[act_dtype], scales, group_size, channel_scales,
+                bias, out, token_scales_out, ws, act, gated, residual)
+        done = _host.gemm_dynamic(*args)
+        return done if done is not NotImplemented else _there(a.device, _host.gemm_dynamic, args)
     lib = load()
     _dense_on(a.device, a=a, b_packed=b_packed, scales=scales, channel_scales=channel_scales,
               bias=bias, out=out, token_scales_out=token_scales_out, ws=ws)
+    if a.device.index != _current_index():
+        return _there(a.device, gemm_dynamic, (a, b_packed, wtype, N, act_dtype, scales, group_size,
+                                               channel_scales, bias, out, token_scales_out, ws))
     M, K = a.shape
     code = _DTYPE_CODE[act_dtype]
     if out is None:
         out = torch.empty((M, N), dtype=torch.float16, device=a.device)
     if ws is None:  # (a given workspace is checked against the plan by the library)
-        ws = workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, code, group_size)))
+        ws = _workspace(a.device, int(lib.w4_gemm_dynamic_workspace_size(M, N, K, code,
+                                                                         group_size)))
     scale_code = _DTYPE_CODE[scales.dtype] if scales is not None else S8
     _check(lib.w4_gemm_dynamic(_ptr(a), _DTYPE_CODE[a.dtype], M, K, _ptr(b_packed), wtype, N,
                                _ptr(scales), scale_code, group_size, _ptr(channel_scales), code,
@@ -411,6 +446,8 @@ def quantize_per_token(a: torch.Tensor, out: torch.Tensor | None = None,
     W4A8 gemm."""
     lib = load()
     assert a.dim() == 2 and a.is_cuda and a.is_contiguous()
+    if a.device.index != _current_index():
+        return _there(a.device, quantize_per_token, (a, out, scales))
     M, K = a.shape
     if out is None:
         out = torch.empty(M, K, dtype=torch.int8, device=a.device)
@@ -430,6 +467,8 @@ def quantize_per_token_fp8(a: torch.Tensor, out: torch.Tensor | None = None,
     and `token_scales` of a W4A8 gemm with fp8 activations."""
     lib = load()
     assert a.dim() == 2 and a.is_cuda and a.is_contiguous()
+    if a.device.index != _current_index():
+        return _there(a.device, quantize_per_token_fp8, (a, out, scales))
     M, K = a.shape
     if out is None:
         out = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=a.device)
@@ -454,7 +493,9 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e
     out and residual_out may be x or residual (in place)."""
     if _host is None:
         load()
-    return _host.norm(x, weight, eps, residual, out, None, residual_out, -1)
+    args = (x, weight, eps, residual, out, None, residual_out, -1)
+    done = _host.norm(*args)
+    return done if done is not NotImplemented else _there(x.device, _host.norm, args)
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -470,9 +511,13 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
         raise ValueError("act_dtype must be torch.int8 or torch.float8_e4m3fn")
     if _host is None:
         load()
-    return _host.norm(x, weight, eps, residual, out, scales, residual_out, code)
+    args = (x, weight, eps, residual, out, scales, residual_out, code)
+    done = _host.norm(*args)
+    return done if done is not NotImplemented else _there(x.device, _host.norm, args)
 
 
 def check_status(ws: torch.Tensor) -> int:
     """w4_check_status: sync and report a device-side timeout recorded in ws."""
+    if ws.device.index != _current_index():
+        return _there(ws.device, check_status, (ws,))
     return load().w4_check_status(_ptr(ws), ws.numel(), _stream(ws.device))

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -83,6 +84,15 @@ void holds(const at::Tensor* t, int64_t n, at::ScalarType type, const char* name
 const void* ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 void* out_ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
+// Whether dev, the tensors' device, is the current one: the library plans for
+// that one and launches on it.  If not, the entry points return NotImplemented
+// and the Python module calls again with dev current (a guard of torch's here
+// would be the same, but could not be tried without a second GPU).
+bool is_current(c10::Device dev) {
+  c10::DeviceIndex now = -1;
+  return c10::cuda::GetDevice(&now) == cudaSuccess && now == dev.index();
+}
+
 at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
@@ -141,6 +151,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     holds(weight, K, dt, "weight");
     holds(residual, n, dt, "residual");
     holds(h, n, dt, "residual_out");
+    if (!is_current(dev)) Py_RETURN_NOTIMPLEMENTED;
     at::Tensor y_new, s_new, h_new;
     if (!y) y = &(y_new = empty(shape, yt, dev));
     if (!scales && code >= 0) scales = &(s_new = empty(shape.slice(0, shape.size() - 1), at::kFloat, dev));
@@ -266,6 +277,7 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
                                                                      : a->scalar_type();
     p.ot = ot;
     p.sizes();
+    if (!is_current(p.dev)) Py_RETURN_NOTIMPLEMENTED;
     const int64_t M = p.M, K = p.K;
     const c10::Device dev = p.dev;
     at::Tensor o_new;
@@ -321,6 +333,7 @@ PyObject* gemm_dynamic(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     Product p{a, b, scales, nullptr, s_tok, s_ch, out, ws, bias, residual, N, gs, at::kHalf, gated};
     p.devices();
     p.sizes();
+    if (!is_current(p.dev)) Py_RETURN_NOTIMPLEMENTED;
     const int64_t M = p.M, K = p.K;
     at::Tensor o_new, w_new;
     if (!out) out = &(o_new = empty({M, p.cols}, at::kHalf, p.dev));
