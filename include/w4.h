@@ -217,8 +217,9 @@ typedef enum w4_act {
  * With act NONE, gated 0 and residual NULL this is exactly w4_gemm_bias.
  * The schedules and workspace are those of w4_gemm for the same M, N and K,
  * and a given schedule sums in the same order; beyond 16 rows the default
- * one is chosen by a rule of its own (the least estimated time; overrides
- * come first).  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
+ * one is chosen by a rule of its own (the least estimated time;
+ * w4_default_epilogue_schedule tells it, w4_override_epilogue_schedule
+ * changes it).  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
  * an odd N with gated, an epilogue on the raw int32 output, a residual not
  * aligned to 2 bytes or one that overlaps out without being out.  With
  * K == 0 the product is 0. */
@@ -234,6 +235,9 @@ w4_status w4_gemm_epilogue(const void* a, int a_type, int64_t M, int64_t K, cons
 int w4_num_schedules(void);
 const char* w4_schedule_name(int schedule);
 int w4_default_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size);
+/* The same of a product with an epilogue (w4_gemm_epilogue with an act, gate
+ * or residual). */
+int w4_default_epilogue_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size);
 
 /* Install a per-shape override of the default heuristic ([MR] Code
  * Generation: per-shape schedule choices; [RDNA] a per-shape override
@@ -244,9 +248,14 @@ int w4_default_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t gro
  * installed here are consulted before the library's built-in table, which
  * holds measured exceptions to the heuristic.  Host-side only; thread-safe;
  * at most 256 entries (UNSUPPORTED beyond).  Errors: INVALID_ARGUMENT for
- * a bad a_type, range, shape, group size or schedule index. */
+ * a bad a_type, range, shape, group size or schedule index.
+ * The entries of w4_override_schedule are for products without an epilogue,
+ * those of w4_override_epilogue_schedule for products with one (either leaves
+ * the other's choice as it is); the built-in table is for both. */
 w4_status w4_override_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N, int64_t K,
                                int64_t group_size, int schedule);
+w4_status w4_override_epilogue_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N,
+                                        int64_t K, int64_t group_size, int schedule);
 
 /* Synchronize `stream`, then report (and clear) a device-side timeout that
  * a kernel recorded in `workspace`: W4_ERR_TIMEOUT, else W4_OK.  On a

@@ -91,10 +91,12 @@ def load():
         lib.w4_num_schedules.restype = i32
         lib.w4_schedule_name.argtypes = [i32]
         lib.w4_schedule_name.restype = ctypes.c_char_p
-        lib.w4_default_schedule.argtypes = [i64, i64, i64, i32, i64]
-        lib.w4_default_schedule.restype = i32
-        lib.w4_override_schedule.argtypes = [i32, i64, i64, i64, i64, i64, i32]
-        lib.w4_override_schedule.restype = i32
+        for name in ("w4_default_schedule", "w4_default_epilogue_schedule"):
+            getattr(lib, name).argtypes = [i64, i64, i64, i32, i64]
+            getattr(lib, name).restype = i32
+        for name in ("w4_override_schedule", "w4_override_epilogue_schedule"):
+            getattr(lib, name).argtypes = [i32, i64, i64, i64, i64, i64, i32]
+            getattr(lib, name).restype = i32
         lib.w4_quantize_per_token.argtypes = [p, i32, i64, i64, p, p, p]
         lib.w4_quantize_per_token.restype = i32
         lib.w4_gemm_dynamic_workspace_size.argtypes = [i64, i64, i64, i32, i64]
@@ -267,29 +269,40 @@ def schedule_names() -> list:
     return [lib.w4_schedule_name(i).decode() for i in range(lib.w4_num_schedules())]
 
 
-def default_schedule(M: int, N: int, K: int, a_dtype: torch.dtype, group_size: int) -> int:
-    return load().w4_default_schedule(M, N, K, _DTYPE_CODE[a_dtype], group_size)
+def default_schedule(M: int, N: int, K: int, a_dtype: torch.dtype, group_size: int,
+                     epilogue: bool = False) -> int:
+    """w4_default_schedule, or w4_default_epilogue_schedule for a product with
+    an activation, a gate or a residual."""
+    lib = load()
+    pick = lib.w4_default_epilogue_schedule if epilogue else lib.w4_default_schedule
+    return pick(M, N, K, _DTYPE_CODE[a_dtype], group_size)
 
 
 def override_schedule(a_dtype: torch.dtype, m_lo: int, m_hi: int, N: int, K: int,
-                      group_size: int, schedule) -> None:
+                      group_size: int, schedule, epilogue: bool = False) -> None:
     """w4_override_schedule: problems of this shape with M in [m_lo, m_hi]
-    run `schedule` (index or name) by default; None / -1 removes the entry."""
+    run `schedule` (index or name) by default; None / -1 removes the entry.
+    epilogue: w4_override_epilogue_schedule, for the products with an
+    activation, a gate or a residual instead of those without."""
     if schedule is None:
         schedule = -1
     elif isinstance(schedule, str):
         schedule = schedule_names().index(schedule)
-    _check(load().w4_override_schedule(_DTYPE_CODE[a_dtype], m_lo, m_hi, N, K, group_size,
-                                       schedule), "w4_override_schedule")
+    name = "w4_override_epilogue_schedule" if epilogue else "w4_override_schedule"
+    _check(getattr(load(), name)(_DTYPE_CODE[a_dtype], m_lo, m_hi, N, K, group_size, schedule),
+           name)
 
 
 def autotune(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int, install: bool = True,
              reps: int = 20, **kw) -> dict:
     """Time every schedule that can run this problem (the arguments of
     gemm()) with CUDA events on the current stream, and, with install=True,
-    make the fastest the default for exactly this shape (w4_override_schedule
-    for this M).  Returns {schedule name: microseconds per call}.  The calls
-    write `out` (or a scratch output) and use `ws` (or the cached workspace)."""
+    make the fastest the default for exactly this shape (override_schedule for
+    this M, and for products with or without an epilogue as these arguments
+    have one).  Returns {schedule name: microseconds per call}.  The calls
+    write `out` (or a scratch output, also where out is the residual: a timed
+    call must not change what the next one reads) and use `ws` (or the cached
+    workspace)."""
     if a.is_cuda and a.device.index != _current_index():
         with torch.cuda.device(a.device):
             return autotune(a, b_packed, wtype, N, install, reps, **kw)
@@ -300,6 +313,10 @@ def autotune(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int, instal
     group_size = kw.get("group_size", -1)
     if kw.get("ws") is None:
         kw["ws"] = workspace(a.device, workspace_size(M, N, K, a.dtype, group_size))
+    residual, out = kw.get("residual"), kw.get("out")
+    if residual is not None and out is not None and out.data_ptr() == residual.data_ptr():
+        kw["out"] = torch.empty_like(out)
+    epilogue = bool(kw.get("act", ACT_NONE) != ACT_NONE or kw.get("gated") or residual is not None)
     times = {}
     stream = torch.cuda.current_stream(a.device)
     for si, name in enumerate(names):
@@ -320,7 +337,7 @@ def autotune(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int, instal
         times[name] = e0.elapsed_time(e1) * 1e3 / reps
     if install and times:
         best = min(times, key=times.get)
-        override_schedule(a.dtype, M, M, N, K, group_size, best)
+        override_schedule(a.dtype, M, M, N, K, group_size, best, epilogue)
     return times
 
 

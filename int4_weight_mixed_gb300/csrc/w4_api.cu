@@ -427,21 +427,24 @@ GvPlan make_gv_plan(int si, int mode, int64_t M, int64_t N, int64_t K) {
 // Built-in entries come from A/B timings of the candidate schedules on
 // GB300 (graphs of 16 back-to-back launches over rotated weight copies, more
 // than 2x L2 between two reads of a copy); entries installed at run time
-// (w4_override_schedule) are consulted first.  M in [m_lo, m_hi]; group_size
-// as resolved (K for one group per column).
+// (w4_override_schedule; w4_override_epilogue_schedule for products with an
+// epilogue of their own, whose fastest schedule may be another) are consulted
+// first.  M in [m_lo, m_hi]; group_size as resolved (K for one group per
+// column).
 struct Override {
   int mode;
   int64_t m_lo, m_hi, N, K, gs;
   int schedule;
+  bool epilogue;  // of products with an epilogue (the built-in entries: of both)
 };
 const char* const kBuiltinOverrideNames[] = {"tc256p_dp", "tc256p_dp"};
 const Override kBuiltinOverrides[] = {
     // W4A16 bf16, Llama-3-70B MLP down projection (N=8192, K=28672), M=4096:
     // tc256p_dp 1252 us, tc256p_sk 1349, tc256_sk 1598
-    {kW4A16_BF16, 4096, 8192, 8192, 28672, 128, -1},
+    {kW4A16_BF16, 4096, 8192, 8192, 28672, 128, -1, false},
     // W4A16 bf16, Llama-3-70B MLP gate/up (N=57344, K=8192), M=4096:
     // tc256p_dp 2585 us, tc256p_sk 2594, tc256_sk 3341
-    {kW4A16_BF16, 4096, 8192, 57344, 8192, 128, -1},
+    {kW4A16_BF16, 4096, 8192, 57344, 8192, 128, -1, false},
 };
 constexpr int kMaxOverrides = 256;
 std::mutex g_ov_mutex;
@@ -459,11 +462,12 @@ bool override_matches(const Override& o, int mode, int64_t M, int64_t N, int64_t
 }
 
 // The schedule an override names for this problem, or -1.
-int override_for(int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
+int override_for(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool epilogue) {
   {
     std::lock_guard<std::mutex> lock(g_ov_mutex);
     for (int i = g_num_overrides - 1; i >= 0; --i)  // the latest installed wins
-      if (override_matches(g_overrides[i], mode, M, N, K, gs)) return g_overrides[i].schedule;
+      if (g_overrides[i].epilogue == epilogue && override_matches(g_overrides[i], mode, M, N, K, gs))
+        return g_overrides[i].schedule;
   }
   for (size_t i = 0; i < sizeof(kBuiltinOverrides) / sizeof(kBuiltinOverrides[0]); ++i)
     if (override_matches(kBuiltinOverrides[i], mode, M, N, K, gs))
@@ -471,9 +475,8 @@ int override_for(int mode, int64_t M, int64_t N, int64_t K, int64_t gs) {
   return -1;
 }
 
-int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
-  const int ov = override_for(mode, M, N, K, gs);
-  if (ov >= 0 && schedule_fits(ov, mode, M, N, K, gs, has_sg)) return ov;
+// The heuristic's choice, whatever the overrides say.
+int rule_schedule(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
   // skinny M (up to 32 rows with the clustered or streamed schedule, 16 with
   // the register-fed one where neither can run: N not a multiple of 8):
   // warp-level MMAs on dequantized weights
@@ -511,6 +514,12 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
         schedule_fits(si, mode, M, N, K, gs, has_sg))
       return si;
   return 0;
+}
+
+int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
+  const int ov = override_for(mode, M, N, K, gs, false);
+  if (ov >= 0 && schedule_fits(ov, mode, M, N, K, gs, has_sg)) return ov;
+  return rule_schedule(mode, M, N, K, gs, has_sg);
 }
 
 // ---------------------------------------------------------------------------
@@ -597,9 +606,10 @@ double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t g
 }
 
 int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
-  const int plain = default_schedule_impl(mode, M, N, K, gs, has_sg);
-  if (M <= 16 || kSchedules[plain].engine == kEngineSimt || override_for(mode, M, N, K, gs) == plain)
-    return plain;
+  const int ov = override_for(mode, M, N, K, gs, true);
+  if (ov >= 0 && schedule_fits(ov, mode, M, N, K, gs, has_sg)) return ov;
+  const int plain = rule_schedule(mode, M, N, K, gs, has_sg);
+  if (M <= 16 || kSchedules[plain].engine == kEngineSimt) return plain;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
@@ -811,16 +821,20 @@ const char* w4_schedule_name(int schedule) {
   return kSchedules[schedule].name;
 }
 
-int w4_default_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size) {
+}  // extern "C"
+
+namespace {
+int default_of(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size, bool epilogue) {
   if (M <= 0 || N <= 0 || K <= 0 || K % kStageK != 0) return -1;
   if (!valid_a_type(a_type)) return -1;
   if (a_type == W4_E4M3 && K % 128 != 0) return -1;
   const int64_t gs = group_size == -1 ? K : group_size;
-  return default_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K);
+  return epilogue ? epilogue_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K)
+                  : default_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K);
 }
 
-w4_status w4_override_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N, int64_t K,
-                               int64_t group_size, int schedule) {
+w4_status install_override(int a_type, int64_t m_lo, int64_t m_hi, int64_t N, int64_t K,
+                           int64_t group_size, int schedule, bool epilogue) {
   if (!valid_a_type(a_type))
     return fail(W4_ERR_INVALID_ARGUMENT, "a_type must be W4_F16, W4_BF16, W4_S8 or W4_E4M3");
   if (m_lo < 1 || m_hi < m_lo || N < 1 || K < 1 || K % kStageK != 0)
@@ -835,14 +849,36 @@ w4_status w4_override_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N
   int n = 0;
   for (int i = 0; i < g_num_overrides; ++i) {
     const Override& o = g_overrides[i];
-    if (!(o.mode == mode && o.m_lo == m_lo && o.m_hi == m_hi && o.N == N && o.K == K && o.gs == gs))
+    if (!(o.mode == mode && o.m_lo == m_lo && o.m_hi == m_hi && o.N == N && o.K == K &&
+          o.gs == gs && o.epilogue == epilogue))
       g_overrides[n++] = o;
   }
   g_num_overrides = n;
   if (schedule < 0) return W4_OK;
   if (g_num_overrides == kMaxOverrides) return fail(W4_ERR_UNSUPPORTED, "override table full");
-  g_overrides[g_num_overrides++] = Override{mode, m_lo, m_hi, N, K, gs, schedule};
+  g_overrides[g_num_overrides++] = Override{mode, m_lo, m_hi, N, K, gs, schedule, epilogue};
   return W4_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int w4_default_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size) {
+  return default_of(M, N, K, a_type, group_size, false);
+}
+
+int w4_default_epilogue_schedule(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size) {
+  return default_of(M, N, K, a_type, group_size, true);
+}
+
+w4_status w4_override_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N, int64_t K,
+                               int64_t group_size, int schedule) {
+  return install_override(a_type, m_lo, m_hi, N, K, group_size, schedule, false);
+}
+
+w4_status w4_override_epilogue_schedule(int a_type, int64_t m_lo, int64_t m_hi, int64_t N,
+                                        int64_t K, int64_t group_size, int schedule) {
+  return install_override(a_type, m_lo, m_hi, N, K, group_size, schedule, true);
 }
 
 size_t w4_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size) {

@@ -1,0 +1,102 @@
+"""Which schedule a product takes by default, with and without an epilogue."""
+import pytest
+import torch
+
+import int4_weight_mixed_gb300 as w4
+from fake_cuda import build
+
+P = 0x10000000  # (never dereferenced: nothing runs)
+
+
+@pytest.fixture(scope="module")
+def rec(tmp_path_factory):
+    return build(tmp_path_factory.mktemp("recorded"))
+
+
+def _launched(rec, M, N, K, a_type, gs=-1, **ep):
+    """The kernels of a product, with an epilogue if `ep` has one."""
+    w8 = a_type in (w4.S8, w4.E4M3)
+    scales = 0 if w8 and gs == -1 else 2 * P
+    d = dict(bias=0, act=0, gated=0, residual=0, out=8 * P, ch=6 * P if w8 else 0)
+    d.update(ep)
+    rec.reset()
+    st = rec.lib.w4_gemm_epilogue(
+        P, a_type, M, K, 3 * P, w4.INT4 if w8 else w4.UINT4B8, N, scales, a_type, 0, gs,
+        5 * P if w8 else 0, d["ch"], d["bias"], d["act"], d["gated"], d["residual"], d["out"],
+        w4.F16 if w8 else a_type, 0x40000000, 1 << 40, None, -1)
+    assert st == w4.OK, rec.lib.w4_last_error()
+    return " ".join(k for _, k in rec.launches())
+
+
+def test_overrides_of_one_kind_leave_the_other(rec):
+    """An override for products without an epilogue does not touch those with
+    one, and the reverse; the kernels that are launched follow."""
+    lib = rec.lib
+    index = {lib.w4_schedule_name(i).decode(): i for i in range(lib.w4_num_schedules())}
+    shape = (64, 4096, 4096, w4.BF16, 128)
+    plain, epilogue = lib.w4_default_schedule(*shape), lib.w4_default_epilogue_schedule(*shape)
+    key = (w4.BF16, 33, 64, 4096, 4096, 128)
+    other = index["tc256p_dp"]
+    assert other not in (plain, epilogue)
+    assert lib.w4_override_schedule(*key, other) == w4.OK
+    assert lib.w4_default_schedule(*shape) == other
+    assert lib.w4_default_epilogue_schedule(*shape) == epilogue
+    pair = "Lb1ELb1E"  # tc_gemm_kernel<mode, MMA2, PAIR, LEAN, ..>
+    M, N, K, at, gs = shape
+    assert pair in _launched(rec, M, N, K, at, gs)
+    assert pair not in _launched(rec, M, N, K, at, gs, act=w4.ACT_SILU)
+    assert lib.w4_override_epilogue_schedule(*key, index["tc16_sk"]) == w4.OK
+    assert lib.w4_default_schedule(*shape) == other
+    assert lib.w4_default_epilogue_schedule(*shape) == index["tc16_sk"]
+    assert lib.w4_override_schedule(*key, -1) == w4.OK      # removed: the other stays
+    assert lib.w4_default_schedule(*shape) == plain
+    assert lib.w4_default_epilogue_schedule(*shape) == index["tc16_sk"]
+    assert lib.w4_override_epilogue_schedule(*key, index["ds8_sk"]) == w4.OK  # cannot run 64 rows
+    assert lib.w4_default_epilogue_schedule(*shape) == epilogue
+    assert lib.w4_override_epilogue_schedule(*key, -1) == w4.OK
+    assert lib.w4_override_epilogue_schedule(7, 1, 2, 8, 64, -1, 1) == w4.ERR_INVALID_ARGUMENT
+    assert lib.w4_override_epilogue_schedule(1, 1, 2, 8, 64, -1, 99) == w4.ERR_INVALID_ARGUMENT
+    # the built-in entries hold for both
+    big = (4096, 57344, 8192, w4.BF16, 128)
+    assert lib.w4_default_epilogue_schedule(*big) == lib.w4_default_schedule(*big) == other
+
+
+def test_the_binding_names_the_kind():
+    shape = (64, 4096, 14336, torch.bfloat16, 128)
+    plain, epilogue = w4.default_schedule(*shape), w4.default_schedule(*shape, epilogue=True)
+    try:
+        w4.override_schedule(torch.bfloat16, 64, 64, 4096, 14336, 128, "tc256_dp", epilogue=True)
+        assert w4.default_schedule(*shape) == plain
+        name = w4.schedule_names()[w4.default_schedule(*shape, epilogue=True)]
+        assert name == "tc256_dp"
+    finally:
+        w4.override_schedule(torch.bfloat16, 64, 64, 4096, 14336, 128, None, epilogue=True)
+    assert w4.default_schedule(*shape, epilogue=True) == epilogue
+
+
+@pytest.mark.gpu
+def test_autotune_of_an_epilogue_is_its_own(gpu_lib):
+    """Tuning a product with an epilogue leaves the plain product's choice,
+    the reverse too, and does not add into a residual that is the output."""
+    dev, M, N, K = "cuda:0", 48, 1024, 2048
+    g = torch.Generator(device=dev).manual_seed(1)
+    b = w4.prepack_B(torch.randint(-2**31, 2**31 - 1, (K // 8, N), generator=g, device=dev,
+                                   dtype=torch.int32), w4.UINT4B8, w4.KN_SEQ, K, N)
+    a = torch.randn(M, K, generator=g, device=dev).bfloat16()
+    s = torch.full((K // 128, N), 2.0**-7, device=dev).bfloat16()
+    h = torch.randn(M, N, generator=g, device=dev).bfloat16()
+    before = h.clone()
+    names = w4.schedule_names()
+    pick = lambda e: names[w4.default_schedule(M, N, K, torch.bfloat16, 128, epilogue=e)]
+    plain, epilogue = pick(False), pick(True)
+    kw = dict(scales=s, group_size=128, reps=3)
+    try:
+        times = w4.autotune(a, b, w4.UINT4B8, N, residual=h, out=h, **kw)
+        assert torch.equal(h, before)
+        assert pick(True) == min(times, key=times.get) and pick(False) == plain
+        w4.override_schedule(torch.bfloat16, M, M, N, K, 128, None, epilogue=True)
+        times = w4.autotune(a, b, w4.UINT4B8, N, **kw)
+        assert pick(False) == min(times, key=times.get) and pick(True) == epilogue
+    finally:
+        for e in (False, True):
+            w4.override_schedule(torch.bfloat16, M, M, N, K, 128, None, epilogue=e)
