@@ -219,7 +219,8 @@ typedef enum w4_act {
  * and a given schedule sums in the same order; beyond 16 rows the default
  * one is chosen by a rule of its own (the least estimated time;
  * w4_default_epilogue_schedule tells it, w4_override_epilogue_schedule
- * changes it).  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
+ * changes it; W4A16 up to 32 rows stays on the schedules that round no
+ * dequantized weight where w4_gemm_bias does).  Errors as w4_gemm_bias, plus INVALID_ARGUMENT for a bad act,
  * an odd N with gated, an epilogue on the raw int32 output, a residual not
  * aligned to 2 bytes or one that overlaps out without being out.  With
  * K == 0 the product is 0. */

@@ -534,7 +534,8 @@ int default_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs,
 // where their last contributor adds the others' partial sums, a time per slot
 // (and drains that take longer with taller tiles); where tc_reduce_kernel adds
 // them, its launch, a time per slot and one per megabyte of partial sums.
-// W4A8 also takes the pass that stages its activations.  The constants
+// W4A8 also takes the pass that stages its activations.  (W4A16 up to 32 rows:
+// among the decode schedules, see keeps_weights.)  The constants
 // (microseconds) are fitted to timings of every schedule at 7000 shapes (bf16
 // g128 and per-channel, int8 per-channel and g128, E4M3; M 17..4096, N
 // 256..57344, K 512..28672).  On 1750 other shapes of more than 16 rows, drawn
@@ -623,6 +624,14 @@ int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs
     const auto it = cache.find(key);
     if (it != cache.end()) return it->second;
   }
+  // W4A16: the decode schedules scale sums in fp32, the tensor-core ones round
+  // each dequantized weight to 16 bits (bf16 24 x 57344 x 8192: relative error
+  // 0.0017 and 0.0022).  Where the plain product does not round them, a residual
+  // or an activation does not make it do so, although that is faster on large
+  // weights (that shape 140 us on ds32_sk, 115 on tc32_sk; 19 x 14576 x 19584 83
+  // and 71; 32 x 23904 x 20608 per channel 112 and 115; 18 x 18256 x 896 14 and
+  // 18): a caller who wants it says so (schedule, or an override).
+  const bool keeps_weights = mode != kW4A8 && mode != kW4A8F8 && kSchedules[plain].engine != kEngineTc;
   int best = plain;
   double best_us = 1e30;
   for (int si = 1; si < kNumSchedules; ++si) {
@@ -632,6 +641,7 @@ int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs
                            ? sc.nt == 1 && sc.decomp != kSplitK
                            : sc.bm == 32 && (sc.engine == kEngineGv || sc.engine == kEngineDs);
     if (!takes || !schedule_fits(si, mode, M, N, K, gs, has_sg)) continue;
+    if (keeps_weights && sc.engine == kEngineTc) continue;
     const double us = estimated_us(si, mode, M, N, K, gs);
     if (us < best_us) {
       best_us = us;

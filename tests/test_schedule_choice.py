@@ -1,4 +1,7 @@
 """Which schedule a product takes by default, with and without an epilogue."""
+import math
+import random
+
 import pytest
 import torch
 
@@ -100,3 +103,54 @@ def test_autotune_of_an_epilogue_is_its_own(gpu_lib):
     finally:
         for e in (False, True):
             w4.override_schedule(torch.bfloat16, M, M, N, K, 128, None, epilogue=e)
+
+
+def test_an_epilogue_rounds_no_weight_that_the_product_does_not():
+    """W4A16: the decode schedules take the weights as they are and scale sums
+    in fp32, the tensor-core ones round each dequantized weight to 16 bits.  A
+    product that runs on the former runs there with an epilogue too."""
+    names = w4.schedule_names()
+    rng = random.Random(3)
+    w4.load()
+    shapes = [(24, 57344, 8192), (18, 18256, 896), (17, 8960, 512)]
+    for _ in range(600):
+        shapes.append((rng.randint(1, 40), 8 * int(math.exp(rng.uniform(2, math.log(7168)))),
+                       128 * int(math.exp(rng.uniform(1, math.log(224))))))
+    decode = 0
+    for M, N, K in shapes:
+        for dt in (torch.float16, torch.bfloat16):
+            for gs in (-1, 128):
+                plain, ep = (names[w4.default_schedule(M, N, K, dt, gs, epilogue=e)]
+                             for e in (False, True))
+                if not plain.startswith("tc"):
+                    assert not ep.startswith("tc"), (M, N, K, dt, gs, plain, ep)
+                    decode += 1
+    assert decode > 1000
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(17, 8960, 512), (18, 18256, 896), (19, 14576, 19584)])
+def test_an_epilogue_keeps_the_products_accuracy(gpu_lib, M, N, K):
+    """bf16 products of 17 to 32 rows with scales of many bits, whose product
+    with a weight bf16 would round.  No weight is rounded, so what is left is
+    the output's one rounding (half an ulp of bf16, at most 2^-8 of it) and the
+    scales' and sums' fp32 arithmetic, far below."""
+    dev = "cuda:0"
+    g = torch.Generator(device=dev).manual_seed(4)
+    wq = torch.randint(-2**31, 2**31 - 1, (K // 8, N), generator=g, device=dev, dtype=torch.int32)
+    b = w4.prepack_B(wq, w4.UINT4B8, w4.KN_SEQ, K, N)
+    a = torch.randn(M, K, generator=g, device=dev).bfloat16()
+    s = ((torch.rand(K // 128, N, generator=g, device=dev) + 0.5) / (4.6 * K**0.5)).bfloat16()
+    r = torch.randn(M, N, generator=g, device=dev).bfloat16()
+    out = w4.gemm(a, b, w4.UINT4B8, N, scales=s, group_size=128, residual=r)
+    C = 256
+    sh = torch.arange(0, 32, 4, device=dev, dtype=torch.int32)
+    q = ((wq[:, None, :C] >> sh[None, :, None]) & 15).reshape(K, C).double() - 8
+    w = q * s[:, :C].double().repeat_interleave(128, 0)
+    ref = a.double() @ w + r[:, :C].double()
+    terms = a.double().abs() @ w.abs()
+    err = (out[:, :C].double() - ref).abs()
+    # rounded weights would be off by up to 2^-9 of the terms' sum, about
+    # 2^-9 sqrt(K) / K of it in the mean square; fp32 sums by K 2^-24
+    bound = 2.0**-8 * ref.abs() + (K + 64) * 2.0**-24 * terms
+    assert bool((err <= bound).all()), (err / bound).max().item()
