@@ -211,9 +211,10 @@ typedef enum w4_act {
  *   residual  array of out's type and shape, or NULL.  It may be out itself
  *             (the residual stream updated in place).
  * The tensor-core schedules' epilogue wants out, residual, bias and
- * ch_scales 16-byte aligned: without that the default rule runs the
- * CUDA-core schedule in their place, and an explicit one returns
- * UNSUPPORTED.
+ * ch_scales 16-byte aligned.  Without that an explicit one returns
+ * UNSUPPORTED, and the default rule takes a streamed or clustered schedule
+ * (up to 32 rows), else the CUDA-core one, which is slow: keep the arrays of
+ * larger products aligned.
  * With act NONE, gated 0 and residual NULL this is exactly w4_gemm_bias.
  * The schedules and workspace are those of w4_gemm for the same M, N and K,
  * and a given schedule sums in the same order; beyond 16 rows the default

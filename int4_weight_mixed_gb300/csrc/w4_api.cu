@@ -606,17 +606,24 @@ double estimated_us(int si, int mode, int64_t M, int64_t N, int64_t K, int64_t g
   return us + drains * kTcSplitDrain + kTcReduce + (slots + 1) * kTcReduceSlot + mb * kTcReduceMB;
 }
 
-int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg) {
+// aligned: whether the arrays are as the tensor-core schedules' epilogue wants
+// them (epilogue_aligned); the decode schedules' takes them by element.
+int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs, bool has_sg,
+                           bool aligned) {
+  const auto runs = [&](int si) {
+    return (aligned || kSchedules[si].engine != kEngineTc) &&
+           schedule_fits(si, mode, M, N, K, gs, has_sg);
+  };
   const int ov = override_for(mode, M, N, K, gs, true);
-  if (ov >= 0 && schedule_fits(ov, mode, M, N, K, gs, has_sg)) return ov;
+  if (ov >= 0 && runs(ov)) return ov;
   const int plain = rule_schedule(mode, M, N, K, gs, has_sg);
-  if (M <= 16 || kSchedules[plain].engine == kEngineSimt) return plain;
+  if ((M <= 16 && runs(plain)) || kSchedules[plain].engine == kEngineSimt) return plain;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     dev = -1;
   }
-  const auto key = std::make_tuple(mode, M, N, K, gs, has_sg, dev);
+  const auto key = std::make_tuple(mode, M, N, K, gs, has_sg, aligned, dev);
   static std::mutex mu;
   static std::map<decltype(key), int> cache;
   {
@@ -632,15 +639,15 @@ int epilogue_schedule_impl(int mode, int64_t M, int64_t N, int64_t K, int64_t gs
   // and 71; 32 x 23904 x 20608 per channel 112 and 115; 18 x 18256 x 896 14 and
   // 18): a caller who wants it says so (schedule, or an override).
   const bool keeps_weights = mode != kW4A8 && mode != kW4A8F8 && kSchedules[plain].engine != kEngineTc;
-  int best = plain;
-  double best_us = 1e30;
+  int best = runs(plain) ? plain : 0;
+  double best_us = HUGE_VAL;  // (above the estimate of a schedule that is a last resort)
   for (int si = 1; si < kNumSchedules; ++si) {
     const Schedule& sc = kSchedules[si];
     // one weight tile a CTA, stream-K or data-parallel; or 32-row decode
     const bool takes = sc.engine == kEngineTc
                            ? sc.nt == 1 && sc.decomp != kSplitK
                            : sc.bm == 32 && (sc.engine == kEngineGv || sc.engine == kEngineDs);
-    if (!takes || !schedule_fits(si, mode, M, N, K, gs, has_sg)) continue;
+    if (!takes || !runs(si)) continue;
     if (keeps_weights && sc.engine == kEngineTc) continue;
     const double us = estimated_us(si, mode, M, N, K, gs);
     if (us < best_us) {
@@ -839,7 +846,7 @@ int default_of(int64_t M, int64_t N, int64_t K, int a_type, int64_t group_size, 
   if (!valid_a_type(a_type)) return -1;
   if (a_type == W4_E4M3 && K % 128 != 0) return -1;
   const int64_t gs = group_size == -1 ? K : group_size;
-  return epilogue ? epilogue_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K)
+  return epilogue ? epilogue_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K, true)
                   : default_schedule_impl(mode_of(a_type), M, N, K, gs, gs != K);
 }
 
@@ -1024,7 +1031,8 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
   int si = schedule;
   const bool forced = schedule >= 0;
   if (!forced)
-    si = ep.any() ? epilogue_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg)
+    si = ep.any() ? epilogue_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg,
+                                           epilogue_aligned(ep, out, bias, ch_scales))
                   : default_schedule_impl(pr.mode, M, N, K, pr.gs, pr.has_sg);
   if (!schedule_fits(si, pr.mode, M, N, K, pr.gs, pr.has_sg))
     return fail(W4_ERR_UNSUPPORTED, "schedule %s cannot run this shape", kSchedules[si].name);
@@ -1035,13 +1043,10 @@ w4_status gemm_impl(const void* a, int a_type, int64_t M, int64_t K, const void*
       return fail(W4_ERR_UNSUPPORTED, "tensor-core schedules need 16-byte aligned inputs");
     si = 0;
   }
-  if (kSchedules[si].engine == kEngineTc && !epilogue_aligned(ep, out, bias, ch_scales)) {
-    if (forced)
-      return fail(W4_ERR_UNSUPPORTED,
-                  "the tensor-core schedules' epilogue needs 16-byte aligned out, residual, bias "
-                  "and channel scales");
-    si = 0;
-  }
+  if (kSchedules[si].engine == kEngineTc && !epilogue_aligned(ep, out, bias, ch_scales))
+    return fail(W4_ERR_UNSUPPORTED,  // (a given schedule: the rule picks another)
+                "the tensor-core schedules' epilogue needs 16-byte aligned out, residual, bias "
+                "and channel scales");
   if (!workspace) return fail(W4_ERR_WORKSPACE, "workspace is null");
   if (!aligned16(workspace)) return fail(W4_ERR_WORKSPACE, "workspace is not 16-byte aligned");
   const size_t need = ws_needed(si, pr);
@@ -1257,7 +1262,8 @@ struct DynLayout {
   bool prestage;    // tensor-core int8: the quantizer writes the bf16 copy
   size_t gemm_ws, codes, stok, total;
 };
-DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs, bool epilogue) {
+DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs, bool epilogue,
+                     bool aligned) {
   DynLayout d{};
   Problem pr{};
   pr.mode = mode_of(act_type);
@@ -1266,7 +1272,7 @@ DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs, 
   pr.K = K;
   pr.gs = gs;
   pr.has_sg = gs != K;
-  d.si = epilogue ? epilogue_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg)
+  d.si = epilogue ? epilogue_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg, aligned)
                   : default_schedule_impl(pr.mode, M, N, K, gs, pr.has_sg);
   d.prestage = pr.mode == kW4A8 && kSchedules[d.si].engine == kEngineTc && K % 8 == 0 &&
                K <= 32768;
@@ -1292,7 +1298,7 @@ size_t w4_gemm_dynamic_workspace_size(int64_t M, int64_t N, int64_t K, int act_t
   if (act_type == W4_E4M3 && K % 128 != 0) return kWsHeader;
   // the largest over the schedules the call may take (the default one),
   // with room for any schedule an override may name
-  const DynLayout d = dyn_layout(act_type, M, N, K, gs, false);
+  const DynLayout d = dyn_layout(act_type, M, N, K, gs, false, true);
   const size_t any = w4_gemm_workspace_size(M, N, K, act_type, group_size);
   const size_t extra = d.total - d.gemm_ws;
   return (any > d.gemm_ws ? align256(any) : d.gemm_ws) + extra;
@@ -1323,7 +1329,8 @@ w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const vo
   if (K == 0 || K % kStageK != 0 || (act_type == W4_E4M3 && K % 128 != 0))
     return fail(W4_ERR_UNSUPPORTED, "K must be a positive multiple of 64 (128 for fp8)");
   if (!workspace || !aligned16(workspace)) return fail(W4_ERR_WORKSPACE, "workspace is null or not 16-byte aligned");
-  const DynLayout d = dyn_layout(act_type, M, N, K, gs, ep.any());
+  const DynLayout d = dyn_layout(act_type, M, N, K, gs, ep.any(),
+                                 epilogue_aligned(ep, out, bias, ch_scales));
   if (workspace_bytes < d.total)
     return fail(W4_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, d.total);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1346,8 +1353,7 @@ w4_status dynamic_impl(const void* a, int a_type, int64_t M, int64_t K, const vo
   void* qdst = codes;
   int qout = act_type == W4_E4M3 ? 2 : 0;
   // the bf16 form is written from rows held in registers (16-byte loads)
-  const bool prestage =
-      d.prestage && aligned16(a) && epilogue_aligned(ep, out, bias, ch_scales);
+  const bool prestage = d.prestage && aligned16(a);
   if (prestage) {
     const TcPlan plan = make_plan(d.si, kW4A8, M, N, K, gs);
     qdst = ws + plan.ws_act;

@@ -154,3 +154,35 @@ def test_an_epilogue_keeps_the_products_accuracy(gpu_lib, M, N, K):
     # 2^-9 sqrt(K) / K of it in the mean square; fp32 sums by K 2^-24
     bound = 2.0**-8 * ref.abs() + (K + 64) * 2.0**-24 * terms
     assert bool((err <= bound).all()), (err / bound).max().item()
+
+
+UNALIGNED = {"out": dict(out=8 * P + 2), "residual": dict(residual=9 * P + 2),
+             "bias": dict(bias=9 * P + 2), "channel scales": dict(ch=6 * P + 4)}
+
+
+@pytest.mark.parametrize("what", list(UNALIGNED))
+@pytest.mark.parametrize("mode,M,N,K,gs", [
+    (w4.S8, 24, 4096, 14336, -1), (w4.S8, 32, 57344, 8192, -1), (w4.S8, 17, 8960, 512, 128),
+    (w4.E4M3, 24, 8192, 21760, -1), (w4.E4M3, 18, 1024, 512, -1), (w4.BF16, 24, 57344, 8192, 128),
+    (w4.F16, 31, 2048, 4096, -1), (w4.S8, 3, 4096, 4096, -1), (w4.E4M3, 9, 4096, 4096, -1)])
+def test_arrays_off_a_boundary_stay_off_the_cuda_cores(rec, mode, M, N, K, gs, what):
+    """Up to 32 rows there is a schedule whose epilogue goes by element."""
+    if what == "channel scales" and mode in (w4.F16, w4.BF16):
+        return
+    got = _launched(rec, M, N, K, mode, gs, act=w4.ACT_SILU, **UNALIGNED[what])
+    assert "simt" not in got and "tc_gemm" not in got, got
+    assert "ds_gemm" in got or "gv_gemm" in got
+
+
+def test_dynamic_products_off_a_boundary(rec):
+    """The same inside the call that quantizes, within its workspace."""
+    for act_type in (w4.S8, w4.E4M3):
+        for M, N, K in ((24, 4096, 14336), (24, 57344, 8192), (18, 1024, 512), (5, 4096, 4096)):
+            rec.reset()
+            ws = rec.lib.w4_gemm_dynamic_workspace_size(M, N, K, act_type, -1)
+            st = rec.lib.w4_gemm_dynamic_epilogue(
+                P, w4.F16, M, K, 3 * P, w4.INT4, N, 0, w4.S8, -1, 6 * P, act_type, 0, w4.ACT_SILU,
+                0, 9 * P + 2, 8 * P, 0, 0x40000000, ws, None)
+            assert st == w4.OK, rec.lib.w4_last_error()
+            got = " ".join(k for _, k in rec.launches())
+            assert "simt" not in got and ("ds_gemm" in got or "gv_gemm" in got), got
