@@ -235,12 +235,13 @@ struct Product {
     cols = gated ? N / 2 : N;
   }
   void sizes() const {
-    const int64_t n_groups = N * (gs == -1 || K == 0 ? 1 : gs > 0 ? K / gs : 0);
+    const int64_t n_groups = N * (gs == -1 ? 1 : gs > 0 ? K / gs : 0);
     if (M && static_cast<int64_t>(b->nbytes()) < (N + 127) / 128 * 64 * K)
       bad_value("b_packed is smaller than the prepacked " + std::to_string(K) + " x " +
                 std::to_string(N) + " weight");
-    if (scales) holds(scales, n_groups, scales->scalar_type(), "scales");
-    holds(zeros, n_groups, ot, "zeros");
+    // (over no K no scale is read, however many groups the array has)
+    if (scales && K) holds(scales, n_groups, scales->scalar_type(), "scales");
+    if (K) holds(zeros, n_groups, ot, "zeros");
     holds(s_tok, M, at::kFloat, "token_scales");
     holds(s_ch, N, at::kFloat, "channel_scales");
     holds(bias, N, ot, "bias");

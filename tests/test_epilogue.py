@@ -703,3 +703,21 @@ def test_binding_workspace_grows_and_capture_is_refused(gpu_lib):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gs,groups", [(128, 0), (128, 1), (-1, 1), (-1, 0)])
+def test_k_zero_with_the_scales_of_no_group(gpu_lib, gs, groups):
+    """A product over no K reads no scale: an array of K / group_size = 0 groups
+    is as good as one of one group, with an epilogue as without."""
+    N = 136
+    b = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    a = torch.empty(3, 0, dtype=torch.bfloat16, device=DEV)
+    s = torch.ones(groups, N, dtype=torch.bfloat16, device=DEV)
+    r = torch.randn(3, N, device=DEV).bfloat16()
+    z = torch.empty_like(s)
+    for kw in (dict(scales=s), dict(scales=s, zeros=z)):
+        plain = w4.gemm(a, b, w4.UINT4B8, N, group_size=gs, **kw)
+        assert torch.equal(plain, torch.zeros_like(r))
+        out = w4.gemm(a, b, w4.UINT4B8, N, group_size=gs, residual=r, **kw)
+        assert torch.equal(out, r)
