@@ -56,7 +56,7 @@ def build(force: bool = False) -> str:
 
 
 def load():
-    """Load libw4.so and the extension module (raises if not built)."""
+    """Load libw4.so (raises if it has not been built)."""
     global _lib
     if _lib is not None:
         return _lib
@@ -116,23 +116,28 @@ def load():
         lib.w4_status_string.argtypes = [i32]
         lib.w4_status_string.restype = ctypes.c_char_p
         lib.w4_last_error.restype = ctypes.c_char_p
-        _load_host()
         _lib = lib
         return lib
 
 
 def _load_host():
+    """The extension module, for the entry points that go through it (the norm,
+    products with an epilogue); the others need libw4.so alone."""
     global _host
-    path = _build_lib.HOST
-    if not os.path.exists(path):
-        raise RuntimeError(
-            f"w4_host.so not found at {path}: the binding's extension module is missing; "
-            "run __graft_entry__.build() or python -m int4_weight_mixed_gb300._build_lib")
-    spec = importlib.util.spec_from_file_location("w4_host", path)
-    host = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(host)
-    host.init(_ws_cache, _workspace, _check)
-    _host = host
+    load()
+    with _lock:
+        if _host is not None:
+            return
+        why = _build_lib.host_lacks()
+        if why:
+            raise RuntimeError(
+                f"w4_host.so {why}: run __graft_entry__.build() or "
+                "python -m int4_weight_mixed_gb300._build_lib")
+        spec = importlib.util.spec_from_file_location("w4_host", _build_lib.HOST)
+        host = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(host)
+        host.init(_ws_cache, _workspace, _check)
+        _host = host
 
 
 def status_string(status: int) -> str:
@@ -375,7 +380,7 @@ def gemm(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     """
     if act != ACT_NONE or gated or residual is not None:
         if _host is None:
-            load()
+            _load_host()
         args = (a, b_packed, wtype, N, scales, zeros, group_size, token_scales, channel_scales,
                 -1 if out_dtype is None else _DTYPE_CODE[out_dtype], out, ws, schedule, bias, act,
                 gated, residual)
@@ -430,7 +435,7 @@ def gemm_dynamic(a: torch.Tensor, b_packed: torch.Tensor, wtype: int, N: int,
     gemm()."""
     if act != ACT_NONE or gated or residual is not None:
         if _host is None:
-            load()
+            _load_host()
         args = (a, b_packed, wtype, N, _DTYPE_CODE[act_dtype], scales, group_size, channel_scales,
                 bias, out, token_scales_out, ws, act, gated, residual)
         done = _host.gemm_dynamic(*args)
@@ -509,7 +514,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e
     residual_out is x + residual, the residual stream after this addition.
     out and residual_out may be x or residual (in place)."""
     if _host is None:
-        load()
+        _load_host()
     args = (x, weight, eps, residual, out, None, residual_out, -1)
     done = _host.norm(*args)
     return done if done is not NotImplemented else _there(x.device, _host.norm, args)
@@ -527,7 +532,7 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
     if code is None:
         raise ValueError("act_dtype must be torch.int8 or torch.float8_e4m3fn")
     if _host is None:
-        load()
+        _load_host()
     args = (x, weight, eps, residual, out, scales, residual_out, code)
     done = _host.norm(*args)
     return done if done is not NotImplemented else _there(x.device, _host.norm, args)

@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libw4.so")
 HOST = os.path.join(BUILD, "w4_host.so")
+HOST_STAMP = os.path.join(BUILD, "w4_host.for")  # the torch and Python it was built for
 HOST_SOURCE = os.path.join(CSRC, "w4_host.cpp")
 SOURCES = ["w4_api.cu", "w4_kernels.cu", "w4_tc.cu", "w4_tc2.cu", "w4_tc3.cu", "w4_dk.cu", "w4_noalloc.cu",
            "w4_ds.cu", "w4_quant.cu", "w4_gv.cu", "w4_norm.cu",
@@ -33,9 +35,27 @@ def _nvcc() -> str:
     return cand
 
 
-def _newest_input() -> float:
-    paths = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
-    return max(os.path.getmtime(p) for p in paths + [HOST_SOURCE])
+def _newest(paths) -> float:
+    return max(os.path.getmtime(p) for p in paths)
+
+
+def _host_key() -> str:
+    """The extension module is compiled against torch's C++ classes: it is good
+    for the torch and the Python it was built with alone."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def host_lacks() -> str:
+    """What keeps the built extension module from being loaded, or ""."""
+    if not os.path.exists(HOST):
+        return f"is not built (no {HOST})"
+    try:
+        with open(HOST_STAMP) as f:
+            built = f.read()
+    except OSError:
+        built = "an unknown torch"
+    return "" if built == _host_key() else f"was built for {built}, this is {_host_key()}"
 
 
 def _torch_dir() -> str:
@@ -59,19 +79,9 @@ def _host_link(obj: str, out: str) -> list:
             "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    newest = _newest_input()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, HOST)):
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
+def _run(jobs, verbose: bool) -> None:
+    """Runs the compiler commands (name, command) side by side."""
     procs = []
-    objs = []
-    host_obj = os.path.join(BUILD, "w4_host.o")
-    jobs = [("w4_host.cpp", _host_compile(nvcc, host_obj))]
-    for src in SOURCES:
-        objs.append(os.path.join(BUILD, src.replace(".cu", ".o")))
-        jobs.append((src, [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", objs[-1]]))
     for src, cmd in jobs:
         if verbose:
             print(" ".join(cmd))
@@ -83,12 +93,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
             errors.append(f"{src}:\n{out.decode(errors='replace')}")
     if errors:
         raise RuntimeError("libw4 build failed\n" + "\n".join(errors))
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
-    tmp = HOST + ".tmp.%d" % os.getpid()
-    subprocess.check_call(_host_link(host_obj, tmp))
-    os.replace(tmp, HOST)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    headers = [os.path.join(CSRC, h) for h in HEADERS]
+    sources = [os.path.join(CSRC, s) for s in SOURCES]
+    fresh = lambda out, inputs: (not force and os.path.exists(out) and
+                                 os.path.getmtime(out) >= _newest(inputs))
+    lib = fresh(LIB, sources + headers)
+    host = fresh(HOST, headers + [HOST_SOURCE]) and not host_lacks()
+    if lib and host:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    nvcc = _nvcc()
+    objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
+    host_obj = os.path.join(BUILD, "w4_host.o")
+    jobs = []
+    if not host:
+        jobs.append(("w4_host.cpp", _host_compile(nvcc, host_obj)))
+    if not lib:
+        jobs += [(s, [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o])
+                 for s, o in zip(SOURCES, objs)]
+    _run(jobs, verbose)
+    if not lib:
+        tmp = LIB + ".tmp.%d" % os.getpid()
+        subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+    if not host:
+        if os.path.exists(HOST_STAMP):
+            os.remove(HOST_STAMP)
+        tmp = HOST + ".tmp.%d" % os.getpid()
+        subprocess.check_call(_host_link(host_obj, tmp))
+        os.replace(tmp, HOST)
+        with open(HOST_STAMP, "w") as f:
+            f.write(_host_key())
     return LIB
 
 

@@ -170,7 +170,7 @@ def tensor(*shape, code=2, bits=16):
     return torch._C._from_dlpack(capsule(ctypes.addressof(t), b"dltensor", None))
 
 
-w4.load()
+w4._load_host()
 x, b, s = tensor(4, 128), tensor(8192, code=1, bits=8), tensor(1, 128)
 assert x.device == torch.device("cuda", 1) and x.dtype == torch.float16
 for done in (w4._host.norm(x, None, 1e-6, x, None, None, None, -1),
