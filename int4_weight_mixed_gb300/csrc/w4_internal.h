@@ -141,7 +141,7 @@ struct EpArgs : TcArgs {
   const void* residual;  // [M][out columns] of the output type, or null; may be out itself
   int act;               // Act
   int gated;             // out[m][j] = act(v[m][2j]) * v[m][2j+1]: N / 2 output columns
-  int reduce;            // tc, one CTA a tile: tc_reduce_kernel follows
+  int reduce;            // tc: tc_reduce_kernel follows and adds the split tiles (tc_reduces)
 };
 
 // Skinny-M schedule (mma.sync, weights dequantized into register fragments).
