@@ -406,6 +406,107 @@ w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void
                      const void* weight, float eps, void* residual_out, void* y, int y_type,
                      float* y_scales, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged key-value cache in 8 bits and the attention over it: what stands
+ * between the product that makes queries, keys and values and the output
+ * product.  Codes and scales are those of the per-token quantization above
+ * ([PT], [QQQ]), one scale for each position and head.
+ *
+ * The cache: `pages` pages of page_size positions.  Codes of a page and head
+ * are contiguous.  Arrays on the device, owned by the caller:
+ *   k, v                [pages, heads, page_size, head_dim] codes of `type`
+ *                       (W4_S8 or W4_E4M3), 16-byte aligned
+ *   k_scales, v_scales  [pages, heads, page_size] fp32, 16-byte aligned
+ * page_size is a power of two, 16 at least; head_dim a multiple of 16 up to
+ * 256 (64 and 128 have the fast kernels). */
+typedef struct w4_kv_cache {
+  void *k, *v;
+  float *k_scales, *v_scales;
+  int64_t pages;
+  int heads, page_size, head_dim, type;
+} w4_kv_cache;
+
+/* The batch, the same for all four calls (device arrays, int32):
+ *   starts [sequences + 1]  sequence b has rows starts[b] .. starts[b+1] - 1
+ *                           of the call's row arrays; not decreasing
+ *   lens   [sequences]      its positions, those of its rows among them: row i
+ *                           of its n rows is position lens[b] - n + i
+ *   table  [sequences, table_width]  position p is slot p % page_size of page
+ *                           table[b][p / page_size]
+ * One row a sequence is a decode step, lens[b] rows a prompt, anything between
+ * a chunk of one; a batch may mix them.  The arrays are read on the device when
+ * the call runs there: a captured graph replays with what they then hold.
+ * Whatever they hold, no access leaves the arrays: starts count as at most the
+ * number of rows there are, lens as at most table_width * page_size, and a page
+ * outside [0, pages) as none.  Rows of no sequence are left as they were. */
+typedef struct w4_kv_batch {
+  const int32_t* table;
+  int64_t table_width;
+  const int32_t *starts, *lens;
+  int64_t sequences;
+} w4_kv_batch;
+
+/* Quantise the rows' keys and values into the cache:
+ *   scale = max_d |x[d]| / 127 (W4_S8) or / 448 (W4_E4M3),
+ *   code  = x[d] / scale, to the nearest integer / E4M3 value (as
+ *           w4_quantize_per_token and w4_quantize_per_token_fp8).
+ * A row of zeros, or with a scale below 2^-100, has scale 0 and codes 0; one
+ * that holds an infinity or a NaN scale NaN and codes 0 (what sees it is NaN).
+ *   k, v    [rows, heads, head_dim] of `type` (W4_F16 / W4_BF16), each row
+ *           contiguous, k_stride / v_stride elements from row to row: slices of
+ *           one product's rows need no copy.
+ * Rows with a position before 0 or no page are not written.  Two rows of a call
+ * must not share a page's slot (sequences that share pages may only write
+ * behind them).  Errors: INVALID_ARGUMENT (null, misaligned or negative,
+ * bad type, strides below heads * head_dim), UNSUPPORTED (page_size, head_dim,
+ * above 2^31 - 1 rows or 2^30 positions a sequence), CUDA. */
+w4_status w4_cache_write(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* k,
+                         const void* v, int type, int64_t rows, int64_t k_stride,
+                         int64_t v_stride, void* stream);
+
+/* Read the rows' keys and values back: k, v [rows, heads, head_dim] of `type`,
+ * contiguous, code * scale rounded once.  Rows without a position or page are
+ * zeros.  Errors as w4_cache_write, and outputs that overlap. */
+w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void* k, void* v,
+                        int type, int64_t rows, void* stream);
+
+/* Attention of the rows over their sequences' cached keys and values, those of
+ * the rows themselves (already written) among them:
+ *   out[i] = sum_j softmax_j(scale * q[i] . k[j]) v[j]
+ * over the keys j <= p that the row at position p sees: all (window <= 0), or
+ * those with j > p - window and the first `sinks`.  Query head h reads key head
+ * h / (heads / cache->heads).  A row that sees no key is zeros.
+ *   q    [rows, heads, head_dim] of `type` (W4_F16 / W4_BF16), q_stride
+ *        elements from row to row; out the same shape and type, contiguous.
+ *   scale  finite; usually 1 / sqrt(head_dim).
+ *   workspace  as w4_gemm's: w4_attention_workspace_size bytes at least,
+ *        16-byte aligned, zero-filled before its first use, not shared by calls
+ *        that overlap on the GPU; it may be the one of the products.
+ * Codes enter the products exactly and are scaled in fp32; scores, softmax
+ * statistics and sums are fp32, and the probabilities (of at most 1, times the
+ * value's scale over the row's largest) are rounded to fp16 before the product
+ * with the values.  Errors as w4_cache_write, plus INVALID_ARGUMENT
+ * for heads not a multiple of the cache's, a scale that is not finite, negative
+ * sinks, or out overlapping q; WORKSPACE. */
+size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim);
+w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
+                             int type, int64_t rows, int heads, int64_t q_stride, float scale,
+                             int window, int sinks, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The same for a tree of drafted tokens: a sequence's n rows are drafts, held by
+ * its last n positions in any order with parents before children or not, and
+ *   mask [rows, mask_width]  bytes: mask[i][t] != 0 where row i sees draft t of
+ *        its own sequence (itself and its ancestors); drafts from mask_width on
+ *        are not seen.
+ * Row i's position is that of the first draft plus the number of drafts it sees
+ * less one (its depth); it sees the keys before the drafts as above, and of the
+ * drafts those of its mask, whatever the window. */
+w4_status w4_tree_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
+                            const uint8_t* mask, int64_t mask_width, int type, int64_t rows,
+                            int heads, int64_t q_stride, float scale, int window, int sinks,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code; message of the last failed call on this
  * host thread ("" when none). */
 const char* w4_status_string(int status);

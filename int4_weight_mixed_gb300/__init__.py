@@ -18,6 +18,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -111,6 +112,17 @@ def load():
         lib.w4_quantize_per_token_fp8.restype = i32
         lib.w4_rmsnorm.argtypes = [p, i32, i64, i64, p, p, ctypes.c_float, p, p, i32, p, p]
         lib.w4_rmsnorm.restype = i32
+        lib.w4_cache_write.argtypes = [p, p, p, p, i32, i64, i64, i64, p]
+        lib.w4_cache_write.restype = i32
+        lib.w4_cache_read.argtypes = [p, p, p, p, i32, i64, p]
+        lib.w4_cache_read.restype = i32
+        lib.w4_attention_workspace_size.argtypes = [i32, i32, i32]
+        lib.w4_attention_workspace_size.restype = sz
+        attn_args = [i32, i64, i32, i64, ctypes.c_float, i32, i32, p, p, sz, p]
+        lib.w4_cache_attention.argtypes = [p, p, p] + attn_args
+        lib.w4_cache_attention.restype = i32
+        lib.w4_tree_attention.argtypes = [p, p, p, p, i64] + attn_args
+        lib.w4_tree_attention.restype = i32
         lib.w4_check_status.argtypes = [p, sz, p]
         lib.w4_check_status.restype = i32
         lib.w4_status_string.argtypes = [i32]
@@ -122,7 +134,8 @@ def load():
 
 def _load_host():
     """The extension module, for the entry points that go through it (the norm,
-    products with an epilogue); the others need libw4.so alone."""
+    products with an epilogue, the key-value cache); the others need libw4.so
+    alone."""
     global _host
     load()
     with _lock:
@@ -536,6 +549,102 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
     args = (x, weight, eps, residual, out, scales, residual_out, code)
     done = _host.norm(*args)
     return done if done is not NotImplemented else _there(x.device, _host.norm, args)
+
+
+class KVCache(NamedTuple):
+    """A paged key-value cache in 8 bits (w4_kv_cache): codes [pages, heads,
+    page_size, head_dim] int8 or float8_e4m3fn and one fp32 scale for each
+    position and head [pages, heads, page_size].  kv_cache() makes one.
+
+    The calls on it share the batch (w4_kv_batch), int32 tensors on its device:
+    starts [B + 1], sequence b's rows being starts[b] .. starts[b+1] - 1 of the
+    call's row arrays; lens [B], its positions, of which its rows are the last;
+    table [B, width], position p being slot p % page_size of page
+    table[b, p // page_size].  They are read when the call runs on the GPU."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def kv_cache(pages: int, heads: int, page_size: int, head_dim: int,
+             dtype: torch.dtype = torch.int8, device="cuda") -> KVCache:
+    """A cache of zeros: page_size a power of two from 16 on, head_dim a
+    multiple of 16 up to 256 (64 and 128 have the fast attention kernels)."""
+    if dtype not in _CODES8:
+        raise ValueError("dtype must be torch.int8 or torch.float8_e4m3fn")
+    codes = [torch.zeros(pages, heads, page_size, head_dim, dtype=torch.int8,
+                         device=device).view(dtype) for _ in range(2)]
+    scales = [torch.zeros(pages, heads, page_size, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales)
+
+
+def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                starts: torch.Tensor, lens: torch.Tensor) -> None:
+    """w4_cache_write: the rows' keys and values [rows, heads, head_dim] (fp16 /
+    bf16, slices of a product's rows) quantised into their positions."""
+    if _host is None:
+        _load_host()
+    args = (k, v, *cache, table, starts, lens)
+    if _host.cache_write(*args) is NotImplemented:
+        _there(k.device, _host.cache_write, args)
+
+
+def cache_read(cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+               rows: int, dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None,
+               v_out: torch.Tensor | None = None):
+    """w4_cache_read: the rows' keys and values as (k, v), [rows, heads,
+    head_dim] of dtype (fp16 / bf16).  starts = 0, lens[0], lens[0] + lens[1],
+    ... reads whole sequences."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+    if _host is None:
+        _load_host()
+    args = (*cache, table, starts, lens, rows, _DTYPE_CODE[dtype], k_out, v_out)
+    done = _host.cache_read(*args)
+    return done if done is not NotImplemented else _there(cache.k.device, _host.cache_read, args)
+
+
+def attention_workspace_size(heads: int, cache: KVCache) -> int:
+    """Bytes of ws that cache_attention and tree_attention need (for calls
+    captured in a CUDA graph, which pass one)."""
+    return int(load().w4_attention_workspace_size(heads, cache.k.shape[1], cache.k.shape[3]))
+
+
+def cache_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, starts: torch.Tensor,
+                    lens: torch.Tensor, scale: float | None = None, window: int = 0,
+                    sinks: int = 0, out: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None) -> torch.Tensor:
+    """w4_cache_attention: causal attention of the rows q [rows, heads,
+    head_dim] over their sequences in the cache (their own keys and values
+    written before), as [rows, heads, head_dim].  One row a sequence is a decode
+    step, all of them a prompt; a batch may mix any numbers.  window: keys a row
+    sees back from itself, itself among them (0: all); sinks: first keys that
+    stay visible to it.  scale: of the scores, 1 / sqrt(head_dim) by default."""
+    if _host is None:
+        _load_host()
+    args = (q, None, *cache, table, starts, lens, scale, window, sinks, out, ws)
+    done = _host.attention(*args)
+    return done if done is not NotImplemented else _there(q.device, _host.attention, args)
+
+
+def tree_attention(cache: KVCache, q: torch.Tensor, mask: torch.Tensor, table: torch.Tensor,
+                   starts: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+                   window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """w4_tree_attention: cache_attention for trees of drafted tokens.  A
+    sequence's rows are its drafts, held by its last positions; mask [rows,
+    drafts] (bool) says which drafts of its own sequence a row sees (itself and
+    its ancestors).  A window counts from the row's depth in the tree and hides
+    keys before the drafts only.  To keep an accepted path, write its keys and
+    values again at the positions they then have."""
+    if mask is None:
+        raise TypeError("mask must be a tensor")
+    if _host is None:
+        _load_host()
+    args = (q, mask, *cache, table, starts, lens, scale, window, sinks, out, ws)
+    done = _host.attention(*args)
+    return done if done is not NotImplemented else _there(q.device, _host.attention, args)
 
 
 def check_status(ws: torch.Tensor) -> int:

@@ -1285,6 +1285,103 @@ DynLayout dyn_layout(int act_type, int64_t M, int64_t N, int64_t K, int64_t gs, 
   return d;
 }
 
+// ------------------------------------------------- the key-value cache's calls
+constexpr int64_t kMaxPositions = int64_t{1} << 30;  // of a sequence: int32 with room
+
+// Checks what all four calls share and fills in their views.
+w4_status cache_views(const w4_kv_cache* cache, const w4_kv_batch* batch, int type, int64_t rows,
+                      CacheView& c, BatchView& b) {
+  if (!cache || !batch) return fail(W4_ERR_INVALID_ARGUMENT, "cache and batch are required");
+  if (type != W4_F16 && type != W4_BF16)
+    return fail(W4_ERR_INVALID_ARGUMENT, "type must be W4_F16 or W4_BF16");
+  if (cache->type != W4_S8 && cache->type != W4_E4M3)
+    return fail(W4_ERR_INVALID_ARGUMENT, "the cache's type must be W4_S8 or W4_E4M3");
+  if (rows < 0 || batch->sequences < 0 || batch->table_width < 0 || cache->pages < 0 ||
+      cache->heads <= 0 || cache->page_size <= 0 || cache->head_dim <= 0)
+    return fail(W4_ERR_INVALID_ARGUMENT, "negative size, or no heads, slots or dimensions");
+  if (cache->page_size < 16 || (cache->page_size & (cache->page_size - 1)) != 0)
+    return fail(W4_ERR_UNSUPPORTED, "page_size must be a power of two, 16 at least");
+  if (cache->head_dim % 16 != 0 || cache->head_dim > 256)
+    return fail(W4_ERR_UNSUPPORTED, "head_dim must be a multiple of 16 up to 256");
+  if (cache->heads > 65535 || cache->pages > 0x7fffffff || batch->sequences > 0x7ffffffe ||
+      rows > 0x7fffffff)
+    return fail(W4_ERR_UNSUPPORTED, "pages, sequences or rows above 2^31 - 1, or heads above 65535");
+  if (batch->table_width > kMaxPositions / cache->page_size)
+    return fail(W4_ERR_UNSUPPORTED, "more than 2^30 positions a sequence");
+  if (rows > 0 && batch->sequences > 0) {
+    if (!batch->starts || !batch->lens || (batch->table_width > 0 && !batch->table))
+      return fail(W4_ERR_INVALID_ARGUMENT, "starts, lens and table are required");
+    if (cache->pages > 0 && (!cache->k || !cache->v || !cache->k_scales || !cache->v_scales))
+      return fail(W4_ERR_INVALID_ARGUMENT, "a null array of the cache");
+  }
+  if (!aligned_to(batch->table, 4) || !aligned_to(batch->starts, 4) || !aligned_to(batch->lens, 4))
+    return fail(W4_ERR_INVALID_ARGUMENT, "starts, lens and table must be 4-byte aligned");
+  if (!aligned16(cache->k) || !aligned16(cache->v) || !aligned16(cache->k_scales) ||
+      !aligned16(cache->v_scales))
+    return fail(W4_ERR_INVALID_ARGUMENT, "the cache's arrays must be 16-byte aligned");
+  c.k = static_cast<uint8_t*>(cache->k);
+  c.v = static_cast<uint8_t*>(cache->v);
+  c.k_scales = cache->k_scales;
+  c.v_scales = cache->v_scales;
+  c.pages = cache->pages;
+  c.heads = cache->heads;
+  c.page_shift = 0;
+  while ((1 << c.page_shift) < cache->page_size) ++c.page_shift;
+  c.dim = cache->head_dim;
+  c.e4m3 = cache->type == W4_E4M3;
+  b.table = batch->table;
+  b.width = batch->table_width;
+  b.starts = batch->starts;
+  b.lens = batch->lens;
+  b.sequences = static_cast<int>(batch->sequences);
+  b.rows = static_cast<int>(rows);
+  return W4_OK;
+}
+
+w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
+                    const uint8_t* mask, int64_t mask_width, int type, int64_t rows, int heads,
+                    int64_t q_stride, float scale, int window, int sinks, void* out,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  AttnArgs a{};
+  w4_status st = cache_views(cache, batch, type, rows, a.c, a.b);
+  if (st != W4_OK) return st;
+  if (heads <= 0 || heads % cache->heads != 0)
+    return fail(W4_ERR_INVALID_ARGUMENT, "heads must be a multiple of the cache's");
+  if (!std::isfinite(scale)) return fail(W4_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (sinks < 0) return fail(W4_ERR_INVALID_ARGUMENT, "sinks must not be negative");
+  const int64_t dense = static_cast<int64_t>(heads) * cache->head_dim;
+  if (q_stride < dense && rows > 1)
+    return fail(W4_ERR_INVALID_ARGUMENT, "q_stride is below heads * head_dim");
+  if (rows * static_cast<int64_t>(heads) > (int64_t{1} << 30))
+    return fail(W4_ERR_UNSUPPORTED, "more than 2^30 rows times heads");
+  if (rows == 0 || batch->sequences == 0) return W4_OK;
+  if (!q || !out) return fail(W4_ERR_INVALID_ARGUMENT, "q and out are required");
+  if (!aligned_to(q, 2) || !aligned_to(out, 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "q or out is not aligned to its element size");
+  if (overlap(out, static_cast<size_t>(rows) * dense * 2, q,
+              (static_cast<size_t>(rows - 1) * q_stride + dense) * 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "out overlaps q");
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.bf16 = type == W4_BF16;
+  a.heads = heads;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.mask = mask;
+  a.mask_width = mask_width;
+  const size_t need = w4_attention_workspace_size(heads, cache->heads, cache->head_dim);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace))
+    return fail(W4_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is required", need);
+  a.status = static_cast<int*>(workspace);
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kWsHeader);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeader + kCounterBytes);
+  std::lock_guard<std::mutex> lock(enqueue_mutex(workspace));
+  const cudaError_t e = launch_attn_simt(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4_OK : cuda_fail(e, "attention launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -1515,6 +1612,68 @@ w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void
   a.eps = eps;
   cudaError_t e = launch_norm(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "norm launch");
+}
+
+w4_status w4_cache_write(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* k,
+                         const void* v, int type, int64_t rows, int64_t k_stride,
+                         int64_t v_stride, void* stream) {
+  CacheWriteArgs a{};
+  w4_status st = cache_views(cache, batch, type, rows, a.c, a.b);
+  if (st != W4_OK) return st;
+  const int64_t dense = static_cast<int64_t>(cache->heads) * cache->head_dim;
+  if ((k_stride < dense || v_stride < dense) && rows > 1)
+    return fail(W4_ERR_INVALID_ARGUMENT, "a row stride is below heads * head_dim");
+  if (rows == 0 || batch->sequences == 0) return W4_OK;
+  if (!k || !v) return fail(W4_ERR_INVALID_ARGUMENT, "k and v are required");
+  if (!aligned_to(k, 2) || !aligned_to(v, 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "k or v is not aligned to its element size");
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.bf16 = type == W4_BF16;
+  const cudaError_t e = launch_cache_write(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4_OK : cuda_fail(e, "cache write launch");
+}
+
+w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void* k, void* v,
+                        int type, int64_t rows, void* stream) {
+  CacheReadArgs a{};
+  w4_status st = cache_views(cache, batch, type, rows, a.c, a.b);
+  if (st != W4_OK) return st;
+  if (rows == 0 || batch->sequences == 0) return W4_OK;
+  if (!k || !v) return fail(W4_ERR_INVALID_ARGUMENT, "k and v are required");
+  if (!aligned_to(k, 2) || !aligned_to(v, 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "k or v is not aligned to its element size");
+  const size_t bytes = static_cast<size_t>(rows) * cache->heads * cache->head_dim * 2;
+  if (overlap(k, bytes, v, bytes)) return fail(W4_ERR_INVALID_ARGUMENT, "k and v overlap");
+  a.k = k;
+  a.v = v;
+  a.bf16 = type == W4_BF16;
+  const cudaError_t e = launch_cache_read(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? W4_OK : cuda_fail(e, "cache read launch");
+}
+
+size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim) {
+  return kWsHeader + kCounterBytes;
+}
+
+w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
+                             int type, int64_t rows, int heads, int64_t q_stride, float scale,
+                             int window, int sinks, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return attention(cache, batch, q, nullptr, 0, type, rows, heads, q_stride, scale, window, sinks,
+                   out, workspace, workspace_bytes, stream);
+}
+
+w4_status w4_tree_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
+                            const uint8_t* mask, int64_t mask_width, int type, int64_t rows,
+                            int heads, int64_t q_stride, float scale, int window, int sinks,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (mask_width < 0) return fail(W4_ERR_INVALID_ARGUMENT, "negative mask_width");
+  if (!mask && rows > 0) return fail(W4_ERR_INVALID_ARGUMENT, "mask is required");
+  return attention(cache, batch, q, mask, mask_width, type, rows, heads, q_stride, scale, window,
+                   sinks, out, workspace, workspace_bytes, stream);
 }
 
 w4_status w4_check_status(void* workspace, size_t workspace_bytes, void* stream) {

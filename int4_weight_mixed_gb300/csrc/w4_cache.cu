@@ -1,0 +1,237 @@
+// w4_cache.cu — the paged key-value cache: rows of keys and values quantised as
+// they are written (w4_cache_write), and read back as 16-bit rows
+// (w4_cache_read).  One scale per position and head, from that row's own
+// values, as the per-token activations have (vLLM PR #6547 "Enable Dynamic Per
+// Token fp8"; pytorch/ao PR #1113: symmetric int8):
+//
+//   scale = max_d |x[d]| / 127 (int8) or / 448 (E4M3), one fp32 rounding;
+//   code  = x[d] / scale rounded once to fp32, then to the nearest integer /
+//           E4M3 value, ties to even;
+//   read  = code * scale in fp32, rounded once to fp16 / bf16.
+//
+// Both are bound by HBM: 3 bytes a value and 8 bytes a row and head.  Eight
+// values a lane: 16 bytes of them, 8 bytes of codes; a head's row is a group of
+// dim / 8 lanes, and consecutive groups of a warp take consecutive heads of a
+// row, which are contiguous on the 16-bit side.
+#include "w4_cache.cuh"
+#include "w4_quant.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kCacheThreads = 256;
+constexpr int kCacheWarps = kCacheThreads / 32;
+constexpr int kMaxRows = 16;  // rows a CTA takes
+
+// A row that has no place: its position is before the first, or its page is
+// none of the cache's; and a row of no sequence.
+constexpr int64_t kNoPlace = -1, kNoSequence = -2;
+
+// The place of each of the CTA's rows.
+__device__ __forceinline__ void find_places(const CacheView& c, const BatchView& b, int row0,
+                                            int rows, int64_t* at) {
+  for (int r = threadIdx.x >> 5; r < rows; r += kCacheWarps) {
+    const int row = row0 + r;
+    const int i = find_sequence(b, row);
+    int64_t p = kNoSequence;
+    if (i < b.sequences) {
+      const Sequence s = sequence(c, b, i);
+      if (row >= s.row0 && row < s.row0 + s.n) {
+        const int pos = s.prefix + (row - s.row0);
+        p = pos >= 0 ? place(c, b, i, pos) : kNoPlace;
+      }
+    }
+    if ((threadIdx.x & 31) == 0) at[r] = p;
+  }
+}
+
+// Eight 16-bit values; 16 bytes at once where every row allows it.
+template <typename T>
+__device__ __forceinline__ uint4 load8(const T* p, bool vec) {
+  if (vec) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[2 * i]) |
+           static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[2 * i + 1]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// max |x|, NaN where there is one
+template <typename T>
+__device__ __forceinline__ float amax_nan(const uint4& v);
+template <>
+__device__ __forceinline__ float amax_nan<__half>(const uint4& v) {
+  const __half2* h = reinterpret_cast<const __half2*>(&v);
+  const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+  return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+template <>
+__device__ __forceinline__ float amax_nan<__nv_bfloat16>(const uint4& v) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                       __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+  return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// lanes: lanes of a row (a power of two); dim / 8 of them have values
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+    cache_write_kernel(CacheWriteArgs a, int rows, int lanes, int vec) {
+  __shared__ int64_t at[kMaxRows];
+  const int row0 = blockIdx.x * rows;
+  const int count = min(rows, a.b.rows - row0);
+  find_places(a.c, a.b, row0, count, at);
+  __syncthreads();
+  const int H = a.c.heads, D = a.c.dim;
+  const int groups = kCacheThreads / lanes;
+  const int d = 8 * (threadIdx.x & (lanes - 1));
+  const int items = count * 2 * H;
+  // (every thread of a warp makes every turn: the shuffles take whole warps)
+  const int turns = (items + groups - 1) / groups;
+  for (int turn = 0, it = threadIdx.x / lanes; turn < turns; ++turn, it += groups) {
+    const int r = it / (2 * H), kv = it / H & 1, h = it % H;
+    const bool mine = it < items && d < D;
+    const int64_t p = mine ? at[r] : kNoPlace;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (p >= 0) {
+      const T* src = static_cast<const T*>(kv ? a.v : a.k) +
+                     (row0 + r) * (kv ? a.v_stride : a.k_stride) + h * D + d;
+      x = load8(src, vec != 0);
+    }
+    // a NaN or an infinity survives as one larger than any number
+    float amax = amax_nan<T>(x);
+    if (!(amax < INFINITY)) amax = INFINITY;
+    for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (p < 0) continue;
+    float s = __fdiv_rn(amax, E4M3 ? 448.f : 127.f);
+    const bool live = s >= 0x1p-100f && amax < INFINITY;
+    if (!live) s = amax < INFINITY ? 0.f : NAN;
+    float f[8];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = pair_f32<T>(w[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+    uint2 o = make_uint2(0, 0);
+    if (live) {
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o.x |= code_e4m3(f[e], s) << (8 * e);
+          o.y |= code_e4m3(f[4 + e], s) << (8 * e);
+        }
+      } else {
+        float t[8];
+        codes8_s8(f, s, __frcp_rn(s), true, t);
+        o.x = pack4_s8(__float_as_int(t[0]), __float_as_int(t[1]), __float_as_int(t[2]),
+                       __float_as_int(t[3]));
+        o.y = pack4_s8(__float_as_int(t[4]), __float_as_int(t[5]), __float_as_int(t[6]),
+                       __float_as_int(t[7]));
+      }
+    }
+    const int64_t to = p + (static_cast<int64_t>(h) << a.c.page_shift);
+    *reinterpret_cast<uint2*>((kv ? a.c.v : a.c.k) + to * D + d) = o;
+    if (d == 0) (kv ? a.c.v_scales : a.c.k_scales)[to] = s;
+  }
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+    cache_read_kernel(CacheReadArgs a, int rows, int lanes, int vec) {
+  __shared__ int64_t at[kMaxRows];
+  const int row0 = blockIdx.x * rows;
+  const int count = min(rows, a.b.rows - row0);
+  find_places(a.c, a.b, row0, count, at);
+  __syncthreads();
+  const int H = a.c.heads, D = a.c.dim;
+  const int groups = kCacheThreads / lanes;
+  const int d = 8 * (threadIdx.x & (lanes - 1));
+  const int items = count * 2 * H;
+  if (d >= D) return;
+  for (int it = threadIdx.x / lanes; it < items; it += groups) {
+    const int r = it / (2 * H), kv = it / H & 1, h = it % H;
+    const int64_t p = at[r];
+    if (p == kNoSequence) continue;
+    uint2 c = make_uint2(0, 0);
+    float s = 0.f;
+    if (p >= 0) {
+      const int64_t from = p + (static_cast<int64_t>(h) << a.c.page_shift);
+      c = __ldg(reinterpret_cast<const uint2*>((kv ? a.c.v : a.c.k) + from * D + d));
+      s = __ldg((kv ? a.c.v_scales : a.c.k_scales) + from);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 v = codes2_f32<E4M3>((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
+      v.x *= s;
+      v.y *= s;
+      if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+        const __half2 y = __floats2half2_rn(v.x, v.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+      } else {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+    }
+    uint16_t* dst = static_cast<uint16_t*>(kv ? a.v : a.k) +
+                    (static_cast<int64_t>(row0 + r) * H + h) * D + d;
+    if (vec) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
+int lanes_of(int dim) {
+  int l = 2;
+  while (8 * l < dim) l *= 2;
+  return l;
+}
+// Rows a CTA takes: one while that leaves CTAs for every SM, so that a decode
+// batch is spread out; more for longer calls.
+int rows_of(int64_t rows) {
+  int r = 1;
+  while (r < kMaxRows && rows / r > 152 * 16) r *= 2;
+  return r;
+}
+bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s) {
+  if (a.b.rows == 0 || a.b.sequences == 0) return cudaSuccess;
+  const int rows = rows_of(a.b.rows), lanes = lanes_of(a.c.dim);
+  const int vec = aligned(a.k) && aligned(a.v) && a.k_stride % 8 == 0 && a.v_stride % 8 == 0;
+  const unsigned grid = static_cast<unsigned>((a.b.rows + rows - 1) / rows);
+  if (a.bf16) {
+    if (a.c.e4m3) cache_write_kernel<__nv_bfloat16, true><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+    else cache_write_kernel<__nv_bfloat16, false><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+  } else {
+    if (a.c.e4m3) cache_write_kernel<__half, true><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+    else cache_write_kernel<__half, false><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s) {
+  if (a.b.rows == 0 || a.b.sequences == 0) return cudaSuccess;
+  const int rows = rows_of(a.b.rows), lanes = lanes_of(a.c.dim);
+  const int vec = aligned(a.k) && aligned(a.v);
+  const unsigned grid = static_cast<unsigned>((a.b.rows + rows - 1) / rows);
+  if (a.bf16) {
+    if (a.c.e4m3) cache_read_kernel<__nv_bfloat16, true><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+    else cache_read_kernel<__nv_bfloat16, false><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+  } else {
+    if (a.c.e4m3) cache_read_kernel<__half, true><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+    else cache_read_kernel<__half, false><<<grid, kCacheThreads, 0, s>>>(a, rows, lanes, vec);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace w4

@@ -1,5 +1,5 @@
-// w4_host.cpp — the binding's per-call work for the norm and for products with
-// an epilogue of their own: checks of the tensors, outputs, the call into
+// w4_host.cpp — the binding's per-call work for the norm, for products with an
+// epilogue of their own and for the key-value cache: checks of the tensors, outputs, the call into
 // libw4.  The smallest of these calls are host time: a norm of one row takes
 // 1.5 us on the GPU, and the host 13.1 us a call when this work was Python's
 // and ctypes', 4.6 here (a gated product of one row 16.1 and 5.4; both with
@@ -16,6 +16,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
 
 #include "../../include/w4.h"
 
@@ -366,6 +368,235 @@ PyObject* gemm_dynamic(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// The key-value cache and the batch, from their tensors.
+struct Cached {
+  w4_kv_cache cache{};
+  w4_kv_batch batch{};
+  int64_t pages = 0, heads = 0, page = 0, dim = 0;
+
+  // o: k, v, k_scales, v_scales, table, starts, lens
+  void take(PyObject* const* o, c10::Device dev) {
+    static const char* const names[7] = {"cache.k",        "cache.v", "cache.k_scales",
+                                         "cache.v_scales", "table",   "starts",
+                                         "lens"};
+    const at::Tensor* t[7];
+    for (int i = 0; i < 7; ++i) {
+      t[i] = tensor(o[i], names[i]);
+      if (!t[i]) bad(PyExc_TypeError, std::string(names[i]) + " must be a tensor");
+      dense(t[i], dev, names[i]);
+    }
+    const at::ScalarType type = t[0]->scalar_type();
+    if (type != at::kChar && type != at::kFloat8_e4m3fn)
+      bad_value("cache.k must hold int8 or float8_e4m3fn codes");
+    if (t[0]->dim() != 4) bad_value("cache.k must be [pages, heads, page_size, head_dim]");
+    if (t[1]->scalar_type() != type || t[1]->sizes() != t[0]->sizes())
+      bad_value("cache.v must have cache.k's type and shape");
+    for (int i = 2; i < 4; ++i)
+      if (t[i]->scalar_type() != at::kFloat || t[i]->sizes() != t[0]->sizes().slice(0, 3))
+        bad_value(std::string(names[i]) + " must be fp32 [pages, heads, page_size]");
+    for (int i = 4; i < 7; ++i)
+      if (t[i]->scalar_type() != at::kInt) bad_value(std::string(names[i]) + " must be int32");
+    if (t[4]->dim() != 2) bad_value("table must be [sequences, pages of each]");
+    const int64_t B = t[4]->size(0);
+    holds(t[5], B + 1, at::kInt, "starts");
+    holds(t[6], B, at::kInt, "lens");
+    pages = t[0]->size(0);
+    heads = t[0]->size(1);
+    page = t[0]->size(2);
+    dim = t[0]->size(3);
+    if (heads > 0x7fffffff || page > 0x7fffffff || dim > 0x7fffffff)
+      bad_value("cache.k is too large");
+    cache.k = t[0]->data_ptr();
+    cache.v = t[1]->data_ptr();
+    cache.k_scales = static_cast<float*>(t[2]->data_ptr());
+    cache.v_scales = static_cast<float*>(t[3]->data_ptr());
+    cache.pages = pages;
+    cache.heads = static_cast<int>(heads);
+    cache.page_size = static_cast<int>(page);
+    cache.head_dim = static_cast<int>(dim);
+    cache.type = type == at::kChar ? W4_S8 : W4_E4M3;
+    batch.table = static_cast<const int32_t*>(t[4]->data_ptr());
+    batch.table_width = t[4]->size(1);
+    batch.starts = static_cast<const int32_t*>(t[5]->data_ptr());
+    batch.lens = static_cast<const int32_t*>(t[6]->data_ptr());
+    batch.sequences = B;
+  }
+};
+
+// Rows [T, heads, dim] whose own values are contiguous, a row any distance from
+// the next (a slice of a product's rows).
+int64_t row_stride(const at::Tensor& t, c10::Device dev, int64_t heads, int64_t dim,
+                   const char* name) {
+  const std::string n(name);
+  if (!t.is_cuda() || t.device() != dev)
+    bad_value(n + " must be a CUDA tensor on " + dev.str() + " (got " + t.device().str() + ")");
+  if (t.scalar_type() != at::kHalf && t.scalar_type() != at::kBFloat16)
+    bad_value(n + " must be fp16 or bf16 (got " + c10::toString(t.scalar_type()) + ")");
+  if (t.dim() != 3 || t.size(2) != dim || (heads >= 0 && t.size(1) != heads))
+    bad_value(n + " must be [rows, heads, head_dim] with the cache's head_dim" +
+              (heads >= 0 ? " and heads" : ""));
+  if ((dim != 1 && t.stride(2) != 1) || (t.size(1) != 1 && t.stride(1) != dim))
+    bad_value("a row of " + n + " must be contiguous");
+  const int64_t dense = t.size(1) * dim;
+  if (t.size(0) <= 1) return dense;
+  if (t.stride(0) < dense) bad_value("the rows of " + n + " overlap");
+  return t.stride(0);
+}
+
+// cache_write(k, v, cache.k, cache.v, cache.k_scales, cache.v_scales, table,
+// starts, lens)
+PyObject* cache_write(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  try {
+    if (nargs != 9) bad(PyExc_TypeError, "cache_write takes 9 arguments");
+    const at::Tensor *k = tensor(o[0], "k"), *v = tensor(o[1], "v");
+    if (!k || !v) bad(PyExc_TypeError, "k and v must be tensors");
+    const c10::Device dev = k->device();
+    Cached c;
+    c.take(o + 2, dev);
+    const int64_t ks = row_stride(*k, dev, c.heads, c.dim, "k");
+    const int64_t vs = row_stride(*v, dev, c.heads, c.dim, "v");
+    if (v->scalar_type() != k->scalar_type() || v->size(0) != k->size(0))
+      bad_value("v must have k's type and rows");
+    if (!is_current(dev)) Py_RETURN_NOTIMPLEMENTED;
+    void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    const void *pk = ptr(k), *pv = ptr(v);
+    const int code = code_of(k->scalar_type());
+    const int64_t T = k->size(0);
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = w4_cache_write(&c.cache, &c.batch, pk, pv, code, T, ks, vs, stream);
+    Py_END_ALLOW_THREADS
+    check(st, "w4_cache_write");
+    Py_RETURN_NONE;
+  } catch (const Bad&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// cache_read(cache.k, cache.v, cache.k_scales, cache.v_scales, table, starts,
+// lens, rows, code, k, v)
+PyObject* cache_read(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  try {
+    if (nargs != 11) bad(PyExc_TypeError, "cache_read takes 11 arguments");
+    const at::Tensor* held = tensor(o[0], "cache.k");
+    if (!held) bad(PyExc_TypeError, "cache.k must be a tensor");
+    const c10::Device dev = held->device();
+    Cached c;
+    c.take(o, dev);
+    const int64_t T = integer(o[7]);
+    if (T < 0) bad_value("rows must not be negative");
+    const int code = static_cast<int>(integer(o[8]));
+    const at::ScalarType type = type_of(code);
+    const at::Tensor* out[2] = {tensor(o[9], "k_out"), tensor(o[10], "v_out")};
+    for (int i = 0; i < 2; ++i)
+      if (out[i]) {
+        const char* const name = i ? "v_out" : "k_out";
+        dense(out[i], dev, name);
+        if (out[i]->scalar_type() != type || out[i]->sizes() != c10::IntArrayRef({T, c.heads, c.dim}))
+          bad_value(std::string(name) + " must be " + c10::toString(type) +
+                    " [rows, heads, head_dim]");
+      }
+    if (!is_current(dev)) Py_RETURN_NOTIMPLEMENTED;
+    at::Tensor made[2];
+    for (int i = 0; i < 2; ++i)
+      if (!out[i]) out[i] = &(made[i] = empty({T, c.heads, c.dim}, type, dev));
+    void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    void *const pk = out_ptr(out[0]), *const pv = out_ptr(out[1]);
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = w4_cache_read(&c.cache, &c.batch, pk, pv, code, T, stream);
+    Py_END_ALLOW_THREADS
+    check(st, "w4_cache_read");
+    PyObject* t = PyTuple_New(2);
+    if (!t) return nullptr;
+    for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(t, i, result(o[9 + i], *out[i]));
+    if (PyErr_Occurred()) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    return t;
+  } catch (const Bad&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// attention(q, mask, cache.k, cache.v, cache.k_scales, cache.v_scales, table,
+// starts, lens, scale (None: 1 / sqrt(head_dim)), window, sinks, out, ws); a
+// mask makes it a tree's
+PyObject* attention(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  try {
+    if (nargs != 14) bad(PyExc_TypeError, "attention takes 14 arguments");
+    const at::Tensor *q = tensor(o[0], "q"), *mask = tensor(o[1], "mask");
+    if (!q) bad(PyExc_TypeError, "q must be a tensor");
+    const c10::Device dev = q->device();
+    Cached c;
+    c.take(o + 2, dev);
+    const int64_t qs = row_stride(*q, dev, -1, c.dim, "q");
+    const int64_t T = q->size(0), heads = q->size(1);
+    if (heads > 0x7fffffff) bad_value("q has too many heads");
+    double scale = 0;
+    if (o[9] == Py_None) {
+      scale = 1 / std::sqrt(static_cast<double>(c.dim > 0 ? c.dim : 1));
+    } else {
+      scale = PyFloat_AsDouble(o[9]);
+      if (scale == -1.0 && PyErr_Occurred()) throw Bad();
+    }
+    const int64_t window = integer(o[10]), sinks = integer(o[11]);
+    if (window < 0 || sinks < 0) bad_value("window and sinks must not be negative");
+    // (no sequence has 2^31 positions: a wider window is none, more sinks are all)
+    const int w = window > 0x7fffffff ? 0 : static_cast<int>(window);
+    const int n_sinks = static_cast<int>(sinks > 0x7fffffff ? 0x7fffffff : sinks);
+    const at::Tensor *out = tensor(o[12], "out"), *ws = tensor(o[13], "ws");
+    if (mask) {
+      dense(mask, dev, "mask");
+      if ((mask->scalar_type() != at::kBool && mask->scalar_type() != at::kByte) ||
+          mask->dim() != 2 || mask->size(0) != T)
+        bad_value("mask must be bool [rows, drafts]");
+    }
+    dense(out, dev, "out");
+    dense(ws, dev, "ws");
+    if (out && (out->scalar_type() != q->scalar_type() || out->sizes() != q->sizes()))
+      bad_value("out must have q's type and shape");
+    if (!is_current(dev)) Py_RETURN_NOTIMPLEMENTED;
+    at::Tensor o_new, w_new;
+    if (!out) out = &(o_new = empty(q->sizes(), q->scalar_type(), dev));
+    void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    const void* const pq = ptr(q);
+    const uint8_t* const pm = static_cast<const uint8_t*>(ptr(mask));
+    const int64_t mw = mask ? mask->size(1) : 0;
+    void* const po = out_ptr(out);
+    const int code = code_of(q->scalar_type());
+    // (a mask of no drafts has no address: any will do, none is read)
+    const uint8_t none = 0;
+    int st;
+    for (int64_t bytes = 0;; bytes = static_cast<int64_t>(w4_attention_workspace_size(
+                                 static_cast<int>(heads), c.cache.heads, c.cache.head_dim))) {
+      if (!ws) w_new = workspace(o[0], dev, stream, bytes);
+      const at::Tensor& w8 = ws ? *ws : w_new;
+      void* const pw = out_ptr(&w8);
+      const size_t nw = static_cast<size_t>(w8.nbytes());
+      Py_BEGIN_ALLOW_THREADS
+      st = mask ? w4_tree_attention(&c.cache, &c.batch, pq, pm ? pm : &none, mw, code, T,
+                                    static_cast<int>(heads), qs, static_cast<float>(scale), w,
+                                    n_sinks, po, pw, nw, stream)
+                : w4_cache_attention(&c.cache, &c.batch, pq, code, T, static_cast<int>(heads), qs,
+                                     static_cast<float>(scale), w, n_sinks, po, pw, nw, stream);
+      Py_END_ALLOW_THREADS
+      if (st != W4_ERR_WORKSPACE || ws || bytes) break;
+    }
+    check(st, mask ? "w4_tree_attention" : "w4_cache_attention");
+    return result(o[12], *out);
+  } catch (const Bad&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 // init(ws_cache, workspace, check)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (nargs != 3) {
@@ -384,6 +615,12 @@ PyMethodDef methods[] = {
     {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm)), METH_FASTCALL, nullptr},
     {"gemm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm)), METH_FASTCALL, nullptr},
     {"gemm_dynamic", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gemm_dynamic)),
+     METH_FASTCALL, nullptr},
+    {"cache_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_write)),
+     METH_FASTCALL, nullptr},
+    {"cache_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_read)),
+     METH_FASTCALL, nullptr},
+    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)),
      METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "w4_host", nullptr, -1, methods};

@@ -249,4 +249,61 @@ int tc_max_stages(int bm, int nsub, int nt, int wblk);
 // Most co-resident two-CTA clusters of the pair kernel (-1 without a device).
 int tc_pair_clusters(int mode, size_t smem);
 
+// ---------------------------------------------------------------------------
+// The paged key-value cache (w4_cache.cu) and the attention over it
+// (w4_attn.cu, w4_attn_tc.cu).  Codes of a page and head are contiguous:
+// [pages][heads][page size][dim], scales [pages][heads][page size].
+struct CacheView {
+  uint8_t *k, *v;
+  float *k_scales, *v_scales;
+  int64_t pages;
+  int heads;
+  int page_shift;  // page size: a power of two, 16 at least
+  int dim;         // a multiple of 16 up to 256
+  int e4m3;        // codes: E4M3, else int8
+};
+// Sequence b: rows starts[b] .. starts[b + 1] - 1 are the last of its lens[b]
+// positions; position p is slot p % page of page table[b][p / page].
+struct BatchView {
+  const int32_t* table;
+  int64_t width;
+  const int32_t* starts;
+  const int32_t* lens;
+  int sequences;
+  int rows;  // of the arrays that the starts count
+};
+struct CacheWriteArgs {
+  CacheView c;
+  BatchView b;
+  const void *k, *v;  // [rows][heads][dim]
+  int64_t k_stride, v_stride;  // elements from row to row
+  int bf16;
+};
+struct CacheReadArgs {
+  CacheView c;
+  BatchView b;
+  void *k, *v;  // [rows][heads][dim], dense
+  int bf16;
+};
+struct AttnArgs {
+  CacheView c;
+  BatchView b;
+  const void* q;  // [rows][heads][dim]
+  int64_t q_stride;
+  void* out;      // [rows][heads][dim], dense
+  int bf16;
+  int heads;      // query heads: a multiple of the cache's
+  float scale;    // of q . k
+  int window;     // keys a row sees back from its position (0: all)
+  int sinks;      // first keys that a window leaves visible
+  const uint8_t* mask;  // tree of drafts: [rows][mask_width], else null
+  int64_t mask_width;
+  int* status;          // workspace: status word, counters, partial sums
+  int* counters;
+  float* partials;
+};
+cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s);
+cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
+
 }  // namespace w4
