@@ -1338,6 +1338,8 @@ w4_status cache_views(const w4_kv_cache* cache, const w4_kv_batch* batch, int ty
   return W4_OK;
 }
 
+bool attn_fast(int dim) { return dim == 64 || dim == 128; }
+
 w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
                     const uint8_t* mask, int64_t mask_width, int type, int64_t rows, int heads,
                     int64_t q_stride, float scale, int window, int sinks, void* out,
@@ -1367,7 +1369,7 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.bf16 = type == W4_BF16;
   a.heads = heads;
   a.scale = scale;
-  a.window = window;
+  a.window = window > 0 && window < kMaxPositions ? window : 0;
   a.sinks = sinks;
   a.mask = mask;
   a.mask_width = mask_width;
@@ -1378,7 +1380,9 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kWsHeader);
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeader + kCounterBytes);
   std::lock_guard<std::mutex> lock(enqueue_mutex(workspace));
-  const cudaError_t e = launch_attn_simt(a, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = attn_fast(cache->head_dim) ? launch_attn_dec(a, sm_count(), cs)
+                                                   : launch_attn_simt(a, cs);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "attention launch");
 }
 
@@ -1655,7 +1659,9 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
 }
 
 size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim) {
-  return kWsHeader + kCounterBytes;
+  size_t partials = 0;
+  if (attn_fast(head_dim)) partials = attn_dec_partials(sm_count(), head_dim);
+  return kWsHeader + kCounterBytes + partials;
 }
 
 w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,

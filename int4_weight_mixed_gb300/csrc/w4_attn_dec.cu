@@ -1,0 +1,587 @@
+// w4_attn_dec.cu — attention over the paged key-value cache for few rows a key
+// head (decode steps): bound by the bytes of the visible codes.
+//
+// A unit is 16 rows (query heads of a key head, of one token or a few) by the
+// key tiles they see; four warps of a CTA take 16 keys each of a 64-key tile.
+// mma.sync m16n8k16 in fp16, both kinds of codes being exact there:
+//
+//   t_j = (q . code_j) * (scale * log2 e * ks_j) + log2 vs_j
+//   p_j = 2^(t_j - m) <= 2^8,  m a running maximum of t
+//   O  += p_j * code_j (fp16 p, fp32 sums),  l += p_j / vs_j,  out = O / l
+//
+// with ks, vs the key's and value's scales: both enter the exponent, so the
+// codes go to the tensor cores as they are, and p is rounded to fp16 relative to
+// what it weighs, however far apart the values' scales are.  m moves only when a
+// row's maximum grows by more than 2^8 (sums are rescaled then).  Queries are
+// fp16 times a power of two of each row (bf16 ones fit: what falls below fp16's
+// subnormals is 2^-25 of the row's largest).
+//
+// Every warp streams its own keys through its own ring of shared memory
+// (cp.async, 16 bytes a lane) and meets the others only at the unit's end.
+// Positions are read in any order within an MMA, so that a lane loads 16
+// neighbouring codes at once: for scores they are consecutive k of its key's
+// row, for sums consecutive columns of its four keys, whose bytes PRMT pairs.
+// Slots behind the sequence's end and pages that are none arrive as zeros and
+// are never read: whatever they hold meets no arithmetic.
+#include <cuda_bf16.h>
+
+#include "w4_attn_plan.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kRows = 16;          // rows of a unit
+constexpr int kWarps = 4;
+constexpr int kKeys = 16;          // keys of a warp's stage
+constexpr int kTile = kKeys * kWarps;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kSlack = 8.f;      // log2 of how far p may exceed 1
+constexpr float kLeastScale = 0x1p-100f;
+
+template <int D>
+struct Ring {
+  static constexpr int kCodes = kKeys * D;                // bytes of one array
+  static constexpr int kStage = 2 * kCodes + 2 * kKeys * 4;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kWarp = kStage * kStages;
+};
+template <int D>
+constexpr size_t smem_bytes() {
+  constexpr size_t ring = static_cast<size_t>(Ring<D>::kWarp) * kWarps;
+  constexpr size_t sums = static_cast<size_t>(kWarps) * kRows * D * 4;
+  return ring > sums ? ring : sums;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Four codes as two pairs of fp16.  int8: 1024 + (code + 128) by its bits, less
+// 1152, exactly.
+template <bool E4M3>
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E4M3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    const uint32_t x = w ^ 0x80808080u;
+    const __half2 c = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t a = prmt(x, 0x64646464u, 0x4140), b = prmt(x, 0x64646464u, 0x4342);
+    const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), c);
+    const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), c);
+    lo = *reinterpret_cast<const uint32_t*>(&ha);
+    hi = *reinterpret_cast<const uint32_t*>(&hb);
+  }
+}
+
+// Where 16-byte chunk c of key `key` (of the stage's 16) lies within an array's
+// bytes, so that the lanes of a 16-byte (8-byte: values of 64) access hit
+// different banks: for keys, lanes 0-7 read four chunks of two neighbouring keys;
+// for values, two neighbouring chunks of every other key.
+template <int D>
+__device__ __forceinline__ uint32_t k_chunk(int key, int c) {
+  if constexpr (D == 128) return key * 128 + ((c ^ (key & 1) << 2) << 4);
+  else return key * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_chunk(int key, int c) {
+  if constexpr (D == 128) return key * 128 + ((c ^ (key & 7)) << 4);
+  else
+    return (key >> 1) * 128 + ((key ^ key >> 1) & 1) * 64 + ((c ^ (key >> 2 & 1) << 1) << 4);
+}
+// The place of 16-byte chunk c of a row of sums, by the same token (a lane's
+// columns are D / 8 neighbouring ones).
+template <int D>
+__device__ __forceinline__ int sum_chunk(int row, int c) {
+  const int x = D == 128 ? (c >> 3 & 3) | (row & 1) << 2 : (c >> 3 & 1) | (row & 1) << 1;
+  return row * (D / 4) + ((c & ~7) | ((c & 7) ^ x));
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int least) {
+  using R = Ring<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Piece piece;
+  __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
+  __shared__ int position[kRows];
+  __shared__ int last_one;
+  plan_piece<kRows, kTile, kThreads>(a, least, &piece);
+  if (piece.begin == piece.end) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int group = a.heads / a.c.heads;
+  const uint32_t ring = smem_addr(smem) + warp * R::kWarp;
+  const uint8_t* const ring_p = smem + warp * R::kWarp;
+  float4* const sums = reinterpret_cast<float4*>(smem);
+
+  Walk<kRows, kTile> w;
+  w.start(a, piece);
+  for (;;) {
+    const Sequence s = w.s;
+    const int r0 = w.rt * kRows, nr = min(kRows, s.n * group - r0);
+    // positions of the rows of a tree
+    if (a.mask) {
+      __syncthreads();
+      const int first = r0 / group, count = (r0 + nr - 1) / group - first + 1;
+      for (int i = warp; i < count; i += kWarps) {
+        const int p = draft_position(a, s, first + i);
+        if (lane == 0) position[i] = p;
+      }
+      __syncthreads();
+    }
+
+    // the two rows of this lane: what they see, their queries
+    int hi[2], lo[2];
+    const uint8_t* mask[2];
+    float rf[2];  // scale of a row's scores
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = g + 8 * e;
+      hi[e] = lo[e] = 0;
+      mask[e] = nullptr;
+      float x[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+      if (r < nr) {
+        const int token = (r0 + r) / group, head = w.h * group + (r0 + r) % group;
+        const int pos = a.mask ? position[token - r0 / group] : s.prefix + token;
+        const Visible v = visible(pos, a.mask ? s.len : min(s.len, pos + 1), a.window, a.sinks);
+        hi[e] = v.hi;
+        lo[e] = v.lo;
+        if (a.mask) mask[e] = a.mask + (static_cast<int64_t>(s.row0) + token) * a.mask_width;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                            (static_cast<int64_t>(s.row0) + token) * a.q_stride + head * D;
+        const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint16_t* from = q + 64 * j + 16 * t4 + 8 * i;
+            uint32_t u[4];
+            if (vec) {
+              const uint4 v4 = __ldg(reinterpret_cast<const uint4*>(from));
+              u[0] = v4.x, u[1] = v4.y, u[2] = v4.z, u[3] = v4.w;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                u[k] = static_cast<uint32_t>(from[2 * k]) | static_cast<uint32_t>(from[2 * k + 1]) << 16;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float2 f;
+              if (a.bf16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[k]));
+              else f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+              x[16 * j + 8 * i + 2 * k] = f.x;
+              x[16 * j + 8 * i + 2 * k + 1] = f.y;
+            }
+          }
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^up, with top * 2^up in [1, 2) (an infinity stays one)
+      const int E = __float_as_int(top) >> 23;
+      const int up = E == 255 ? 127 : min(max(254 - E, 1), 253);
+      const float grow = __int_as_float(up << 23);
+      rf[e] = a.scale * 1.44269504f * __int_as_float((254 - up) << 23);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int o = 16 * j + 4 * i;
+          const __half2 p0 = __floats2half2_rn(x[o] * grow, x[o + 1] * grow);
+          const __half2 p1 = __floats2half2_rn(x[o + 2] * grow, x[o + 3] * grow);
+          qf[4 * j + i][e] = *reinterpret_cast<const uint32_t*>(&p0);
+          qf[4 * j + i][2 + e] = *reinterpret_cast<const uint32_t*>(&p1);
+        }
+    }
+    // keys that every row sees: [lo_all, hi_all) and below `sinks`
+    int hi_all, lo_all;
+    if (a.mask) {
+      hi_all = s.prefix;
+      lo_all = a.window > 0 ? s.prefix + s.n - a.window : 0;
+    } else {
+      hi_all = min(s.len, s.prefix + r0 / group + 1);
+      lo_all = a.window > 0 ? s.prefix + (r0 + nr - 1) / group - a.window + 1 : 0;
+    }
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+
+    // this warp's keys of tile i: the page, looked up 32 tiles at a time
+    const int32_t* const line = a.b.table + w.b * a.b.width;
+    const auto look_up = [&](int i) -> int {
+      if (i >= w.to) return -1;
+      const int key = tile_at(w.t, i) * kTile + warp * kKeys;
+      if (key >= s.len) return -1;
+      const int page = __ldg(line + (key >> a.c.page_shift));
+      return page >= 0 && page < a.c.pages ? page : -1;
+    };
+    int pages = look_up(w.from + lane), pages_next = look_up(w.from + 32 + lane);
+    int base = w.from;  // tile of lane 0's page
+    const auto page_of = [&](int i) -> int {
+      const int d = i - base;
+      return d < 32 ? __shfl_sync(0xffffffffu, pages, d) : __shfl_sync(0xffffffffu, pages_next, d - 32);
+    };
+    const auto load = [&](int i, int slot) {
+      const int page = page_of(i);
+      if (page >= 0) {
+        const int key = tile_at(w.t, i) * kTile + warp * kKeys;
+        const int valid = min(s.len - key, kKeys);
+        const int64_t at = (((static_cast<int64_t>(page) * a.c.heads + w.h) << a.c.page_shift) +
+                            (key & ((1 << a.c.page_shift) - 1)));
+        const uint32_t dst = ring + slot * R::kStage;
+        const uint8_t *k = a.c.k + at * D, *v = a.c.v + at * D;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+          const int n = lane + 32 * u, row = n / (D / 16), c = n % (D / 16);
+          const uint32_t bytes = row < valid ? 16 : 0;
+          cp_async16(dst + k_chunk<D>(row, c), k + n * 16, bytes);
+          cp_async16(dst + R::kCodes + v_chunk<D>(row, c), v + n * 16, bytes);
+        }
+        if (lane < 8) {
+          const float* sc = (lane < 4 ? a.c.k_scales : a.c.v_scales) + at + 4 * (lane & 3);
+          cp_async16(dst + 2 * R::kCodes + lane * 16, sc, 4 * min(max(valid - 4 * (lane & 3), 0), 4));
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < R::kStages - 1; ++i) load(w.from + i, i);
+
+    int slot = 0;
+    for (int i = w.from; i < w.to; ++i) {
+      if (i - base >= 32) {
+        base += 32;
+        pages = pages_next;
+        pages_next = look_up(base + 32 + lane);
+      }
+      cp_async_wait<R::kStages - 2>();
+      __syncwarp();
+      // (asked for before this stage is used: its slot is the one left last)
+      load(i + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
+      const int page = page_of(i);
+      if (page >= 0) {
+        const uint8_t* const st = ring_p + slot * R::kStage;
+        const int key0 = tile_at(w.t, i) * kTile + warp * kKeys;
+        // scores: two blocks of eight keys
+        float c[2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(st + k_chunk<D>(8 * nt + g, 4 * j + t4));
+            const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t b0, b1;
+              codes4_f16<E4M3>(ww[q], b0, b1);
+              mma16816(c[nt], qf[4 * j + q], b0, b1);
+            }
+          }
+        }
+        // this lane's keys: 2 t4, 2 t4 + 1 of both blocks
+        const float* const ks = reinterpret_cast<const float*>(st + 2 * R::kCodes);
+        float rvs[4];
+        const bool all = key0 + kKeys <= hi_all &&
+                         (key0 >= lo_all || key0 + kKeys <= a.sinks);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int key = 8 * (n >> 1) + 2 * t4 + (n & 1);
+          const float vs = ks[kKeys + key];
+          const float kss = ks[key] + (vs - vs);  // NaN where the value's is
+          const float safe = fmaxf(vs, kLeastScale);
+          const float lvs = lg2(safe);
+          rvs[n] = rcp(safe);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = c[n >> 1][2 * e + (n & 1)];
+            x = fmaf(x * rf[e], kss, lvs);
+            if (!all) {
+              const int j = key0 + key;
+              bool see = j < hi[e];
+              if (mask[e] && j >= s.prefix)
+                see = see && j - s.prefix < a.mask_width && mask[e][j - s.prefix] != 0;
+              else
+                see = see && (j >= lo[e] || j < a.sinks);
+              if (!see) x = -INFINITY;
+            }
+          }
+        }
+        // the running maximum, of a row over its four lanes
+        float top[2], from[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[e] = fmaxf(fmaxf(c[0][2 * e], c[0][2 * e + 1]), fmaxf(c[1][2 * e], c[1][2 * e + 1]));
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float to = fmaxf(m[e], top[e]);
+            const float shrink = to == -INFINITY ? 1.f : ex2(m[e] - to);
+            m[e] = to;
+            l[e] *= shrink;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              o[d][2 * e] *= shrink;
+              o[d][2 * e + 1] *= shrink;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          from[e] = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            float& x = c[n >> 1][2 * e + (n & 1)];
+            x = ex2(x - from[e]);
+            l[e] = fmaf(x, rvs[n], l[e]);
+          }
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const __half2 h = __floats2half2_rn(c[nt][2 * e], c[nt][2 * e + 1]);
+            p[2 * nt + e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        // sums: columns D / 8 * g .. of the four keys
+        const uint8_t* const vp = st + R::kCodes;
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int key = 8 * (n >> 1) + 2 * t4 + (n & 1);
+          if constexpr (D == 128) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(vp + v_chunk<D>(key, g));
+            v[n][0] = w4.x, v[n][1] = w4.y, v[n][2] = w4.z, v[n][3] = w4.w;
+          } else {
+            const uint2 w2 = *reinterpret_cast<const uint2*>(vp + v_chunk<D>(key, g >> 1) + 8 * (g & 1));
+            v[n][0] = w2.x, v[n][1] = w2.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t sel = hf ? 0x7362 : 0x5140;
+            uint32_t b[2][2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+              codes4_f16<E4M3>(prmt(v[2 * nt][q], v[2 * nt + 1][q], sel), b[nt][0], b[nt][1]);
+            mma16816(o[4 * q + 2 * hf], p, b[0][0], b[1][0]);
+            mma16816(o[4 * q + 2 * hf + 1], p, b[0][1], b[1][1]);
+          }
+      }
+      slot = slot + 1 == R::kStages ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
+
+    // the four warps' sums, relative to the largest maximum
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (t4 == 0) {
+        part_m[warp][g + 8 * e] = m[e];
+        part_l[warp][g + 8 * e] = l[e];
+      }
+    }
+    __syncthreads();  // the rings are free
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = g + 8 * e;
+      if (row < nr) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q)
+            sums[warp * kRows * (D / 4) + sum_chunk<D>(row, (D / 32) * (2 * t4 + n) + q)] =
+                make_float4(o[4 * q][2 * e + n], o[4 * q + 1][2 * e + n], o[4 * q + 2][2 * e + n],
+                            o[4 * q + 3][2 * e + n]);
+      }
+    }
+    __syncthreads();
+    const int64_t u0 = w.unit_begin();
+    const int c0 = piece_of(piece.total, piece.pieces, u0);
+    const int c1 = piece_of(piece.total, piece.pieces, u0 + w.t.count - 1);
+    const bool whole = c0 == c1;
+    // partial sums of CTA c: slot 2 c where the unit began before its piece, 2 c + 1
+    // where it begins in it
+    constexpr int kSlot = kRows * D + 2 * kRows;  // floats
+    const auto slot_of = [&](int c) {
+      return a.partials + (2 * static_cast<int64_t>(c) + (c == c0)) * kSlot;
+    };
+    const auto store = [&](int r, int c, float4 y) {
+      const int token = (r0 + r) / group, head = w.h * group + (r0 + r) % group;
+      uint16_t* const to = static_cast<uint16_t*>(a.out) +
+                           ((static_cast<int64_t>(s.row0) + token) * a.heads + head) * D + 4 * c;
+      uint32_t u[2];
+      if (a.bf16) {
+        const __nv_bfloat162 p0 = __floats2bfloat162_rn(y.x, y.y), p1 = __floats2bfloat162_rn(y.z, y.w);
+        u[0] = *reinterpret_cast<const uint32_t*>(&p0);
+        u[1] = *reinterpret_cast<const uint32_t*>(&p1);
+      } else {
+        const __half2 p0 = __floats2half2_rn(y.x, y.y), p1 = __floats2half2_rn(y.z, y.w);
+        u[0] = *reinterpret_cast<const uint32_t*>(&p0);
+        u[1] = *reinterpret_cast<const uint32_t*>(&p1);
+      }
+      if ((reinterpret_cast<uintptr_t>(to) & 7) == 0) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+      }
+    };
+    for (int i = tid; i < nr * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = i % (D / 4);
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, part_m[k][r]);
+      const float from = top == -INFINITY ? 0.f : top;
+      float sum_l = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float f = ex2(part_m[k][r] - from);
+        const float4 x = sums[k * kRows * (D / 4) + sum_chunk<D>(r, c)];
+        sum_l = fmaf(f, part_l[k][r], sum_l);
+        y.x = fmaf(f, x.x, y.x);
+        y.y = fmaf(f, x.y, y.y);
+        y.z = fmaf(f, x.z, y.z);
+        y.w = fmaf(f, x.w, y.w);
+      }
+      if (whole) {
+        const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+        store(r, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+      } else {
+        float* const to = slot_of(blockIdx.x);
+        __stcg(reinterpret_cast<float4*>(to) + r * (D / 4) + c, y);
+        if (c == 0) __stcg(reinterpret_cast<float2*>(to + kRows * D) + r, make_float2(top, sum_l));
+      }
+    }
+    if (!whole) {
+      // the last of the unit's CTAs adds the partial sums, in their order
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int n = atomicAdd(a.counters + c0, 1);
+        last_one = n == c1 - c0;
+        if (last_one) a.counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (last_one) {
+        for (int i = tid; i < nr * (D / 4); i += kThreads) {
+          const int r = i / (D / 4), c = i % (D / 4);
+          float top = -INFINITY, sum_l = 0.f;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kAhead = 4;
+          for (int k0 = c0; k0 <= c1; k0 += kAhead) {
+            float4 x[kAhead];
+            float2 ml[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              ml[k] = make_float2(-INFINITY, 0.f);
+              x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k0 + k <= c1) {
+                const float* const at = slot_of(k0 + k);
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(at + kRows * D) + r);
+                x[k] = __ldcg(reinterpret_cast<const float4*>(at) + r * (D / 4) + c);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+              const float to = fmaxf(top, ml[k].x);
+              const float from = to == -INFINITY ? 0.f : to;
+              const float f = ex2(top - from), fk = ex2(ml[k].x - from);
+              top = to;
+              sum_l = sum_l * f + fk * ml[k].y;
+              y.x = y.x * f + fk * x[k].x;
+              y.y = y.y * f + fk * x[k].y;
+              y.z = y.z * f + fk * x[k].z;
+              y.w = y.w * f + fk * x[k].w;
+            }
+          }
+          const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+          store(r, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        }
+      }
+    }
+    if (!w.next(a)) break;
+    __syncthreads();  // the sums are read
+  }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
+  constexpr size_t smem = smem_bytes<D>();
+  const cudaError_t e = cudaFuncSetAttribute(attn_dec_kernel<D, E4M3>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  attn_dec_kernel<D, E4M3><<<ctas, kThreads, smem, s>>>(a, 2);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_dec_ctas(int sms) { return 3 * sms; }
+size_t attn_dec_partials(int sms, int dim) {
+  return 2 * static_cast<size_t>(attn_dec_ctas(sms)) * (kRows * dim + 2 * kRows) * sizeof(float);
+}
+
+cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s) {
+  const int ctas = attn_dec_ctas(sms);
+  if (a.c.dim == 128) return a.c.e4m3 ? launch<128, true>(a, ctas, s) : launch<128, false>(a, ctas, s);
+  return a.c.e4m3 ? launch<64, true>(a, ctas, s) : launch<64, false>(a, ctas, s);
+}
+
+}  // namespace w4

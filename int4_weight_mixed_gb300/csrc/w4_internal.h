@@ -305,5 +305,8 @@ struct AttnArgs {
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s);
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
+// Head dimensions 64 and 128; bytes of partial sums.
+size_t attn_dec_partials(int sms, int dim);
+cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s);
 
 }  // namespace w4

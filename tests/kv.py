@@ -126,7 +126,8 @@ def attention(q, cache, batch, window=0, sinks=0, mask=None, scale=None):
         added: 2^-25 max|q| sum|k| scale) and by |t| 2^-21 (its scaling, and the
         logarithm of the value's scale, in fp32);
       a probability is then off by twice the largest of these (numerator and
-        denominator), by 2^-20 (exponential, reciprocals, sums) and by half a
+        denominator), by 2^-17 (the logarithm of a value's scale, of magnitude up
+        to 2^5, by 2^-22 of itself; exponential, reciprocals, sums) and by half a
         step of fp16, 2^-11, or by 2^-25 of the row's largest probability times
         scale where fp16 has no more bits;
       the output is rounded by half a step of its type."""
@@ -162,7 +163,7 @@ def attention(q, cache, batch, window=0, sinks=0, mask=None, scale=None):
         o = torch.einsum("hgnk,hkd->hgnd", p, V)
         mag = torch.einsum("hgnk,hkd->hgnd", p, V.abs())
         worst = off.amax(-1, keepdim=True)
-        rel = 2 * worst + 2.0**-20 + 2.0**-11
+        rel = 2 * worst + 2.0**-17 + 2.0**-11
         # p' below fp16's normal range: 2^-25 of the largest p' = p * scale
         pg, sl = batch.slots(b, 0, k)
         vs = cache.v_scales[pg, :, sl].double().movedim(1, 0)[:, None, None]  # [Hkv,1,1,k]
