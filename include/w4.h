@@ -409,8 +409,8 @@ w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void
 /* ---------------------------------------------------------------------------
  * A paged key-value cache in 8 bits and the attention over it: what stands
  * between the product that makes queries, keys and values and the output
- * product.  Codes and scales are those of the per-token quantization above
- * ([PT], [QQQ]), one scale for each position and head.
+ * product.  Codes are symmetric with one scale for each position and head, from
+ * that row's own values, as in the per-token quantization above ([PT], [QQQ]).
  *
  * The cache: `pages` pages of page_size positions.  Codes of a page and head
  * are contiguous.  Arrays on the device, owned by the caller:
@@ -447,9 +447,10 @@ typedef struct w4_kv_batch {
 } w4_kv_batch;
 
 /* Quantise the rows' keys and values into the cache:
- *   scale = max_d |x[d]| / 127 (W4_S8) or / 448 (W4_E4M3),
- *   code  = x[d] / scale, to the nearest integer / E4M3 value (as
- *           w4_quantize_per_token and w4_quantize_per_token_fp8).
+ *   scale = max_d |x[d]| * r, r = 1 / 127 (W4_S8) or 1 / 448 (W4_E4M3), r and
+ *           the product each rounded once to fp32,
+ *   code  = x[d] / scale rounded once to fp32, then to the nearest integer /
+ *           E4M3 value, ties to even.
  * A row of zeros, or with a scale below 2^-100, has scale 0 and codes 0; one
  * that holds an infinity or a NaN scale NaN and codes 0 (what sees it is NaN).
  *   k, v    [rows, heads, head_dim] of `type` (W4_F16 / W4_BF16), each row

@@ -4,7 +4,8 @@
 // values, as the per-token activations have (vLLM PR #6547 "Enable Dynamic Per
 // Token fp8"; pytorch/ao PR #1113: symmetric int8):
 //
-//   scale = max_d |x[d]| / 127 (int8) or / 448 (E4M3), one fp32 rounding;
+//   scale = max_d |x[d]| * (1 / 127) (int8) or (1 / 448) (E4M3), the reciprocal
+//           and the product each rounded once to fp32;
 //   code  = x[d] / scale rounded once to fp32, then to the nearest integer /
 //           E4M3 value, ties to even;
 //   read  = code * scale in fp32, rounded once to fp16 / bf16.
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kCacheThreads)
     if (!(amax < INFINITY)) amax = INFINITY;
     for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (p < 0) continue;
-    float s = __fdiv_rn(amax, E4M3 ? 448.f : 127.f);
+    float s = __fmul_rn(amax, E4M3 ? 1.f / 448.f : 1.f / 127.f);
     const bool live = s >= 0x1p-100f && amax < INFINITY;
     if (!live) s = amax < INFINITY ? 0.f : NAN;
     float f[8];

@@ -17,7 +17,8 @@ def quantised(x, codes):
     x = x.float().numpy()
     with np.errstate(all="ignore"):
         top = np.abs(x).max(-1)
-        s = (top / np.float32(TOP[codes])).astype(np.float32)
+        s = top * (np.float32(1) / np.float32(TOP[codes]))
+        assert s.dtype == np.float32
         s = np.where(np.isfinite(top), np.where(s < np.float32(2.0**-100), np.float32(0), s),
                      np.float32(np.nan))
         q = np.where((s > 0)[..., None], x / s[..., None], np.float32(0)).astype(np.float32)
