@@ -22,8 +22,8 @@ HOST_STAMP = os.path.join(BUILD, "w4_host.for")  # the torch and Python it was b
 HOST_SOURCE = os.path.join(CSRC, "w4_host.cpp")
 SOURCES = ["w4_api.cu", "w4_kernels.cu", "w4_tc.cu", "w4_tc2.cu", "w4_tc3.cu", "w4_dk.cu", "w4_noalloc.cu",
            "w4_ds.cu", "w4_quant.cu", "w4_gv.cu", "w4_norm.cu",
-           "w4_tc_ep.cu", "w4_tc_ep2.cu", "w4_cache.cu", "w4_attn.cu", "w4_attn_dec.cu"]
-HEADERS = ["w4_internal.h", "w4_ptx.cuh", "w4_tc_kernel.cuh", "w4_epilogue.cuh", "w4_quant.cuh", "w4_cache.cuh", "w4_attn_plan.cuh", os.path.join("..", "..", "include", "w4.h")]
+           "w4_tc_ep.cu", "w4_tc_ep2.cu", "w4_cache.cu", "w4_attn.cu", "w4_attn_dec.cu", "w4_attn_tc.cu"]
+HEADERS = ["w4_internal.h", "w4_ptx.cuh", "w4_tc_kernel.cuh", "w4_epilogue.cuh", "w4_quant.cuh", "w4_cache.cuh", "w4_attn_plan.cuh", "w4_attn_math.cuh", os.path.join("..", "..", "include", "w4.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

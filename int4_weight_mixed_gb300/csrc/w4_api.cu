@@ -1381,8 +1381,12 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeader + kCounterBytes);
   std::lock_guard<std::mutex> lock(enqueue_mutex(workspace));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = attn_fast(cache->head_dim) ? launch_attn_dec(a, sm_count(), cs)
-                                                   : launch_attn_simt(a, cs);
+  // rows a key head and sequence has on average: up to one tile of the decode
+  // kernel's, more go to the tensor cores
+  const bool few = rows * heads <= 16 * batch->sequences * cache->heads;
+  const cudaError_t e = !attn_fast(cache->head_dim) ? launch_attn_simt(a, cs)
+                        : few                       ? launch_attn_dec(a, sm_count(), cs)
+                                                    : launch_attn_tc(a, sm_count(), cs);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "attention launch");
 }
 
@@ -1660,7 +1664,8 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
 
 size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim) {
   size_t partials = 0;
-  if (attn_fast(head_dim)) partials = attn_dec_partials(sm_count(), head_dim);
+  if (attn_fast(head_dim)) 
+    partials = std::max(attn_dec_partials(sm_count(), head_dim), attn_tc_partials(sm_count(), head_dim));
   return kWsHeader + kCounterBytes + partials;
 }
 

@@ -25,6 +25,7 @@
 // are never read: whatever they hold meets no arithmetic.
 #include <cuda_bf16.h>
 
+#include "w4_attn_math.cuh"
 #include "w4_attn_plan.cuh"
 
 namespace w4 {
@@ -35,8 +36,6 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 16;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kSlack = 8.f;      // log2 of how far p may exceed 1
-constexpr float kLeastScale = 0x1p-100f;
 
 template <int D>
 struct Ring {
@@ -69,47 +68,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Four codes as two pairs of fp16.  int8: 1024 + (code + 128) by its bits, less
-// 1152, exactly.
-template <bool E4M3>
-__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (E4M3) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {
-    const uint32_t x = w ^ 0x80808080u;
-    const __half2 c = __half2half2(__ushort_as_half(0x6480));  // 1152
-    const uint32_t a = prmt(x, 0x64646464u, 0x4140), b = prmt(x, 0x64646464u, 0x4342);
-    const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), c);
-    const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), c);
-    lo = *reinterpret_cast<const uint32_t*>(&ha);
-    hi = *reinterpret_cast<const uint32_t*>(&hb);
-  }
-}
-
 // Where 16-byte chunk c of key `key` (of the stage's 16) lies within an array's
 // bytes, so that the lanes of a 16-byte (8-byte: values of 64) access hit
 // different banks: for keys, lanes 0-7 read four chunks of two neighbouring keys;

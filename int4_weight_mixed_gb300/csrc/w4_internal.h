@@ -308,5 +308,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
 // Head dimensions 64 and 128; bytes of partial sums.
 size_t attn_dec_partials(int sms, int dim);
 cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s);
+size_t attn_tc_partials(int sms, int dim);
+cudaError_t launch_attn_tc(const AttnArgs& a, int sms, cudaStream_t s);
 
 }  // namespace w4
