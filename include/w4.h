@@ -480,7 +480,9 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  *   q    [rows, heads, head_dim] of `type` (W4_F16 / W4_BF16), q_stride
  *        elements from row to row; out the same shape and type, contiguous.
  *   scale  finite; usually 1 / sqrt(head_dim).
- *   workspace  as w4_gemm's: w4_attention_workspace_size bytes at least,
+ *   workspace  as w4_gemm's: w4_attention_workspace_size bytes at least (it goes
+ *        by the sizes in cache and batch and reads no array; with many rows it
+ *        includes up to 256 MB for 16-bit copies of the keys and values),
  *        16-byte aligned, zero-filled before its first use, not shared by calls
  *        that overlap on the GPU; it may be the one of the products.
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
@@ -489,7 +491,8 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  * with the values.  Errors as w4_cache_write, plus INVALID_ARGUMENT
  * for heads not a multiple of the cache's, a scale that is not finite, negative
  * sinks, or out overlapping q; WORKSPACE. */
-size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim);
+size_t w4_attention_workspace_size(const w4_kv_cache* cache, const w4_kv_batch* batch,
+                                   int64_t rows, int heads);
 w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
                              int type, int64_t rows, int heads, int64_t q_stride, float scale,
                              int window, int sinks, void* out, void* workspace,

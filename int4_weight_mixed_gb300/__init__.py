@@ -116,7 +116,7 @@ def load():
         lib.w4_cache_write.restype = i32
         lib.w4_cache_read.argtypes = [p, p, p, p, i32, i64, p]
         lib.w4_cache_read.restype = i32
-        lib.w4_attention_workspace_size.argtypes = [i32, i32, i32]
+        lib.w4_attention_workspace_size.argtypes = [p, p, i64, i32]
         lib.w4_attention_workspace_size.restype = sz
         attn_args = [i32, i64, i32, i64, ctypes.c_float, i32, i32, p, p, sz, p]
         lib.w4_cache_attention.argtypes = [p, p, p] + attn_args
@@ -605,10 +605,25 @@ def cache_read(cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: 
     return done if done is not NotImplemented else _there(cache.k.device, _host.cache_read, args)
 
 
-def attention_workspace_size(heads: int, cache: KVCache) -> int:
-    """Bytes of ws that cache_attention and tree_attention need (for calls
-    captured in a CUDA graph, which pass one)."""
-    return int(load().w4_attention_workspace_size(heads, cache.k.shape[1], cache.k.shape[3]))
+class _Cache(ctypes.Structure):  # w4_kv_cache
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")] + [
+        ("pages", ctypes.c_int64)] + [(n, ctypes.c_int) for n in ("heads", "page_size", "head_dim",
+                                                                  "type")]
+
+
+class _Batch(ctypes.Structure):  # w4_kv_batch
+    _fields_ = [("table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("sequences", ctypes.c_int64)]
+
+
+def attention_workspace_size(cache: KVCache, rows: int, heads: int, table: torch.Tensor) -> int:
+    """Bytes of ws that cache_attention and tree_attention of q [rows, heads,
+    head_dim] with this table need (for calls captured in a CUDA graph, which
+    pass one)."""
+    c = _Cache(None, None, None, None, *cache.k.shape, _DTYPE_CODE[cache.k.dtype])
+    b = _Batch(None, table.shape[1], None, None, table.shape[0])
+    return int(load().w4_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), rows, heads))
 
 
 def cache_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, starts: torch.Tensor,

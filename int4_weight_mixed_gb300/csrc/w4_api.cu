@@ -1338,7 +1338,40 @@ w4_status cache_views(const w4_kv_cache* cache, const w4_kv_batch* batch, int ty
   return W4_OK;
 }
 
-bool attn_fast(int dim) { return dim == 64 || dim == 128; }
+// Which kernel attends, and (tensor cores) whether the visible keys and values are
+// unpacked to 16 bits first, each tile of 128 keys once (tiles_each: tiles of a
+// sequence and key head), instead of by every unit of 256 rows that visits it.
+enum AttnEngine { kAttnSimt, kAttnDec, kAttnTc };
+struct AttnPlan {
+  AttnEngine engine;
+  int64_t tiles_each;
+  size_t partials, tiles;  // bytes
+};
+constexpr int64_t kMaxTileBytes = int64_t{256} << 20;
+AttnPlan attn_plan(const w4_kv_cache* cache, const w4_kv_batch* batch, int64_t rows, int heads) {
+  AttnPlan p{kAttnSimt, 0, 0, 0};
+  const int dim = cache->head_dim;
+  // (with no page there is no key, and the others load some key's row)
+  if ((dim != 64 && dim != 128) || cache->pages == 0 || cache->heads <= 0) return p;
+  const int sms = sm_count();
+  p.partials = std::max(attn_dec_partials(sms, dim), attn_tc_partials(sms, dim));
+  // rows of a sequence and key head, on average: up to one tile of the decode
+  // kernel's, more go to the tensor cores
+  const int64_t lines = batch->sequences * cache->heads;
+  const int64_t flat = rows * heads;
+  if (flat <= 16 * lines) {
+    p.engine = kAttnDec;
+    return p;
+  }
+  p.engine = kAttnTc;
+  const int64_t each = (batch->table_width * cache->page_size + 127) / 128;
+  if (flat >= 3 * 256 * lines && each > 0 && lines > 0 &&
+      each <= kMaxTileBytes / attn_tc_tile_bytes(dim) / lines) {
+    p.tiles_each = each;
+    p.tiles = static_cast<size_t>(each * lines * attn_tc_tile_bytes(dim));
+  }
+  return p;
+}
 
 w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,
                     const uint8_t* mask, int64_t mask_width, int type, int64_t rows, int heads,
@@ -1373,20 +1406,23 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.sinks = sinks;
   a.mask = mask;
   a.mask_width = mask_width;
-  const size_t need = w4_attention_workspace_size(heads, cache->heads, cache->head_dim);
+  const AttnPlan plan = attn_plan(cache, batch, rows, heads);
+  const size_t need = w4_attention_workspace_size(cache, batch, rows, heads);
   if (!workspace || workspace_bytes < need || !aligned16(workspace))
     return fail(W4_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is required", need);
-  a.status = static_cast<int*>(workspace);
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kWsHeader);
-  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeader + kCounterBytes);
+  char* const ws = static_cast<char*>(workspace);
+  a.status = reinterpret_cast<int*>(ws);
+  a.counters = reinterpret_cast<int*>(ws + kWsHeader);
+  a.partials = reinterpret_cast<float*>(ws + kWsHeader + kCounterBytes);
+  if (plan.tiles_each > 0) {
+    a.tiles = reinterpret_cast<uint8_t*>(ws + kWsHeader + kCounterBytes + align256(plan.partials));
+    a.tiles_each = plan.tiles_each;
+  }
   std::lock_guard<std::mutex> lock(enqueue_mutex(workspace));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  // rows a key head and sequence has on average: up to one tile of the decode
-  // kernel's, more go to the tensor cores
-  const bool few = rows * heads <= 16 * batch->sequences * cache->heads;
-  const cudaError_t e = !attn_fast(cache->head_dim) ? launch_attn_simt(a, cs)
-                        : few                       ? launch_attn_dec(a, sm_count(), cs)
-                                                    : launch_attn_tc(a, sm_count(), cs);
+  const cudaError_t e = plan.engine == kAttnSimt  ? launch_attn_simt(a, cs)
+                        : plan.engine == kAttnDec ? launch_attn_dec(a, sm_count(), cs)
+                                                  : launch_attn_tc(a, sm_count(), cs);
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "attention launch");
 }
 
@@ -1662,11 +1698,11 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
   return e == cudaSuccess ? W4_OK : cuda_fail(e, "cache read launch");
 }
 
-size_t w4_attention_workspace_size(int heads, int cache_heads, int head_dim) {
-  size_t partials = 0;
-  if (attn_fast(head_dim)) 
-    partials = std::max(attn_dec_partials(sm_count(), head_dim), attn_tc_partials(sm_count(), head_dim));
-  return kWsHeader + kCounterBytes + partials;
+size_t w4_attention_workspace_size(const w4_kv_cache* cache, const w4_kv_batch* batch,
+                                   int64_t rows, int heads) {
+  if (!cache || !batch) return kWsHeader + kCounterBytes;
+  const AttnPlan p = attn_plan(cache, batch, rows, heads);
+  return kWsHeader + kCounterBytes + align256(p.partials) + p.tiles;
 }
 
 w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,

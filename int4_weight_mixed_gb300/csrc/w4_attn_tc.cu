@@ -47,6 +47,12 @@ constexpr float kNoKey = -0x1p120f;
 // rows 80 bytes apart (16-byte accesses of eight rows hit different banks)
 constexpr int kOutRow = 80, kOutBytes = 32 * kOutRow;
 
+// Where codes become 16-bit values: by the CTA's own converter warps, tile by tile
+// (kOwn), or once for all units by attn_unpack_kernel, whose tiles a warp copies
+// (kTiles).  kUnpack: that kernel's use of the converters' code.
+enum Source { kOwn = 0, kTiles = 1, kUnpack = 2 };
+__host__ __device__ constexpr int tc_threads(int source) { return source == kTiles ? 320 : kTcCta; }
+
 template <int D>
 struct Tc {
   static constexpr int kStages = D == 128 ? 2 : 4;    // of K and of V
@@ -61,6 +67,8 @@ struct Tc {
   static constexpr int kOutAt = kFactorsAt + kSlots * kFactors;
   static constexpr int kBytes = kOutAt + 8 * kOutBytes;
   static constexpr int kSmem = kBytes + 1024;         // (for the alignment of the first)
+  // an unpacked tile in the workspace: K and V as in a stage, the factors
+  static constexpr int kRecord = 2 * kTileBytes + kFactors;
   // tensor memory columns: S (P in its first half) of both halves, then O
   static constexpr int kS = 0, kO = 2 * kTcKeys;
   // partial sums of a piece, in floats: [D / 4][rows] of 16 bytes, [rows] of (m, l)
@@ -190,14 +198,18 @@ __device__ __forceinline__ uint32_t below(int n) {
 }
 
 // ---------------------------------------------------------------- the roles
-template <int D, bool E4M3, bool BF16>
+template <int D, bool E4M3, bool BF16, int SOURCE>
 struct AttnTc {
   using T = Tc<D>;
   const AttnArgs& a;
   uint32_t base;  // shared address of the tiles
   uint32_t tmem;
+  uint8_t* record = nullptr;  // kUnpack: the tile's place in the workspace
 
   using Way = Walk<kTcRows, kTcKeys>;
+  static __device__ __forceinline__ void sts4(uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+  }
   static __device__ __forceinline__ TcShared& sh() { return tc_shared(); }
   static __device__ __forceinline__ Way& way() { return sh().ways[threadIdx.x >> 5]; }
   static __device__ __forceinline__ Way& way_next() { return sh().next[threadIdx.x >> 5]; }
@@ -380,7 +392,30 @@ struct AttnTc {
     asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
   }
-  static __device__ __forceinline__ int conv_warp() { return (threadIdx.x >> 5) - kConvWarp; }
+  static __device__ __forceinline__ int conv_warp() {
+    return (threadIdx.x >> 5) - (SOURCE == kUnpack ? 0 : kConvWarp);
+  }
+  // 16 bytes of a stage (of an unpacked tile) at offset `at` from base.
+  __device__ __forceinline__ void put(uint32_t at, const uint32_t (&o)[4]) const {
+    if constexpr (SOURCE == kUnpack)
+      *reinterpret_cast<uint4*>(record + at) = make_uint4(o[0], o[1], o[2], o[3]);
+    else
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]),
+                   "r"(o[2]), "r"(o[3])
+                   : "memory");
+  }
+  __device__ __forceinline__ void put_factors(uint32_t to, int key, bool none, float ks, float vs) const {
+    const uint32_t f = to + 16 * (key >> 1) + 4 * (key & 1);
+    const float x = none ? 0.f : (ks + (vs - vs)) * (a.scale * 1.44269504f);
+    const float y = none ? kNoKey : lg2(fmaxf(vs, kLeastScale));
+    if constexpr (SOURCE == kUnpack) {
+      *reinterpret_cast<float*>(record + f) = x;
+      *reinterpret_cast<float*>(record + f + 8) = y;
+    } else {
+      sts4(f, x);
+      sts4(f + 8, y);
+    }
+  }
   // This lane's key of turn u, and its first dimension.
   static __device__ __forceinline__ int k_key(int u) {
     return 16 * conv_warp() + 512 / D * u + ((threadIdx.x & 31) * 16 / D);
@@ -427,7 +462,8 @@ struct AttnTc {
     vs = __uint_as_float(load4(a.c.v_scales + (r < 0 ? 0 : r)));
     in |= r >= 0 ? 256u : 0u;
   }
-  __device__ __forceinline__ void store_k(uint32_t st, uint32_t (&c)[kTurns][4], uint32_t in) const {
+  // to: where the stage's K lies.
+  __device__ __forceinline__ void store_k(uint32_t to, uint32_t (&c)[kTurns][4], uint32_t in) const {
     if ((in & ((1u << kTurns) - 1)) != (1u << kTurns) - 1) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u)
@@ -436,7 +472,7 @@ struct AttnTc {
     // the lanes of the second 64 dimensions write their two chunks the other way
     // round: other banks than those of the first
     const int sub = k_dim() >> 6, ch = (k_dim() & 63) >> 3;
-    const uint32_t to = k_at(st) + sub * (kTcKeys * 128);
+    to += sub * (kTcKeys * 128);
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
       const int key = k_key(u);
@@ -454,10 +490,9 @@ struct AttnTc {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t at = to + key * 128 + (((ch + (e ^ sub)) ^ (key & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                     "r"(sub ? o[e ^ 1][0] : o[e][0]), "r"(sub ? o[e ^ 1][1] : o[e][1]),
-                     "r"(sub ? o[e ^ 1][2] : o[e][2]), "r"(sub ? o[e ^ 1][3] : o[e][3])
-                     : "memory");
+        const uint32_t y[4] = {sub ? o[e ^ 1][0] : o[e][0], sub ? o[e ^ 1][1] : o[e][1],
+                               sub ? o[e ^ 1][2] : o[e][2], sub ? o[e ^ 1][3] : o[e][3]};
+        put(at, y);
       }
     }
   }
@@ -474,7 +509,7 @@ struct AttnTc {
       else c[u][0] = load4(q);
     }
   }
-  __device__ __forceinline__ void store_v(uint32_t st, uint32_t (&c)[8][kVWords], int valid) const {
+  __device__ __forceinline__ void store_v(uint32_t to, uint32_t (&c)[8][kVWords], int valid) const {
     if (valid < 8) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
@@ -483,8 +518,8 @@ struct AttnTc {
           if (u >= valid) c[u][q] = 0;
     }
     const int lane = threadIdx.x & 31, kg = 2 * conv_warp() + (lane >> 4);
-    const uint32_t to = v_at(st) + (kg >> 3) * (D * 128) + (lane & 15) * 128 +
-                        (((kg & 7) ^ (lane & 7)) << 4);  // (row c + 16 e: its low bits are c's)
+    // (row c + 16 e: its low bits are c's)
+    to += (kg >> 3) * (D * 128) + (lane & 15) * 128 + (((kg & 7) ^ (lane & 7)) << 4);
 #pragma unroll
     for (int q = 0; q < kVWords; ++q)
 #pragma unroll
@@ -494,14 +529,8 @@ struct AttnTc {
         for (int p = 0; p < 4; ++p)
           codes4_f16<E4M3>(prmt(c[2 * p][q], c[2 * p + 1][q], hf ? 0x7362 : 0x5140), o[0][p], o[1][p]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (4 * q + 2 * hf + e) * 2048),
-                       "r"(o[e][0]), "r"(o[e][1]), "r"(o[e][2]), "r"(o[e][3])
-                       : "memory");
+        for (int e = 0; e < 2; ++e) put(to + (4 * q + 2 * hf + e) * 2048, o[e]);
       }
-  }
-  static __device__ __forceinline__ void sts4(uint32_t at, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
   }
   // What this warp wrote is there.  The fence that lets the tensor cores see it is the
   // issuing warp's, after its wait: here it would wait for the loads in flight
@@ -517,7 +546,6 @@ struct AttnTc {
     // Codes of K are loaded a tile before they are stored, pages before that; V
     // follows K by a tile.
     start();
-    const float to_log2 = a.scale * 1.44269504f;
     uint32_t ck[kTurns][4], cv[8][kVWords];
     float ks = 0.f, vs = 0.f;
     uint32_t in = 0;
@@ -551,13 +579,8 @@ struct AttnTc {
       if (kc < tiles) {
         const uint32_t st = kc % T::kStages, slot = kc % T::kSlots;
         if (!wait(sh().bar.k_empty[st], kc / T::kStages + 1)) return;
-        store_k(st, ck, in);
-        if (tid < kTcKeys) {
-          const uint32_t f = factors(slot) + 16 * (tid >> 1) + 4 * (tid & 1);
-          const bool none = !(in & 256u);
-          sts4(f, none ? 0.f : (ks + (vs - vs)) * to_log2);
-          sts4(f + 8, none ? kNoKey : lg2(fmaxf(vs, kLeastScale)));
-        }
+        store_k(k_at(st), ck, in);
+        if (tid < kTcKeys) put_factors(factors(slot), tid, !(in & 256u), ks, vs);
         done(sh().bar.k_full[st]);
         if (tid < kTcKeys && (tid & 31) == 0) mbar_arrive(&sh().bar.f_full[slot]);
         if (kc + 1 < tiles) {
@@ -569,11 +592,65 @@ struct AttnTc {
       if (kc > 0) {
         const uint32_t vc = kc - 1, st = vc % T::kStages;
         if (!wait(sh().bar.v_empty[st], vc / T::kStages + 1)) return;
-        store_v(st, cv, valid);
+        store_v(v_at(st), cv, valid);
         done(sh().bar.v_full[st]);
       }
       if (kc < tiles) load_v(before, cv, valid);
     }
+  }
+
+  // ---- kTiles: warp 8 copies the unpacked tiles instead
+  __device__ void copy() const {
+    Way& w = way();
+    start();
+    const uint32_t tiles = static_cast<uint32_t>(sh().piece.end - sh().piece.begin);
+    const uint8_t *now = nullptr, *before = nullptr;
+    int i = w.from;
+    for (uint32_t kc = 0; kc <= tiles; ++kc) {
+      before = now;
+      if (kc < tiles) {
+        if (kc > 0 && ++i >= w.to) {
+          next();
+          i = w.from;
+        }
+        now = a.tiles + ((static_cast<int64_t>(w.b) * a.c.heads + w.h) * a.tiles_each +
+                         tile_at(w.t, i)) * T::kRecord;
+        const uint32_t st = kc % T::kStages, slot = kc % T::kSlots;
+        if (!wait(sh().bar.k_empty[st], kc / T::kStages + 1)) return;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh().bar.k_full[st], T::kTileBytes);
+          bulk_g2s_a(k_at(st), now, T::kTileBytes, smem_addr(&sh().bar.k_full[st]));
+          mbar_arrive_expect_tx(&sh().bar.f_full[slot], T::kFactors);
+          bulk_g2s_a(factors(slot), now + 2 * T::kTileBytes, T::kFactors, smem_addr(&sh().bar.f_full[slot]));
+        }
+        __syncwarp();
+      }
+      if (kc > 0) {
+        const uint32_t vc = kc - 1, st = vc % T::kStages;
+        if (!wait(sh().bar.v_empty[st], vc / T::kStages + 1)) return;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sh().bar.v_full[st], T::kTileBytes);
+          bulk_g2s_a(v_at(st), before + T::kTileBytes, T::kTileBytes, smem_addr(&sh().bar.v_full[st]));
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  // ---- kUnpack: the CTA's tile
+  __device__ __forceinline__ void unpack(const Sequence& s, int b, int h, int tile) const {
+    At t;
+    t.tile = tile, t.len = s.len, t.h = h, t.i = 0, t.pages = -1;
+    const int key = tile * kTcKeys + 16 * (threadIdx.x & 7);
+    if (key < s.len) t.pages = __ldg(a.b.table + b * a.b.width + (key >> a.c.page_shift));
+    uint32_t ck[kTurns][4], cv[8][kVWords], in;
+    float ks, vs;
+    int valid;
+    load_k(t, ck, ks, vs, in);
+    load_v(t, cv, valid);
+    store_k(0, ck, in);
+    if (threadIdx.x < kTcKeys) put_factors(2 * T::kTileBytes, threadIdx.x, !(in & 256u), ks, vs);
+    store_v(T::kTileBytes, cv, valid);
   }
 
   // ---- warps 0-3 (half 0) and 4-7 (half 1)
@@ -1042,8 +1119,8 @@ struct AttnTc {
   }
 };
 
-template <int D, bool E4M3, bool BF16>
-__global__ void __launch_bounds__(kTcCta, 1)
+template <int D, bool E4M3, bool BF16, int SOURCE>
+__global__ void __launch_bounds__(tc_threads(SOURCE), 1)
     attn_tc_kernel(const __grid_constant__ AttnArgs a, int least) {
   extern __shared__ uint8_t raw[];
   TcShared& sh = tc_shared();
@@ -1054,7 +1131,8 @@ __global__ void __launch_bounds__(kTcCta, 1)
     none.last_cta = -1;
     reinterpret_cast<Cut*>(a.partials)[blockIdx.x] = none;
   }
-  plan_piece<kTcRows, kTcKeys, kTcCta>(a, least, &sh.piece);
+  constexpr int kIssue = SOURCE == kTiles ? kConvWarp + 1 : kIssueWarp;
+  plan_piece<kTcRows, kTcKeys, tc_threads(SOURCE)>(a, least, &sh.piece);
   if (sh.piece.begin == sh.piece.end) return;
   if (tid == 0) {
     sh.abort = 0;
@@ -1062,12 +1140,12 @@ __global__ void __launch_bounds__(kTcCta, 1)
     mbar_init(&bar.q_full, kConvWarp);
     mbar_init(&bar.join, kConvWarp);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bar.k_full[i], kConvWarps);
+      mbar_init(&bar.k_full[i], SOURCE == kTiles ? 1 : kConvWarps);
       mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.v_full[i], kConvWarps);
+      mbar_init(&bar.v_full[i], SOURCE == kTiles ? 1 : kConvWarps);
       mbar_init(&bar.v_empty[i], 1);
     }
-    for (int i = 0; i < 6; ++i) mbar_init(&bar.f_full[i], 4);
+    for (int i = 0; i < 6; ++i) mbar_init(&bar.f_full[i], SOURCE == kTiles ? 1 : 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 4);
@@ -1075,15 +1153,19 @@ __global__ void __launch_bounds__(kTcCta, 1)
     }
     fence_mbar_init();
   }
-  if (warp == kIssueWarp) {
+  if (warp == kIssue) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const AttnTc<D, E4M3, BF16> r{a, (smem_addr(raw) + 1023) & ~1023u, sh.tmem};
-  if (warp < kConvWarp) {
+  const AttnTc<D, E4M3, BF16, SOURCE> r{a, (smem_addr(raw) + 1023) & ~1023u, sh.tmem};
+  if constexpr (SOURCE == kTiles) {  // (registers are plenty)
+    if (warp < kConvWarp) r.softmax();
+    else if (warp == kIssue) r.issue();
+    else r.copy();
+  } else if (warp < kConvWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     r.softmax();
   } else if (warp < kIssueWarp) {
@@ -1095,10 +1177,26 @@ __global__ void __launch_bounds__(kTcCta, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssueWarp) {
+  if (warp == kIssue) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, 512);
   }
+}
+
+// The visible tiles of all sequences as 16-bit values in the workspace, a CTA a tile:
+// where many units share them, each would be converted many times over.
+template <int D, bool E4M3, bool BF16>
+__global__ void __launch_bounds__(32 * kConvWarps) attn_unpack_kernel(const __grid_constant__ AttnArgs a) {
+  const int64_t line = blockIdx.x / a.tiles_each;
+  const int tile = static_cast<int>(blockIdx.x - line * a.tiles_each);
+  const int b = static_cast<int>(line / a.c.heads), h = static_cast<int>(line - static_cast<int64_t>(b) * a.c.heads);
+  const Sequence s = sequence(a.c, a.b, b);
+  if (s.n == 0 || (tile > 0 && tile * kTcKeys >= s.len)) return;
+  const int lo = a.window > 0 ? max(0, s.prefix - a.window + 1) : 0;
+  if ((tile + 1) * kTcKeys <= lo && tile * kTcKeys >= a.sinks) return;
+  const AttnTc<D, E4M3, BF16, kUnpack> r{a, 0, 0,
+                                         a.tiles + static_cast<int64_t>(blockIdx.x) * Tc<D>::kRecord};
+  r.unpack(s, b, h, tile);
 }
 
 // Adds up the units that were cut between CTAs, in the order of the CTAs: a
@@ -1162,14 +1260,26 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
   }
 }
 
-template <int D, bool E4M3, bool BF16>
-cudaError_t launch_tc_kernel(const AttnArgs& a, int sms, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, E4M3, BF16>,
+template <int D, bool E4M3, bool BF16, int SOURCE>
+cudaError_t launch_tc_source(const AttnArgs& a, int sms, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, E4M3, BF16, SOURCE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<D>::kSmem);
   if (e != cudaSuccess) return e;
-  attn_tc_kernel<D, E4M3, BF16><<<sms, kTcCta, Tc<D>::kSmem, s>>>(a, 2);
-  const cudaError_t l = cudaGetLastError();
-  if (l != cudaSuccess) return l;
+  attn_tc_kernel<D, E4M3, BF16, SOURCE><<<sms, tc_threads(SOURCE), Tc<D>::kSmem, s>>>(a, 2);
+  return cudaGetLastError();
+}
+template <int D, bool E4M3, bool BF16>
+cudaError_t launch_tc_kernel(const AttnArgs& a, int sms, cudaStream_t s) {
+  cudaError_t e;
+  if (a.tiles) {
+    const int64_t ctas = static_cast<int64_t>(a.b.sequences) * a.c.heads * a.tiles_each;
+    attn_unpack_kernel<D, E4M3, BF16><<<static_cast<unsigned>(ctas), 32 * kConvWarps, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_tc_source<D, E4M3, BF16, kTiles>(a, sms, s);
+  } else {
+    e = launch_tc_source<D, E4M3, BF16, kOwn>(a, sms, s);
+  }
+  if (e != cudaSuccess) return e;
   attn_tc_reduce_kernel<D><<<dim3(sms, kReduceShare), kReduceThreads, 0, s>>>(a, sms);
   return cudaGetLastError();
 }
@@ -1188,6 +1298,8 @@ size_t attn_tc_partials(int sms, int dim) {
   return static_cast<size_t>(sms) * sizeof(Cut) +
          2 * static_cast<size_t>(sms) * kTcRows * (dim + 2) * sizeof(float);
 }
+
+int64_t attn_tc_tile_bytes(int dim) { return dim == 128 ? Tc<128>::kRecord : Tc<64>::kRecord; }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int sms, cudaStream_t s) {
   return a.c.dim == 128 ? launch_tc_dim<128>(a, sms, s) : launch_tc_dim<64>(a, sms, s);

@@ -575,7 +575,7 @@ PyObject* attention(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
     const uint8_t none = 0;
     int st;
     for (int64_t bytes = 0;; bytes = static_cast<int64_t>(w4_attention_workspace_size(
-                                 static_cast<int>(heads), c.cache.heads, c.cache.head_dim))) {
+                                 &c.cache, &c.batch, T, static_cast<int>(heads)))) {
       if (!ws) w_new = workspace(o[0], dev, stream, bytes);
       const at::Tensor& w8 = ws ? *ws : w_new;
       void* const pw = out_ptr(&w8);

@@ -301,6 +301,10 @@ struct AttnArgs {
   int* status;          // workspace: status word, counters, partial sums
   int* counters;
   float* partials;
+  // unpacked tiles of 128 keys (w4_attn_tc.cu), or null: [sequences][cache heads]
+  // [tiles_each]
+  uint8_t* tiles;
+  int64_t tiles_each;
 };
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s);
@@ -309,6 +313,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
 size_t attn_dec_partials(int sms, int dim);
 cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s);
 size_t attn_tc_partials(int sms, int dim);
+int64_t attn_tc_tile_bytes(int dim);
 cudaError_t launch_attn_tc(const AttnArgs& a, int sms, cudaStream_t s);
 
 }  // namespace w4

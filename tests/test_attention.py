@@ -88,7 +88,7 @@ def test_pages(gpu_lib, page, D, codes, dt):
 
 
 MIXED = {
-    "prompt": ([200], [200]), "prompts": ([1, 129, 64, 300], [1, 129, 64, 300]),
+    "prompt": ([200], [200]), "long prompts": ([700, 900], [1300, 900]), "prompts": ([1, 129, 64, 300], [1, 129, 64, 300]),
     "chunk": ([70], [333]), "mixed": ([1, 90, 0, 1, 17, 5], [400, 131, 40, 1, 17, 260]),
     "more rows than positions": ([6, 3, 2], [4, 0, 2]), "nothing": ([0, 0], [5, 0]),
     "long": ([2, 1], [3000, 2111]),
@@ -115,6 +115,16 @@ def test_window_and_sinks(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16), (F8, torch.bfloat16),
+                                      (S8, torch.float16)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (300, 4), (1000, 200)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 1, 128), (32, 2, 64)])
+def test_window_and_sinks_of_chunks(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt):
+    """Rows enough for the keys and values to be unpacked first; some sequences
+    have few, or none."""
+    _check([1, 300, 0, 128, 63], [900, 1000, 70, 128, 1999], Hq, Hkv, D, 64, codes, dt, window, sinks)
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16)])
 @pytest.mark.parametrize("kind", ["tree", "any", "none"])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4), (3, 0)])
@@ -123,6 +133,15 @@ def test_tree(gpu_lib, Hq, Hkv, D, window, sinks, kind, codes, dt):
     rows = [1, 7, 64, 0, 33, 130, 4]
     lens = [1, 300, 600, 10, 33, 500, 2]
     _check(rows, lens, Hq, Hkv, D, 16, codes, dt, window, sinks, _tree(rows, 130, kind=kind))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 4)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 1, 128), (64, 2, 64)])
+def test_large_trees(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt):
+    rows = [130, 70, 1]
+    _check(rows, [900, 300, 40], Hq, Hkv, D, 16, codes, dt, window, sinks, _tree(rows, 130))
 
 
 @pytest.mark.gpu
@@ -253,11 +272,12 @@ def test_same_bits_again(gpu_lib, D):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("D", [64, 128, 80])
-def test_pages_that_are_none(gpu_lib, D):
+@pytest.mark.parametrize("D,n", [(64, 40), (128, 40), (80, 40), (128, 1), (64, 1), (128, 1300),
+                                 (64, 1300)])
+def test_pages_that_are_none(gpu_lib, D, n):
     """Keys of pages outside the cache are not seen; a row with no other is
     zeros; lengths beyond the table count as its end."""
-    batch = kv.Batch([1, 1, 40], [64, 64, 64], 16, behind=0)
+    batch = kv.Batch([1, 1, n], [64, 64, max(64, n)], 16, behind=0)
     cache = kv.random_cache(batch, 1, D, S8)
     q = torch.randn(batch.T, 2, D).half()
     held = kv.on(cache, DEV)
@@ -266,7 +286,7 @@ def test_pages_that_are_none(gpu_lib, D):
     bad[0, :] = -1
     bad[1, 1] = batch.pages
     bad[2, 2] = 1 << 30
-    lens[1] = 100000
+    assert int(bad.shape[1]) == -(-max(64, n) // 16)
     got = w4.cache_attention(held, q.to(DEV), bad, starts, lens).cpu()
     assert bool((got[0] == 0).all())
     # the same with these pages' keys cut out
@@ -280,15 +300,15 @@ def test_pages_that_are_none(gpu_lib, D):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("D,n", [(128, 1), (64, 1), (128, 64), (96, 2)])
+@pytest.mark.parametrize("D,n", [(128, 1), (64, 1), (128, 64), (96, 2), (128, 390), (64, 200)])
 def test_captured_and_replayed(gpu_lib, D, n):
     """A captured call follows what its arrays hold when it is replayed."""
-    batch = kv.Batch([n, n], [400, 300], 16, behind=0)
+    batch = kv.Batch([n, n], [n + 400, n + 300], 16, behind=0)
     cache = kv.random_cache(batch, 2, D, S8)
     held, (table, starts, lens) = kv.on(cache, DEV), batch.plan(DEV)
     q = torch.randn(batch.T, 4, D).half().to(DEV)
     out = torch.empty_like(q)
-    ws = torch.zeros(w4.attention_workspace_size(4, held), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(w4.attention_workspace_size(held, batch.T, 4, table), dtype=torch.uint8, device=DEV)
     w4.cache_attention(held, q, table, starts, lens, out=out, ws=ws)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -298,7 +318,7 @@ def test_captured_and_replayed(gpu_lib, D, n):
         bad = torch.cuda.CUDAGraph()
         with torch.cuda.graph(bad):
             w4.cache_attention(held, q, table, starts, lens, out=out)
-    for k in ([400, 300], [n, 77], [200, n + 1]):
+    for k in ([n + 400, n + 300], [n, 77], [200, n + 1]):
         lens.copy_(torch.tensor(k))
         q.copy_(torch.randn(batch.T, 4, D))
         graph.replay()
