@@ -9,6 +9,8 @@
 //   t_j = S_j * (scale * log2 e * ks_j) + log2 vs_j       (ks, vs: the scales)
 //   P_j = 2^(t_j - m) <= 2^8, fp16, written over S in tensor memory
 //   O_X += P V            V: codes as fp16, exact;  l += P_j / vs_j;  out = O / l
+//                         (64 keys at a time: the first half's product runs while
+//                         the second half's P is made)
 //
 // as in w4_attn_dec.cu: both scales enter the exponent, so that no code is
 // rounded and P is rounded relative to what it weighs.  Keys that are none
@@ -76,8 +78,8 @@ struct Tc {
 };
 
 struct TcBarriers {
-  uint64_t q_full, join, k_full[4], k_empty[4], v_full[4], v_empty[4], f_full[6], s_full[2], p_full[2],
-      pv_done[2];
+  uint64_t q_full, join, k_full[4], k_empty[4], v_full[4], v_empty[4], f_full[6], s_full[2], p_half[2],
+      p_full[2], pv_half[2], pv_done[2];
 };
 
 // What the roles share, at an address known when compiled (no register holds one).
@@ -275,17 +277,28 @@ struct AttnTc {
     }
     __syncwarp();
   }
-  __device__ __forceinline__ void pv(int half, uint32_t st, bool add, uint32_t lo, uint32_t hi) const {
+  // The first (second) 64 keys' part of the product with V.
+  __device__ __forceinline__ void pv(int half, int part, uint32_t st, bool add, uint32_t lo,
+                                     uint32_t hi) const {
     constexpr uint32_t kId = idesc_f16_c(0u, D);
     if (elect_one()) {
-      const uint32_t vd = lo + ((2 * T::kQ + (T::kStages + st) * T::kTileBytes) >> 4);
-      const uint32_t d = tmem + T::kO + half * D, p = tmem + T::kS + half * kTcKeys;
+      const uint32_t vd = lo + ((2 * T::kQ + (T::kStages + st) * T::kTileBytes + part * D * 128) >> 4);
+      const uint32_t d = tmem + T::kO + half * D, p = tmem + T::kS + half * kTcKeys + 32 * part;
 #pragma unroll
-      for (int i = 0; i < kTcKeys / 16; ++i)
-        mma_ts32(d, p + 8 * i, vd + (i >> 2) * (D * 128 >> 4) + 2 * (i & 3), hi, kId, i != 0 || add);
-      mma_commit(&sh().bar.pv_done[half]);
+      for (int i = 0; i < kTcKeys / 32; ++i) mma_ts32(d, p + 8 * i, vd + 2 * i, hi, kId, i != 0 || add);
+      mma_commit(part ? &sh().bar.pv_done[half] : &sh().bar.pv_half[half]);
     }
     __syncwarp();
+  }
+  __device__ __forceinline__ bool pv_parts(int half, uint32_t& count, uint32_t st, bool add, uint32_t lo,
+                                           uint32_t hi) const {
+    if (!wait(sh().bar.p_half[half], count)) return false;
+    tc_fence_after();
+    pv(half, 0, st, add, lo, hi);
+    if (!wait(sh().bar.p_full[half], count++)) return false;
+    tc_fence_after();
+    pv(half, 1, st, true, lo, hi);
+    return true;
   }
   __device__ __forceinline__ void commit(uint64_t& b) const {
     if (elect_one()) mma_commit(&b);
@@ -316,18 +329,14 @@ struct AttnTc {
           st = kc % T::kStages;
           if (!wait(sh().bar.v_full[vs], vc / T::kStages)) return;
           fence_async_shared();
-          if (!wait(sh().bar.p_full[0], pc0++)) return;
-          tc_fence_after();
-          pv(0, vs, i > 0, lo, hi);
+          if (!pv_parts(0, pc0, vs, i > 0, lo, hi)) return;
           if (i + 1 < n) {
             if (!wait(sh().bar.k_full[st], kc / T::kStages)) return;
             fence_async_shared();
             tc_fence_after();
             qk(0, 0, st, lo, hi);
           }
-          if (!wait(sh().bar.p_full[1], pc1++)) return;
-          tc_fence_after();
-          pv(1, vs, i > 0, lo, hi);
+          if (!pv_parts(1, pc1, vs, i > 0, lo, hi)) return;
           commit(sh().bar.v_empty[vs]);
           ++vc;
           if (i + 1 < n) {
@@ -344,11 +353,7 @@ struct AttnTc {
             const uint32_t vs = vc % T::kStages;
             if (!wait(sh().bar.v_full[vs], vc / T::kStages)) return;
             fence_async_shared();
-            if (!(odd ? wait(sh().bar.p_full[1], pc1) : wait(sh().bar.p_full[0], pc0))) return;
-            if (odd) ++pc1;
-            else ++pc0;
-            tc_fence_after();
-            pv(odd, vs, i > 1, lo, hi);
+            if (!(odd ? pv_parts(1, pc1, vs, i > 1, lo, hi) : pv_parts(0, pc0, vs, i > 1, lo, hi))) return;
             commit(sh().bar.v_empty[vs]);
             ++vc;
           }
@@ -758,10 +763,8 @@ struct AttnTc {
                  : "memory");
     return v;
   }
-  // O, the sums of the tiles before, times shrink (a row's own).
-  __device__ __forceinline__ bool rescale_sums(uint32_t o_at, int half, uint32_t sc,
-                                               const float (&shrink)[4]) const {
-    if (!wait(sh().bar.pv_done[half], sc - 1)) return false;
+  // O times shrink (a row's own); the products so far are done.
+  __device__ __forceinline__ void rescale_sums(uint32_t o_at, const float (&shrink)[4]) const {
     tc_fence_after();
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
@@ -777,15 +780,15 @@ struct AttnTc {
       tmem_st_frag(o_at + c, y[0]);
       tmem_st_frag(o_at + c + (16u << 16), y[1]);
     }
-    return true;
   }
-  // The tile's probabilities before chunk `end` times shrink: exactly, it is a power
-  // of two (but for those that fall below fp16's subnormals).
-  __device__ __forceinline__ void rescale_tile(uint32_t s_at, int end, const float (&shrink)[4]) const {
-    if (end == 0) return;
+  // The tile's probabilities of chunks begin .. end - 1 times shrink: exactly, it is a
+  // power of two (but for those that fall below fp16's subnormals).
+  __device__ __forceinline__ void rescale_tile(uint32_t s_at, int begin, int end,
+                                               const float (&shrink)[4]) const {
+    if (begin >= end) return;
     tmem_wait_st();
 #pragma unroll 1
-    for (int c = 0; c < end; ++c) {
+    for (int c = begin; c < end; ++c) {
       uint32_t p[2][8];
       tmem_ld_pairs(s_at + 16 * c, p[0]);
       tmem_ld_pairs(s_at + 16 * c + (16u << 16), p[1]);
@@ -846,7 +849,7 @@ struct AttnTc {
     for (;;) {
       const int nr = rows_of(w), n = w.to - w.from;
       const bool full = nr > kHalf;
-      bool more = false;
+      const bool more = look_ahead();
 
       // what the warp's rows see, a row a lane (rows that are none: all)
       const int first_row = (full ? half * kHalf : 0) + 32 * (warp & 3);
@@ -888,7 +891,6 @@ struct AttnTc {
         tc_fence_after();
         if (full && i + 1 == n) {
           // this half's last product with Q is done: the next unit's Q
-          more = look_ahead();
           if (more && (half == 0 || rows_of(way_next()) > kHalf)) load_q(way_next(), half);
         }
         const bool all = key0 + kTcKeys <= hi_all && (key0 >= lo_all || key0 + kTcKeys <= a.sinks);
@@ -954,8 +956,19 @@ struct AttnTc {
               l[k].x *= shrink[k];
               l[k].y *= shrink[k];
             }
-            if (begun && !rescale_sums(o_at, half, sc, shrink)) return;
-            rescale_tile(s_at, c, shrink);
+            // O holds the sums of the tiles before and, from the third chunk on, of
+            // this one's first half
+            if (c >= 2) {
+              if (!wait(sh().bar.pv_half[half], sc)) return;
+              rescale_sums(o_at, shrink);
+              rescale_tile(s_at, 2, c, shrink);
+            } else {
+              if (begun) {
+                if (!wait(sh().bar.pv_done[half], sc - 1)) return;
+                rescale_sums(o_at, shrink);
+              }
+              rescale_tile(s_at, 0, c, shrink);
+            }
           }
           float2 neg[4];
 #pragma unroll
@@ -980,6 +993,12 @@ struct AttnTc {
           }
           tmem_st_pairs(s_at + 16 * c, p[0]);
           tmem_st_pairs(s_at + 16 * c + (16u << 16), p[1]);
+          if (c == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh().bar.p_half[half]);
+          }
         }
         begun = true;
         tmem_wait_st();
@@ -991,7 +1010,7 @@ struct AttnTc {
       first_tile += n;
       // (before the result is written, so that the next unit's first scores are
       // computed meanwhile; a unit of one half still needs Q's memory)
-      if (more) q_loaded();
+      if (more && full) q_loaded();
       if (begun) {
         if (!wait(sh().bar.pv_done[half], sc - 1)) return;
         tc_fence_after();
@@ -1008,12 +1027,9 @@ struct AttnTc {
         if (lane >> 3 == k) row_m = mk, row_l = lk;
       }
       if (!finish(full, half, nr, begun, row_m, row_l, o_at, meets)) return;
-      if (!full) {
-        more = look_ahead();
-        if (more) {
-          if (half == 0 || rows_of(way_next()) > kHalf) load_q(way_next(), half);
-          q_loaded();
-        }
+      if (!full && more) {
+        if (half == 0 || rows_of(way_next()) > kHalf) load_q(way_next(), half);
+        q_loaded();
       }
       if (!more) return;
       __syncwarp();
@@ -1148,7 +1164,9 @@ __global__ void __launch_bounds__(tc_threads(SOURCE), 1)
     for (int i = 0; i < 6; ++i) mbar_init(&bar.f_full[i], SOURCE == kTiles ? 1 : 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_half[i], 4);
       mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.pv_half[i], 1);
       mbar_init(&bar.pv_done[i], 1);
     }
     fence_mbar_init();
