@@ -2,7 +2,7 @@
 // head (decode steps): bound by the bytes of the visible codes.
 //
 // A unit is 16 rows (query heads of a key head, of one token or a few) by the
-// key tiles they see; four warps of a CTA take 16 keys each of a 64-key tile.
+// key tiles they see; four warps of a CTA take 32 keys each of a 128-key tile.
 // mma.sync m16n8k16 in fp16, both kinds of codes being exact there:
 //
 //   t_j = (q . code_j) * (scale * log2 e * ks_j) + log2 vs_j
@@ -21,8 +21,8 @@
 // Positions are read in any order within an MMA, so that a lane loads 16
 // neighbouring codes at once: for scores they are consecutive k of its key's
 // row, for sums consecutive columns of its four keys, whose bytes PRMT pairs.
-// Slots behind the sequence's end and pages that are none arrive as zeros and
-// are never read: whatever they hold meets no arithmetic.
+// Slots behind the sequence's end and pages that are none are not read: zeros
+// stand for their codes, and log2 vs = kNoKey for their scales.
 #include <cuda_bf16.h>
 
 #include "w4_attn_math.cuh"
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kRows = 16;          // rows of a unit
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;          // keys of a warp's stage
+constexpr int kKeys = 32;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
 
@@ -41,8 +41,11 @@ template <int D>
 struct Ring {
   static constexpr int kCodes = kKeys * D;                // bytes of one array
   static constexpr int kStage = 2 * kCodes + 2 * kKeys * 4;
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kWarp = kStage * kStages;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  // then the factors of the stage in use: of pairs of keys ks, ks, log2 vs, log2 vs;
+  // then of pairs 1 / vs
+  static constexpr int kFactors = kStage * kStages;
+  static constexpr int kWarp = kFactors + kKeys * 12;
 };
 template <int D>
 constexpr size_t smem_bytes() {
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
   const int group = a.heads / a.c.heads;
   const uint32_t ring = smem_addr(smem) + warp * R::kWarp;
   const uint8_t* const ring_p = smem + warp * R::kWarp;
+  float4* const factors = reinterpret_cast<float4*>(smem + warp * R::kWarp + R::kFactors);
   float4* const sums = reinterpret_cast<float4*>(smem);
 
   Walk<kRows, kTile> w;
@@ -202,47 +206,54 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
       lo_all = a.window > 0 ? s.prefix + (r0 + nr - 1) / group - a.window + 1 : 0;
     }
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY};
+    float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // of even and odd keys
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 
-    // this warp's keys of tile i: the page, looked up 32 tiles at a time
+    // the pages of this warp's two groups of 16 keys in a tile, looked up 16 tiles at
+    // a time: lane 2 i + n has that of group n of tile base + i
     const int32_t* const line = a.b.table + w.b * a.b.width;
     const auto look_up = [&](int i) -> int {
+      i += lane >> 1;
       if (i >= w.to) return -1;
-      const int key = tile_at(w.t, i) * kTile + warp * kKeys;
+      const int key = tile_at(w.t, i) * kTile + warp * kKeys + 16 * (lane & 1);
       if (key >= s.len) return -1;
       const int page = __ldg(line + (key >> a.c.page_shift));
       return page >= 0 && page < a.c.pages ? page : -1;
     };
-    int pages = look_up(w.from + lane), pages_next = look_up(w.from + 32 + lane);
-    int base = w.from;  // tile of lane 0's page
-    const auto page_of = [&](int i) -> int {
-      const int d = i - base;
+    int base = w.from;
+    int pages = look_up(base), pages_next = look_up(base + 16);
+    const auto page_of = [&](int i, int n) -> int {
+      const int d = 2 * (i - base) + n;
       return d < 32 ? __shfl_sync(0xffffffffu, pages, d) : __shfl_sync(0xffffffffu, pages_next, d - 32);
     };
     const auto load = [&](int i, int slot) {
-      const int page = page_of(i);
-      if (page >= 0) {
-        const int key = tile_at(w.t, i) * kTile + warp * kKeys;
-        const int valid = min(s.len - key, kKeys);
-        const int64_t at = (((static_cast<int64_t>(page) * a.c.heads + w.h) << a.c.page_shift) +
-                            (key & ((1 << a.c.page_shift) - 1)));
-        const uint32_t dst = ring + slot * R::kStage;
+      const uint32_t dst = ring + slot * R::kStage;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int page = page_of(i, n);
+        const int key = tile_at(w.t, i) * kTile + warp * kKeys + 16 * n;
+        const int valid = page >= 0 ? min(s.len - key, 16) : 0;
+        const int64_t at = page < 0 ? 0
+                                    : ((static_cast<int64_t>(page) * a.c.heads + w.h) << a.c.page_shift) +
+                                          (key & ((1 << a.c.page_shift) - 1));
         const uint8_t *k = a.c.k + at * D, *v = a.c.v + at * D;
 #pragma unroll
         for (int u = 0; u < D / 32; ++u) {
-          const int n = lane + 32 * u, row = n / (D / 16), c = n % (D / 16);
+          const int e = lane + 32 * u, row = e / (D / 16), c = e % (D / 16);
           const uint32_t bytes = row < valid ? 16 : 0;
-          cp_async16(dst + k_chunk<D>(row, c), k + n * 16, bytes);
-          cp_async16(dst + R::kCodes + v_chunk<D>(row, c), v + n * 16, bytes);
+          cp_async16(dst + n * 16 * D + k_chunk<D>(row, c), k + e * 16, bytes);
+          cp_async16(dst + R::kCodes + n * 16 * D + v_chunk<D>(row, c), v + e * 16, bytes);
         }
-        if (lane < 8) {
-          const float* sc = (lane < 4 ? a.c.k_scales : a.c.v_scales) + at + 4 * (lane & 3);
-          cp_async16(dst + 2 * R::kCodes + lane * 16, sc, 4 * min(max(valid - 4 * (lane & 3), 0), 4));
+        if (lane >> 3 == n) {  // four lanes for ks, four for vs
+          const int q = lane & 3;
+          const float* sc = (lane & 4 ? a.c.v_scales : a.c.k_scales) + at + 4 * q;
+          cp_async16(dst + 2 * R::kCodes + (lane & 4 ? kKeys * 4 : 0) + n * 64 + q * 16, sc,
+                     4 * min(max(valid - 4 * q, 0), 4));
         }
       }
       cp_async_commit();
@@ -252,28 +263,43 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
 
     int slot = 0;
     for (int i = w.from; i < w.to; ++i) {
-      if (i - base >= 32) {
-        base += 32;
+      if (i - base >= 16) {
+        base += 16;
         pages = pages_next;
-        pages_next = look_up(base + 32 + lane);
+        pages_next = look_up(base + 16);
       }
       cp_async_wait<R::kStages - 2>();
       __syncwarp();
       // (asked for before this stage is used: its slot is the one left last)
       load(i + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
-      const int page = page_of(i);
-      if (page >= 0) {
+      const int page0 = page_of(i, 0), page1 = page_of(i, 1);
+      if (page0 >= 0 || page1 >= 0) {
         const uint8_t* const st = ring_p + slot * R::kStage;
         const int key0 = tile_at(w.t, i) * kTile + warp * kKeys;
-        // scores: two blocks of eight keys
-        float c[2][4];
+        // the factors of the warp's keys, a key a lane
+        {
+          const float* const sc = reinterpret_cast<const float*>(st + 2 * R::kCodes);
+          const bool in = (lane < 16 ? page0 : page1) >= 0 && key0 + lane < s.len;
+          const float ks = sc[lane], vs = sc[kKeys + lane];
+          const float safe = fmaxf(vs, kLeastScale);
+          float* const f = reinterpret_cast<float*>(factors);
+          f[4 * (lane >> 1) + (lane & 1)] = in ? ks + (vs - vs) : 0.f;  // NaN where vs is
+          f[4 * (lane >> 1) + 2 + (lane & 1)] = in ? lg2(safe) : kNoKey;
+          f[4 * kKeys / 2 + lane] = in ? rcp(safe) : 0.f;
+          __syncwarp();
+        }
+        // scores: four blocks of eight keys
+        float c[4][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(st + k_chunk<D>(8 * nt + g, 4 * j + t4));
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(st + (nt >> 1) * 16 * D +
+                                                             k_chunk<D>(8 * (nt & 1) + g, 4 * j + t4));
             const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -282,42 +308,44 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
               mma16816(c[nt], qf[4 * j + q], b0, b1);
             }
           }
-        }
-        // this lane's keys: 2 t4, 2 t4 + 1 of both blocks
-        const float* const ks = reinterpret_cast<const float*>(st + 2 * R::kCodes);
-        float rvs[4];
-        const bool all = key0 + kKeys <= hi_all &&
-                         (key0 >= lo_all || key0 + kKeys <= a.sinks);
+        // this lane's keys: 2 t4, 2 t4 + 1 of the four blocks
+        float2 rvs[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int key = 8 * (n >> 1) + 2 * t4 + (n & 1);
-          const float vs = ks[kKeys + key];
-          const float kss = ks[key] + (vs - vs);  // NaN where the value's is
-          const float safe = fmaxf(vs, kLeastScale);
-          const float lvs = lg2(safe);
-          rvs[n] = rcp(safe);
+        for (int nt = 0; nt < 4; ++nt) {
+          const float4 f = factors[4 * nt + t4];
+          rvs[nt] = reinterpret_cast<const float2*>(factors + kKeys / 2)[4 * nt + t4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float& x = c[n >> 1][2 * e + (n & 1)];
-            x = fmaf(x * rf[e], kss, lvs);
-            if (!all) {
-              const int j = key0 + key;
+            const float2 x = fma2(mul2(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), make_float2(rf[e], rf[e])),
+                                  make_float2(f.x, f.y), make_float2(f.z, f.w));
+            c[nt][2 * e] = x.x;
+            c[nt][2 * e + 1] = x.y;
+          }
+        }
+        if (!(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= a.sinks))) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = key0 + 8 * (n >> 1) + 2 * t4 + (n & 1);
               bool see = j < hi[e];
               if (mask[e] && j >= s.prefix)
                 see = see && j - s.prefix < a.mask_width && mask[e][j - s.prefix] != 0;
               else
                 see = see && (j >= lo[e] || j < a.sinks);
-              if (!see) x = -INFINITY;
+              if (!see) c[n >> 1][2 * e + (n & 1)] = -INFINITY;
             }
-          }
         }
         // the running maximum, of a row over its four lanes
-        float top[2], from[2];
+        float top[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          top[e] = fmaxf(fmaxf(c[0][2 * e], c[0][2 * e + 1]), fmaxf(c[1][2 * e], c[1][2 * e + 1]));
+          top[e] = max3(max3(c[0][2 * e], c[0][2 * e + 1], c[1][2 * e]),
+                        max3(c[1][2 * e + 1], c[2][2 * e], c[2][2 * e + 1]),
+                        fmaxf(c[3][2 * e], c[3][2 * e + 1]));
           top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
           top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+          if (top[e] < 0.5f * kNoKey) top[e] = -INFINITY;  // no key but such that are none
         }
         if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
 #pragma unroll
@@ -325,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
             const float to = fmaxf(m[e], top[e]);
             const float shrink = to == -INFINITY ? 1.f : ex2(m[e] - to);
             m[e] = to;
-            l[e] *= shrink;
+            l[e].x *= shrink;
+            l[e].y *= shrink;
 #pragma unroll
             for (int d = 0; d < D / 8; ++d) {
               o[d][2 * e] *= shrink;
@@ -333,50 +362,49 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
             }
           }
         }
+        uint32_t p[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          from[e] = m[e] == -INFINITY ? 0.f : m[e];
+          const float from = m[e] == -INFINITY ? 0.f : -m[e];
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            float2 x = add2(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), make_float2(from, from));
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            l[e] = fma2(x, rvs[nt], l[e]);
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            p[nt >> 1][2 * (nt & 1) + e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        // sums: columns D / 8 * g .. of four keys at a time
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const uint8_t* const vp = st + R::kCodes + kk * 16 * D;
+          uint32_t v[4][D / 32];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            float& x = c[n >> 1][2 * e + (n & 1)];
-            x = ex2(x - from[e]);
-            l[e] = fmaf(x, rvs[n], l[e]);
+            const int key = 8 * (n >> 1) + 2 * t4 + (n & 1);
+            if constexpr (D == 128) {
+              const uint4 w4 = *reinterpret_cast<const uint4*>(vp + v_chunk<D>(key, g));
+              v[n][0] = w4.x, v[n][1] = w4.y, v[n][2] = w4.z, v[n][3] = w4.w;
+            } else {
+              const uint2 w2 = *reinterpret_cast<const uint2*>(vp + v_chunk<D>(key, g >> 1) + 8 * (g & 1));
+              v[n][0] = w2.x, v[n][1] = w2.y;
+            }
           }
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t sel = hf ? 0x7362 : 0x5140;
+              uint32_t b[2][2];
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+                codes4_f16<E4M3>(prmt(v[2 * nt][q], v[2 * nt + 1][q], sel), b[nt][0], b[nt][1]);
+              mma16816(o[4 * q + 2 * hf], p[kk], b[0][0], b[1][0]);
+              mma16816(o[4 * q + 2 * hf + 1], p[kk], b[0][1], b[1][1]);
+            }
         }
-        uint32_t p[4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const __half2 h = __floats2half2_rn(c[nt][2 * e], c[nt][2 * e + 1]);
-            p[2 * nt + e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        // sums: columns D / 8 * g .. of the four keys
-        const uint8_t* const vp = st + R::kCodes;
-        uint32_t v[4][D / 32];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int key = 8 * (n >> 1) + 2 * t4 + (n & 1);
-          if constexpr (D == 128) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(vp + v_chunk<D>(key, g));
-            v[n][0] = w4.x, v[n][1] = w4.y, v[n][2] = w4.z, v[n][3] = w4.w;
-          } else {
-            const uint2 w2 = *reinterpret_cast<const uint2*>(vp + v_chunk<D>(key, g >> 1) + 8 * (g & 1));
-            v[n][0] = w2.x, v[n][1] = w2.y;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t sel = hf ? 0x7362 : 0x5140;
-            uint32_t b[2][2];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-              codes4_f16<E4M3>(prmt(v[2 * nt][q], v[2 * nt + 1][q], sel), b[nt][0], b[nt][1]);
-            mma16816(o[4 * q + 2 * hf], p, b[0][0], b[1][0]);
-            mma16816(o[4 * q + 2 * hf + 1], p, b[0][1], b[1][1]);
-          }
       }
       slot = slot + 1 == R::kStages ? 0 : slot + 1;
     }
@@ -385,11 +413,12 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
     // the four warps' sums, relative to the largest maximum
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      float sum = l[e].x + l[e].y;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       if (t4 == 0) {
         part_m[warp][g + 8 * e] = m[e];
-        part_l[warp][g + 8 * e] = l[e];
+        part_l[warp][g + 8 * e] = sum;
       }
     }
     __syncthreads();  // the rings are free
@@ -525,7 +554,7 @@ cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_dec_kernel<D, E4M3><<<ctas, kThreads, smem, s>>>(a, 2);
+  attn_dec_kernel<D, E4M3><<<ctas, kThreads, smem, s>>>(a, 1);
   return cudaGetLastError();
 }
 

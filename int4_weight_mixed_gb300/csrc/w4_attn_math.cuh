@@ -13,6 +13,8 @@ namespace {
 // (log2): probabilities reach 2^8, well within fp16, and sums are seldom
 // rescaled.
 constexpr float kSlack = 8.f;
+// log2 vs of a key that is none: far below any score, and still a number.
+constexpr float kNoKey = -0x1p120f;
 // Scales count as this at least where their logarithm is taken (a row of zeros
 // has scale 0; the cache's writer makes none smaller than this but that).
 constexpr float kLeastScale = 0x1p-100f;
@@ -99,6 +101,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
       "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;

@@ -43,8 +43,6 @@ constexpr int kConvWarp = 8, kConvWarps = 8, kIssueWarp = 16;
 // registers a thread after the split: 2 * 128 + 2 * 72 + 80 = 480 = 5 * 96 launched
 constexpr int kTcRegs = 96, kSoftRegs = 128, kConvRegs = 72, kIssueRegs = 80;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kIssueRegs <= 5 * kTcRegs, "register split");
-// log2 vs of a key that is none: far below any score, and still a number
-constexpr float kNoKey = -0x1p120f;
 // a warp's 32 rows by 32 columns of the result on their way out: 64 bytes a row,
 // rows 80 bytes apart (16-byte accesses of eight rows hit different banks)
 constexpr int kOutRow = 80, kOutBytes = 32 * kOutRow;
@@ -1219,7 +1217,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) attn_unpack_kernel(const __gr
 
 // Adds up the units that were cut between CTAs, in the order of the CTAs: a
 // block takes a share of the rows of the unit that began in CTA blockIdx.x.
-constexpr int kReduceThreads = 256, kReduceShare = 16;
+constexpr int kReduceThreads = 256, kReduceShare = kTcRows / 32;
 template <int D>
 __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs a, int ctas) {
   const int c0 = blockIdx.x;
@@ -1229,13 +1227,20 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
   const Sequence s = sequence(a.c, a.b, cut.b);
   const int group = a.heads / a.c.heads;
   const int r0 = cut.rt * kTcRows, nr = min(kTcRows, s.n * group - r0);
-  // a warp takes 32 rows of one chunk of four columns
-  const int lane = threadIdx.x & 31;
-  const int tasks = (nr + 31) / 32 * (D / 4);
-  for (int i = blockIdx.y * (kReduceThreads / 32) + (threadIdx.x >> 5); i < tasks;
-       i += kReduceShare * (kReduceThreads / 32)) {
-    const int c = i % (D / 4), r = i / (D / 4) * 32 + lane;
-    if (r >= nr) continue;
+  // 32 rows a block: a warp takes some of their chunks of four columns, a row a lane;
+  // then, through shared memory, whole rows
+  __shared__ uint2 out[32][D / 4 + 1];
+  __shared__ uint64_t to[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = 32 * blockIdx.y, r = first + lane;
+  if (first >= nr) return;
+  if (warp == 0) {
+    const int flat = r0 + min(r, nr - 1), token = flat / group;
+    to[lane] = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(a.out) +
+                                          ((static_cast<int64_t>(s.row0) + token) * a.heads + cut.h * group +
+                                           flat - token * group) * D);
+  }
+  for (int c = warp; r < nr && c < D / 4; c += kReduceThreads / 32) {
     float top = -INFINITY, sum_l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kAhead = 4;
@@ -1255,10 +1260,10 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const float to = fmaxf(top, ml[k].x);
-        const float from = to == -INFINITY ? 0.f : to;
+        const float up = fmaxf(top, ml[k].x);
+        const float from = up == -INFINITY ? 0.f : up;
         const float f = ex2(top - from), fk = ex2(ml[k].x - from);
-        top = to;
+        top = up;
         sum_l = sum_l * f + fk * ml[k].y;
         y.x = y.x * f + fk * x[k].x;
         y.y = y.y * f + fk * x[k].y;
@@ -1267,14 +1272,29 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
       }
     }
     const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
-    const int token = (r0 + r) / group, head = cut.h * group + (r0 + r) % group;
-    uint16_t* const to = static_cast<uint16_t*>(a.out) +
-                         ((static_cast<int64_t>(s.row0) + token) * a.heads + head) * D + 4 * c;
-    const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      to[k] = a.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(z[k]))
-                     : __half_as_ushort(__float2half_rn(z[k]));
+    uint2 u;
+    if (a.bf16) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(y.x * inv, y.y * inv);
+      const __nv_bfloat162 q = __floats2bfloat162_rn(y.z * inv, y.w * inv);
+      u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    } else {
+      const __half2 p = __floats2half2_rn(y.x * inv, y.y * inv);
+      const __half2 q = __floats2half2_rn(y.z * inv, y.w * inv);
+      u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+    }
+    out[lane][c] = u;
+  }
+  __syncthreads();
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
+  for (int i = threadIdx.x; i < min(32, nr - first) * (D / 4); i += kReduceThreads) {
+    const uint2 u = out[i / (D / 4)][i % (D / 4)];
+    uint16_t* const p = reinterpret_cast<uint16_t*>(to[i / (D / 4)]) + 4 * (i % (D / 4));
+    if (vec) {
+      *reinterpret_cast<uint2*>(p) = u;
+    } else {
+      p[0] = static_cast<uint16_t>(u.x), p[1] = static_cast<uint16_t>(u.x >> 16);
+      p[2] = static_cast<uint16_t>(u.y), p[3] = static_cast<uint16_t>(u.y >> 16);
+    }
   }
 }
 
