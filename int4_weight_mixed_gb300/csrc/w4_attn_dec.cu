@@ -37,11 +37,15 @@ constexpr int kKeys = 32;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
 
+// CTAs an SM: two for 128 dimensions (three spill registers: two contexts of
+// 131072 keys 83 us, with two 77), three for 64 (48 windows of 4096 57 us, 66).
+__host__ __device__ constexpr int ctas_per_sm(int dim) { return dim == 128 ? 2 : 3; }
+
 template <int D>
 struct Ring {
   static constexpr int kCodes = kKeys * D;                // bytes of one array
   static constexpr int kStage = 2 * kCodes + 2 * kKeys * 4;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 3 : 4;
   // then the factors of the stage in use: of pairs of keys ks, ks, log2 vs, log2 vs;
   // then of pairs 1 / vs
   static constexpr int kFactors = kStage * kStages;
@@ -65,7 +69,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -95,7 +99,7 @@ __device__ __forceinline__ int sum_chunk(int row, int c) {
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int least) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(AttnArgs a, int least) {
   using R = Ring<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Piece piece;
@@ -295,19 +299,24 @@ __global__ void __launch_bounds__(kThreads, 3) attn_dec_kernel(AttnArgs a, int l
 #pragma unroll
           for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t ww[4][4];
 #pragma unroll
           for (int nt = 0; nt < 4; ++nt) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(st + (nt >> 1) * 16 * D +
                                                              k_chunk<D>(8 * (nt & 1) + g, 4 * j + t4));
-            const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+            ww[nt][0] = w4.x, ww[nt][1] = w4.y, ww[nt][2] = w4.z, ww[nt][3] = w4.w;
+          }
+          // (the four blocks in turn: products of one block wait for each other)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
               uint32_t b0, b1;
-              codes4_f16<E4M3>(ww[q], b0, b1);
+              codes4_f16<E4M3>(ww[nt][q], b0, b1);
               mma16816(c[nt], qf[4 * j + q], b0, b1);
             }
-          }
+        }
         // this lane's keys: 2 t4, 2 t4 + 1 of the four blocks
         float2 rvs[4];
 #pragma unroll
@@ -560,13 +569,12 @@ cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-int attn_dec_ctas(int sms) { return 3 * sms; }
 size_t attn_dec_partials(int sms, int dim) {
-  return 2 * static_cast<size_t>(attn_dec_ctas(sms)) * (kRows * dim + 2 * kRows) * sizeof(float);
+  return 2 * static_cast<size_t>(ctas_per_sm(dim) * sms) * (kRows * dim + 2 * kRows) * sizeof(float);
 }
 
 cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s) {
-  const int ctas = attn_dec_ctas(sms);
+  const int ctas = ctas_per_sm(a.c.dim) * sms;
   if (a.c.dim == 128) return a.c.e4m3 ? launch<128, true>(a, ctas, s) : launch<128, false>(a, ctas, s);
   return a.c.e4m3 ? launch<64, true>(a, ctas, s) : launch<64, false>(a, ctas, s);
 }

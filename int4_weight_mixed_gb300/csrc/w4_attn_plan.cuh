@@ -59,6 +59,7 @@ struct Piece {
   int pieces;     // CTAs that have one
   int b, h, rt;   // the unit that `begin` lies in
   int at;         // tiles of it before `begin`
+  Sequence s;     // its sequence
 };
 
 __device__ __forceinline__ int64_t piece_begin(int64_t total, int pieces, int i) {
@@ -80,9 +81,10 @@ __device__ __forceinline__ void plan_piece(const AttnArgs& a, int least, Piece* 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = a.heads / a.c.heads, B = a.b.sequences;
   int64_t mine = 0;
+  Sequence s;
   const auto cost = [&](int i) -> int64_t {
-    if (i >= B) return 0;
-    return head_tiles<RT, TK>(a, sequence(a.c, a.b, i), group);
+    s = sequence(a.c, a.b, i);
+    return head_tiles<RT, TK>(a, s, group);
   };
   for (int i = tid; i < B; i += NT) mine += cost(i);
   int64_t all = mine;
@@ -111,7 +113,7 @@ __device__ __forceinline__ void plan_piece(const AttnArgs& a, int least, Piece* 
   int64_t run = 0;
   for (int base = 0; base < B; base += NT) {
     const int i = base + tid;
-    const int64_t per_head = B <= NT ? mine : cost(i);
+    const int64_t per_head = B <= NT ? mine : i < B ? cost(i) : 0;  // (s stays the one of i)
     const int64_t w = per_head * a.c.heads;
     int64_t to = w;  // inclusive sum
     for (int o = 1; o < 32; o <<= 1) {
@@ -132,7 +134,7 @@ __device__ __forceinline__ void plan_piece(const AttnArgs& a, int least, Piece* 
       p->b = i;
       p->h = static_cast<int>(div_nn(off, per_head));
       off -= p->h * per_head;
-      const Sequence s = sequence(a.c, a.b, i);
+      p->s = s;
       int rt = 0;
       for (;; ++rt) {
         const int n = unit_tiles<RT, TK>(a, s, group, rt).count;
@@ -161,7 +163,7 @@ struct Walk {
     b = p.b;
     h = p.h;
     rt = p.rt;
-    s = sequence(a.c, a.b, b);
+    s = p.s;
     t = unit_tiles<RT, TK>(a, s, a.heads / a.c.heads, rt);
     from = p.at;
     clip();
