@@ -1348,20 +1348,34 @@ struct AttnPlan {
   size_t partials, tiles;  // bytes
 };
 constexpr int64_t kMaxTileBytes = int64_t{256} << 20;
-AttnPlan attn_plan(const w4_kv_cache* cache, const w4_kv_batch* batch, int64_t rows, int heads) {
+// most: the plan that needs the most workspace, whatever the window.
+AttnPlan attn_plan(const w4_kv_cache* cache, const w4_kv_batch* batch, int64_t rows, int heads,
+                   int window, int sinks, bool most = false) {
   AttnPlan p{kAttnSimt, 0, 0, 0};
   const int dim = cache->head_dim;
   // (with no page there is no key, and the others load some key's row)
   if ((dim != 64 && dim != 128) || cache->pages == 0 || cache->heads <= 0) return p;
   const int sms = sm_count();
   p.partials = std::max(attn_dec_partials(sms, dim), attn_tc_partials(sms, dim));
-  // rows of a sequence and key head, on average: up to one tile of the decode
-  // kernel's, more go to the tensor cores
+  // The kernel with the less estimated time, from the longest a sequence can be (its
+  // line of the table; its window): the decode kernel reads a key head's codes for
+  // every 16 of its rows, at about 4.5 GB/ms; the tensor cores' has 35 us before and
+  // after, and an SM takes a tile of 128 keys by 256 rows in about 3.7 us (64
+  // dimensions: 2.2), half of it by 128.  (One tree of 64 drafts, 32 heads over 8, 2112
+  // keys: 32 us and 54; 32 trees of up to 48, 64 heads, 4096 keys: 680 and 282.)
   const int64_t lines = batch->sequences * cache->heads;
   const int64_t flat = rows * heads;
-  if (flat <= 16 * lines) {
-    p.engine = kAttnDec;
-    return p;
+  if (lines > 0) {
+    const double each_rows = std::ceil(static_cast<double>(flat) / lines);
+    double keys = static_cast<double>(batch->table_width) * cache->page_size;
+    if (window > 0) keys = std::min(keys, static_cast<double>(window) + sinks + each_rows);
+    const double dec = 8 + lines * std::ceil(each_rows / 16) * keys * (2 * dim) / 4.5e6;
+    const double tc = 35 + lines * std::ceil(each_rows / 128) / 2 * std::ceil(keys / 128) *
+                              (dim == 128 ? 3.7 : 2.2) / sms;
+    if (each_rows <= 16 || (!most && dec <= tc)) {
+      p.engine = kAttnDec;
+      return p;
+    }
   }
   p.engine = kAttnTc;
   const int64_t each = (batch->table_width * cache->page_size + 127) / 128;
@@ -1406,8 +1420,8 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.sinks = sinks;
   a.mask = mask;
   a.mask_width = mask_width;
-  const AttnPlan plan = attn_plan(cache, batch, rows, heads);
-  const size_t need = w4_attention_workspace_size(cache, batch, rows, heads);
+  const AttnPlan plan = attn_plan(cache, batch, rows, heads, a.window, a.sinks);
+  const size_t need = kWsHeader + kCounterBytes + align256(plan.partials) + plan.tiles;
   if (!workspace || workspace_bytes < need || !aligned16(workspace))
     return fail(W4_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is required", need);
   char* const ws = static_cast<char*>(workspace);
@@ -1701,7 +1715,7 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
 size_t w4_attention_workspace_size(const w4_kv_cache* cache, const w4_kv_batch* batch,
                                    int64_t rows, int heads) {
   if (!cache || !batch) return kWsHeader + kCounterBytes;
-  const AttnPlan p = attn_plan(cache, batch, rows, heads);
+  const AttnPlan p = attn_plan(cache, batch, rows, heads, 0, 0, true);
   return kWsHeader + kCounterBytes + align256(p.partials) + p.tiles;
 }
 

@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) attn_unpack_kernel(const __gr
 
 // Adds up the units that were cut between CTAs, in the order of the CTAs: a
 // block takes a share of the rows of the unit that began in CTA blockIdx.x.
-constexpr int kReduceThreads = 256, kReduceShare = kTcRows / 32;
+constexpr int kReduceThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs a, int ctas) {
   const int c0 = blockIdx.x;
@@ -1227,23 +1227,24 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
   const Sequence s = sequence(a.c, a.b, cut.b);
   const int group = a.heads / a.c.heads;
   const int r0 = cut.rt * kTcRows, nr = min(kTcRows, s.n * group - r0);
-  // 32 rows a block: a warp takes some of their chunks of four columns, a row a lane;
-  // then, through shared memory, whole rows
-  __shared__ uint2 out[32][D / 4 + 1];
+  // 32 rows by 32 columns a block (few units cut many times still make many blocks): a
+  // warp takes a chunk of four columns, a row a lane; then, through shared memory, 64
+  // bytes of a row
+  __shared__ uint2 out[32][9];
   __shared__ uint64_t to[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int first = 32 * blockIdx.y, r = first + lane;
+  const int first = 32 * blockIdx.y, r = first + lane, c = 8 * blockIdx.z + warp;
   if (first >= nr) return;
   if (warp == 0) {
     const int flat = r0 + min(r, nr - 1), token = flat / group;
     to[lane] = reinterpret_cast<uint64_t>(static_cast<uint16_t*>(a.out) +
                                           ((static_cast<int64_t>(s.row0) + token) * a.heads + cut.h * group +
-                                           flat - token * group) * D);
+                                           flat - token * group) * D + 32 * blockIdx.z);
   }
-  for (int c = warp; r < nr && c < D / 4; c += kReduceThreads / 32) {
+  if (r < nr) {
     float top = -INFINITY, sum_l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     for (int k0 = c0; k0 <= cut.last_cta; k0 += kAhead) {
       float4 x[kAhead];
       float2 ml[kAhead];
@@ -1282,13 +1283,14 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
       const __half2 q = __floats2half2_rn(y.z * inv, y.w * inv);
       u = make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
     }
-    out[lane][c] = u;
+    out[lane][warp] = u;
   }
   __syncthreads();
   const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
-  for (int i = threadIdx.x; i < min(32, nr - first) * (D / 4); i += kReduceThreads) {
-    const uint2 u = out[i / (D / 4)][i % (D / 4)];
-    uint16_t* const p = reinterpret_cast<uint16_t*>(to[i / (D / 4)]) + 4 * (i % (D / 4));
+  const int i = threadIdx.x >> 3, e = threadIdx.x & 7;
+  if (first + i < nr) {
+    const uint2 u = out[i][e];
+    uint16_t* const p = reinterpret_cast<uint16_t*>(to[i]) + 4 * e;
     if (vec) {
       *reinterpret_cast<uint2*>(p) = u;
     } else {
@@ -1318,7 +1320,7 @@ cudaError_t launch_tc_kernel(const AttnArgs& a, int sms, cudaStream_t s) {
     e = launch_tc_source<D, E4M3, BF16, kOwn>(a, sms, s);
   }
   if (e != cudaSuccess) return e;
-  attn_tc_reduce_kernel<D><<<dim3(sms, kReduceShare), kReduceThreads, 0, s>>>(a, sms);
+  attn_tc_reduce_kernel<D><<<dim3(sms, kTcRows / 32, D / 32), kReduceThreads, 0, s>>>(a, sms);
   return cudaGetLastError();
 }
 template <int D>

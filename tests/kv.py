@@ -29,15 +29,17 @@ def quantised(x, codes):
 
 class Batch:
     """rows[b] rows and lens[b] positions of each sequence, pages in no order,
-    the unused entries of the table no page's."""
+    the unused entries of the table no page's.  wide: a table with room for far
+    longer sequences, for which calls of more than 16 rows a key head go to the
+    tensor cores' kernel."""
 
-    def __init__(self, rows, lens, page, seed=0, spare=3, behind=0):
+    def __init__(self, rows, lens, page, seed=0, spare=3, behind=0, wide=False):
         self.rows, self.lens, self.page = list(rows), list(lens), page
         used = [-(-k // page) for k in lens]
         self.pages = sum(used) + spare
         order = list(range(self.pages))
         random.Random(seed).shuffle(order)
-        self.width = max([1, *used])
+        self.width = max([1 << 16 if wide else 1, *used])
         self.table = torch.full((len(rows), self.width), -1, dtype=torch.int32)
         at = 0
         for b, u in enumerate(used):

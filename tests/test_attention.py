@@ -34,8 +34,8 @@ def _tree(rows, width, seed=0, kind="tree"):
 
 
 def _check(rows, lens, Hq, Hkv, D, page, codes, dt, window=0, sinks=0, mask=None, scale=None,
-           seed=0, q=None, cache=None, batch=None, behind=2):
-    batch = batch or kv.Batch(rows, lens, page, seed, behind=behind)
+           seed=0, q=None, cache=None, batch=None, behind=2, wide=False):
+    batch = batch or kv.Batch(rows, lens, page, seed, behind=behind, wide=wide)
     cache = cache or kv.random_cache(batch, Hkv, D, codes, seed)
     g = torch.Generator().manual_seed(seed + 1)
     if q is None:  # queries as a slice of wider rows
@@ -80,11 +80,13 @@ def test_decode(gpu_lib, Hq, Hkv, D, dt, codes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16)])
 @pytest.mark.parametrize("page", [16, 32, 128, 256])
 @pytest.mark.parametrize("D", [64, 128])
-def test_pages(gpu_lib, page, D, codes, dt):
-    _check([1, 1, 3, 40], [page - 1, page + 1, 5 * page, 3 * page + 7], 4, 2, D, page, codes, dt)
+def test_pages(gpu_lib, page, D, codes, dt, wide):
+    _check([1, 1, 3, 40], [page - 1, page + 1, 5 * page, 3 * page + 7], 4, 2, D, page, codes, dt,
+           wide=wide)
 
 
 MIXED = {
@@ -96,22 +98,24 @@ MIXED = {
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16), (F8, torch.bfloat16),
                                       (S8, torch.float16)])
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 2, 64), (3, 3, 128), (16, 1, 64), (2, 1, 48)])
 @pytest.mark.parametrize("kind", list(MIXED))
-def test_mixed(gpu_lib, kind, Hq, Hkv, D, codes, dt):
-    _check(*MIXED[kind], Hq, Hkv, D, 32, codes, dt)
+def test_mixed(gpu_lib, kind, Hq, Hkv, D, codes, dt, wide):
+    _check(*MIXED[kind], Hq, Hkv, D, 32, codes, dt, wide=wide)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16)])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (129, 33), (64, 300),
                                           (1000, 4), (5000, 1)])
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (3, 1, 64), (2, 1, 80)])
-def test_window_and_sinks(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt):
+def test_window_and_sinks(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt, wide):
     _check([1, 1, 1, 150, 40, 20], [1, 130, 900, 150, 777, 1200], Hq, Hkv, D, 16, codes, dt, window,
-           sinks)
+           sinks, wide=wide)
 
 
 @pytest.mark.gpu
@@ -125,14 +129,16 @@ def test_window_and_sinks_of_chunks(gpu_lib, Hq, Hkv, D, window, sinks, codes, d
     _check([1, 300, 0, 128, 63], [900, 1000, 70, 128, 1999], Hq, Hkv, D, 64, codes, dt, window, sinks)
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("codes,dt", [(S8, torch.bfloat16), (F8, torch.float16)])
 @pytest.mark.parametrize("kind", ["tree", "any", "none"])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4), (3, 0)])
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (3, 1, 64), (2, 1, 112)])
-def test_tree(gpu_lib, Hq, Hkv, D, window, sinks, kind, codes, dt):
+def test_tree(gpu_lib, Hq, Hkv, D, window, sinks, kind, codes, dt, wide):
     rows = [1, 7, 64, 0, 33, 130, 4]
     lens = [1, 300, 600, 10, 33, 500, 2]
-    _check(rows, lens, Hq, Hkv, D, 16, codes, dt, window, sinks, _tree(rows, 130, kind=kind))
+    _check(rows, lens, Hq, Hkv, D, 16, codes, dt, window, sinks, _tree(rows, 130, kind=kind),
+           wide=wide)
 
 
 @pytest.mark.gpu
@@ -145,21 +151,23 @@ def test_large_trees(gpu_lib, Hq, Hkv, D, window, sinks, codes, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("width", [0, 1, 20, 200])
-def test_tree_masks_of_other_widths(gpu_lib, width):
+def test_tree_masks_of_other_widths(gpu_lib, width, wide):
     rows, lens = [5, 40], [77, 140]
-    _check(rows, lens, 4, 1, 64, 32, S8, torch.bfloat16, mask=_tree(rows, width))
+    _check(rows, lens, 4, 1, 64, 32, S8, torch.bfloat16, mask=_tree(rows, width), wide=wide)
 
 
 @pytest.mark.gpu
-def test_chain_is_causal(gpu_lib):
+@pytest.mark.parametrize("wide", [False, True])
+def test_chain_is_causal(gpu_lib, wide):
     """A tree that is one chain sees what the causal rows see: both within the
     bound of the causal definition."""
     rows, lens = [9, 30], [300, 64]
     mask = torch.cat([torch.ones(n, 30, dtype=torch.bool).tril() for n in rows])
     for codes, D in ((S8, 128), (F8, 64)):
-        a = _check(rows, lens, 8, 2, D, 16, codes, torch.bfloat16)
-        b = _check(rows, lens, 8, 2, D, 16, codes, torch.bfloat16, mask=mask)
+        a = _check(rows, lens, 8, 2, D, 16, codes, torch.bfloat16, wide=wide)
+        b = _check(rows, lens, 8, 2, D, 16, codes, torch.bfloat16, mask=mask, wide=wide)
         batch = kv.Batch(rows, lens, 16, behind=2)
         q = torch.randn(batch.T, 10 * D, generator=torch.Generator().manual_seed(1)) * 1.5
         q = q.bfloat16()[:, D:9 * D].reshape(batch.T, 8, D)
@@ -169,14 +177,15 @@ def test_chain_is_causal(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D,rows", [(128, 1), (64, 1), (128, 90), (64, 40), (96, 3)])
 @pytest.mark.parametrize("codes", [S8, F8])
-def test_scales_far_apart(gpu_lib, D, rows, codes):
+def test_scales_far_apart(gpu_lib, D, rows, codes, wide):
     """Values whose scales span twenty binary orders, values of zeros, keys of
     zeros, large scores: the probabilities are rounded relative to what they
     weigh."""
     for dt in (torch.float16, torch.bfloat16):
-        batch = kv.Batch([rows], [500], 32, behind=2)
+        batch = kv.Batch([rows], [500], 32, behind=2, wide=wide)
         cache = kv.random_cache(batch, 1, D, codes)
         g = torch.Generator().manual_seed(3)
         up = torch.exp2(torch.randint(-14, 7, cache.v_scales.shape, generator=g).float())
@@ -190,12 +199,13 @@ def test_scales_far_apart(gpu_lib, D, rows, codes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D,rows", [(128, 1), (128, 70), (64, 70), (32, 2)])
-def test_sizes_of_queries(gpu_lib, D, rows):
+def test_sizes_of_queries(gpu_lib, D, rows, wide):
     """Queries near the types' ends: large, small, zero rows, one channel far
     above the others."""
     for dt, sizes in ((torch.bfloat16, (1e-30, 1e-4, 1.0, 1e4)), (torch.float16, (1e-6, 1.0, 300.0))):
-        batch = kv.Batch([rows] * len(sizes), [130] * len(sizes), 32, behind=0)
+        batch = kv.Batch([rows] * len(sizes), [130] * len(sizes), 32, behind=0, wide=wide)
         cache = kv.random_cache(batch, 2, D, S8)
         g = torch.Generator().manual_seed(3)
         q = torch.randn(batch.T, 4, D, generator=g)
@@ -209,20 +219,22 @@ def test_sizes_of_queries(gpu_lib, D, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.25])
-def test_scale(gpu_lib, scale):
+def test_scale(gpu_lib, scale, wide):
     for D in (64, 32):
-        _check([1, 40], [90, 100], 4, 2, D, 16, S8, torch.float16, scale=scale)
+        _check([1, 40], [90, 100], 4, 2, D, 16, S8, torch.float16, scale=scale, wide=wide)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D,Hq", [(128, 4), (64, 16), (96, 2)])
 @pytest.mark.parametrize("codes", [S8, F8])
-def test_what_holds_nan_is_seen_by_its_rows_alone(gpu_lib, D, Hq, codes):
+def test_what_holds_nan_is_seen_by_its_rows_alone(gpu_lib, D, Hq, codes, wide):
     """A key or value written from an infinity or NaN makes the rows that see it
     NaN and no others."""
     n = 90
-    batch = kv.Batch([n, 1], [n, 50], 16, behind=0)
+    batch = kv.Batch([n, 1], [n, 50], 16, behind=0, wide=wide)
     dt = torch.bfloat16
     for which in ("k_scales", "v_scales"):
         cache = kv.random_cache(batch, 1, D, codes)
@@ -240,10 +252,11 @@ def test_what_holds_nan_is_seen_by_its_rows_alone(gpu_lib, D, Hq, codes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 48])
-def test_queries_of_nan(gpu_lib, D):
+def test_queries_of_nan(gpu_lib, D, wide):
     """A row of queries that holds one is NaN, the others are as without it."""
-    batch = kv.Batch([20, 1], [60, 90], 16, behind=0)
+    batch = kv.Batch([20, 1], [60, 90], 16, behind=0, wide=wide)
     cache = kv.on(kv.random_cache(batch, 2, D, S8), DEV)
     q = torch.randn(batch.T, 4, D).bfloat16()
     clean = w4.cache_attention(cache, q.to(DEV), *batch.plan(DEV)).cpu()
@@ -257,11 +270,12 @@ def test_queries_of_nan(gpu_lib, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 160])
-def test_same_bits_again(gpu_lib, D):
+def test_same_bits_again(gpu_lib, D, wide):
     """Runs of a call give the same bits (no sum's order is left to chance), on
     one workspace with calls of other shapes between them."""
-    batch = kv.Batch([1, 60, 3, 1], [5000, 900, 2000, 17], 32, behind=0)
+    batch = kv.Batch([1, 60, 3, 1], [5000, 900, 2000, 17], 32, behind=0, wide=wide)
     cache = kv.on(kv.random_cache(batch, 2, D, F8), DEV)
     q = torch.randn(batch.T, 16, D).half().to(DEV)
     small = kv.Batch([1], [100], 32, behind=0)
@@ -274,10 +288,11 @@ def test_same_bits_again(gpu_lib, D):
 @pytest.mark.gpu
 @pytest.mark.parametrize("D,n", [(64, 40), (128, 40), (80, 40), (128, 1), (64, 1), (128, 1300),
                                  (64, 1300)])
-def test_pages_that_are_none(gpu_lib, D, n):
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_that_are_none(gpu_lib, D, n, wide):
     """Keys of pages outside the cache are not seen; a row with no other is
     zeros; lengths beyond the table count as its end."""
-    batch = kv.Batch([1, 1, n], [64, 64, max(64, n)], 16, behind=0)
+    batch = kv.Batch([1, 1, n], [64, 64, max(64, n)], 16, behind=0, wide=wide)
     cache = kv.random_cache(batch, 1, D, S8)
     q = torch.randn(batch.T, 2, D).half()
     held = kv.on(cache, DEV)
@@ -286,7 +301,7 @@ def test_pages_that_are_none(gpu_lib, D, n):
     bad[0, :] = -1
     bad[1, 1] = batch.pages
     bad[2, 2] = 1 << 30
-    assert int(bad.shape[1]) == -(-max(64, n) // 16)
+    lens[1] = 2**31 - 1  # (the entries behind its four pages are none)
     got = w4.cache_attention(held, q.to(DEV), bad, starts, lens).cpu()
     assert bool((got[0] == 0).all())
     # the same with these pages' keys cut out
@@ -300,10 +315,11 @@ def test_pages_that_are_none(gpu_lib, D, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D,n", [(128, 1), (64, 1), (128, 64), (96, 2), (128, 390), (64, 200)])
-def test_captured_and_replayed(gpu_lib, D, n):
+def test_captured_and_replayed(gpu_lib, D, n, wide):
     """A captured call follows what its arrays hold when it is replayed."""
-    batch = kv.Batch([n, n], [n + 400, n + 300], 16, behind=0)
+    batch = kv.Batch([n, n], [n + 400, n + 300], 16, behind=0, wide=wide)
     cache = kv.random_cache(batch, 2, D, S8)
     held, (table, starts, lens) = kv.on(cache, DEV), batch.plan(DEV)
     q = torch.randn(batch.T, 4, D).half().to(DEV)
