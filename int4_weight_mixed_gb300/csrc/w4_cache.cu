@@ -14,6 +14,8 @@
 // values a lane: 16 bytes of them, 8 bytes of codes; a head's row is a group of
 // dim / 8 lanes, and consecutive groups of a warp take consecutive heads of a
 // row, which are contiguous on the 16-bit side.
+#include <type_traits>
+
 #include "w4_cache.cuh"
 #include "w4_quant.cuh"
 
@@ -22,7 +24,9 @@ namespace {
 
 constexpr int kCacheThreads = 256;
 constexpr int kCacheWarps = kCacheThreads / 32;
-constexpr int kMaxRows = 16;  // rows a CTA takes
+constexpr int kMaxRows = 32;  // rows a CTA takes
+// items (rows of a head) a thread has in flight
+constexpr int kDeep = 4;
 
 // A row that has no place: its position is before the first, or its page is
 // none of the cache's; and a row of no sequence.
@@ -44,6 +48,49 @@ __device__ __forceinline__ void find_places(const CacheView& c, const BatchView&
     }
     if ((threadIdx.x & 31) == 0) at[r] = p;
   }
+}
+
+// Item `it` of a CTA: row r, head and kind kvh = kv * heads + h; steps without
+// divisions.
+struct Item {
+  int r, kvh;
+  __device__ __forceinline__ void step(int by, int per_row) {
+    kvh += by;
+    while (kvh >= per_row) {
+      kvh -= per_row;
+      ++r;
+    }
+  }
+};
+
+// The E4M3 codes of f / s, fl(f / s) to the nearest (ties to even): p = f * (1 / s) is
+// within 2^-22 of the quotient, relatively, so it has the quotient's code unless it
+// is within four units in the last place of a point halfway between two E4M3 values,
+// the low 20 bits of whose pattern are 0x80000 (values from 2^-6 on).  Those few,
+// and smaller values but 0, are divided.
+__device__ __forceinline__ uint2 codes8_e4m3(const float (&f)[8], float s) {
+  const float r = __frcp_rn(s);
+  float p[8];
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    p[e] = __fmul_rn(f[e], r);
+    near |= ((__float_as_uint(p[e]) - (0x80000u - 4u)) & 0xFFFFFu) <= 8u ||
+            (fabsf(p[e]) < 0x1p-6f && p[e] != 0.f);
+  }
+  if (near) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __fdiv_rn(f[e], s);
+  }
+  uint32_t o[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(p[4 * h + 1]), "f"(p[4 * h]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(p[4 * h + 3]), "f"(p[4 * h + 2]));
+    o[h] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+  }
+  return make_uint2(o[0], o[1]);
 }
 
 // Eight 16-bit values; 16 bytes at once where every row allows it.
@@ -88,55 +135,62 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int H = a.c.heads, D = a.c.dim;
   const int groups = kCacheThreads / lanes;
   const int d = 8 * (threadIdx.x & (lanes - 1));
-  const int items = count * 2 * H;
+  const int items = count * 2 * H, first = threadIdx.x / lanes;
+  Item next{first / (2 * H), first % (2 * H)};
   // (every thread of a warp makes every turn: the shuffles take whole warps)
   const int turns = (items + groups - 1) / groups;
-  for (int turn = 0, it = threadIdx.x / lanes; turn < turns; ++turn, it += groups) {
-    const int r = it / (2 * H), kv = it / H & 1, h = it % H;
-    const bool mine = it < items && d < D;
-    const int64_t p = mine ? at[r] : kNoPlace;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (p >= 0) {
-      const T* src = static_cast<const T*>(kv ? a.v : a.k) +
-                     (row0 + r) * (kv ? a.v_stride : a.k_stride) + h * D + d;
-      x = load8(src, vec != 0);
-    }
-    // a NaN or an infinity survives as one larger than any number
-    float amax = amax_nan<T>(x);
-    if (!(amax < INFINITY)) amax = INFINITY;
-    for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (p < 0) continue;
-    float s = __fmul_rn(amax, E4M3 ? 1.f / 448.f : 1.f / 127.f);
-    const bool live = s >= 0x1p-100f && amax < INFINITY;
-    if (!live) s = amax < INFINITY ? 0.f : NAN;
-    float f[8];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  for (int turn = 0; turn < turns; turn += kDeep) {
+    uint4 x[kDeep];
+    int64_t to[kDeep];
+    int kv[kDeep];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = pair_f32<T>(w[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-    uint2 o = make_uint2(0, 0);
-    if (live) {
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o.x |= code_e4m3(f[e], s) << (8 * e);
-          o.y |= code_e4m3(f[4 + e], s) << (8 * e);
-        }
-      } else {
-        float t[8];
-        codes8_s8(f, s, __frcp_rn(s), true, t);
-        o.x = pack4_s8(__float_as_int(t[0]), __float_as_int(t[1]), __float_as_int(t[2]),
-                       __float_as_int(t[3]));
-        o.y = pack4_s8(__float_as_int(t[4]), __float_as_int(t[5]), __float_as_int(t[6]),
-                       __float_as_int(t[7]));
+    for (int i = 0; i < kDeep; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      to[i] = kNoPlace;
+      kv[i] = next.kvh >= H;
+      if (next.r < count && d < D && at[next.r] >= 0) {
+        const int h = kv[i] ? next.kvh - H : next.kvh;
+        const T* const src = static_cast<const T*>(kv[i] ? a.v : a.k) +
+                             static_cast<int64_t>(row0 + next.r) * (kv[i] ? a.v_stride : a.k_stride) + h * D + d;
+        x[i] = load8(src, vec != 0);
+        to[i] = at[next.r] + (static_cast<int64_t>(h) << a.c.page_shift);
       }
+      next.step(groups, 2 * H);
     }
-    const int64_t to = p + (static_cast<int64_t>(h) << a.c.page_shift);
-    *reinterpret_cast<uint2*>((kv ? a.c.v : a.c.k) + to * D + d) = o;
-    if (d == 0) (kv ? a.c.v_scales : a.c.k_scales)[to] = s;
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      // a NaN or an infinity survives as one larger than any number
+      float amax = amax_nan<T>(x[i]);
+      if (!(amax < INFINITY)) amax = INFINITY;
+      for (int o = lanes >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (to[i] < 0) continue;
+      float s = __fmul_rn(amax, E4M3 ? 1.f / 448.f : 1.f / 127.f);
+      const bool live = s >= 0x1p-100f && amax < INFINITY;
+      if (!live) s = amax < INFINITY ? 0.f : NAN;
+      float f[8];
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = pair_f32<T>(w[k]);
+        f[2 * k] = v.x;
+        f[2 * k + 1] = v.y;
+      }
+      uint2 o = make_uint2(0, 0);
+      if (live) {
+        if constexpr (E4M3) {
+          o = codes8_e4m3(f, s);
+        } else {
+          float t[8];
+          codes8_s8(f, s, __frcp_rn(s), true, t);
+          o.x = pack4_s8(__float_as_int(t[0]), __float_as_int(t[1]), __float_as_int(t[2]),
+                         __float_as_int(t[3]));
+          o.y = pack4_s8(__float_as_int(t[4]), __float_as_int(t[5]), __float_as_int(t[6]),
+                         __float_as_int(t[7]));
+        }
+      }
+      *reinterpret_cast<uint2*>((kv[i] ? a.c.v : a.c.k) + to[i] * D + d) = o;
+      if (d == 0) (kv[i] ? a.c.v_scales : a.c.k_scales)[to[i]] = s;
+    }
   }
 }
 
@@ -151,40 +205,54 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int H = a.c.heads, D = a.c.dim;
   const int groups = kCacheThreads / lanes;
   const int d = 8 * (threadIdx.x & (lanes - 1));
-  const int items = count * 2 * H;
   if (d >= D) return;
-  for (int it = threadIdx.x / lanes; it < items; it += groups) {
-    const int r = it / (2 * H), kv = it / H & 1, h = it % H;
-    const int64_t p = at[r];
-    if (p == kNoSequence) continue;
-    uint2 c = make_uint2(0, 0);
-    float s = 0.f;
-    if (p >= 0) {
-      const int64_t from = p + (static_cast<int64_t>(h) << a.c.page_shift);
-      c = __ldg(reinterpret_cast<const uint2*>((kv ? a.c.v : a.c.k) + from * D + d));
-      s = __ldg((kv ? a.c.v_scales : a.c.k_scales) + from);
-    }
-    uint32_t o[4];
+  const int first = threadIdx.x / lanes;
+  Item next{first / (2 * H), first % (2 * H)};
+  while (next.r < count) {
+    uint2 c[kDeep];
+    float s[kDeep];
+    uint16_t* to[kDeep];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 v = codes2_f32<E4M3>((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
-      v.x *= s;
-      v.y *= s;
-      if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
-        const __half2 y = __floats2half2_rn(v.x, v.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
-      } else {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+    for (int i = 0; i < kDeep; ++i) {
+      c[i] = make_uint2(0, 0);
+      s[i] = 0.f;
+      to[i] = nullptr;
+      if (next.r < count && at[next.r] != kNoSequence) {
+        const int64_t p = at[next.r];
+        const bool kv = next.kvh >= H;
+        const int h = kv ? next.kvh - H : next.kvh;
+        if (p >= 0) {
+          const int64_t from = p + (static_cast<int64_t>(h) << a.c.page_shift);
+          c[i] = __ldg(reinterpret_cast<const uint2*>((kv ? a.c.v : a.c.k) + from * D + d));
+          s[i] = __ldg((kv ? a.c.v_scales : a.c.k_scales) + from);
+        }
+        to[i] = static_cast<uint16_t*>(kv ? a.v : a.k) + (static_cast<int64_t>(row0 + next.r) * H + h) * D + d;
       }
+      next.step(groups, 2 * H);
     }
-    uint16_t* dst = static_cast<uint16_t*>(kv ? a.v : a.k) +
-                    (static_cast<int64_t>(row0 + r) * H + h) * D + d;
-    if (vec) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < kDeep; ++i) {
+      if (!to[i]) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 v = codes2_f32<E4M3>((k < 2 ? c[i].x : c[i].y) >> (16 * (k & 1)));
+        v.x *= s[i];
+        v.y *= s[i];
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 y = __floats2half2_rn(v.x, v.y);
+          o[k] = *reinterpret_cast<const uint32_t*>(&y);
+        } else {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y);
+          o[k] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      if (vec) {
+        *reinterpret_cast<uint4*>(to[i]) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[i][k] = static_cast<uint16_t>(o[k >> 1] >> (16 * (k & 1)));
+      }
     }
   }
 }
