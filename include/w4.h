@@ -467,7 +467,8 @@ w4_status w4_cache_write(const w4_kv_cache* cache, const w4_kv_batch* batch, con
 
 /* Read the rows' keys and values back: k, v [rows, heads, head_dim] of `type`,
  * contiguous, code * scale rounded once.  Rows without a position or page are
- * zeros.  Errors as w4_cache_write, and outputs that overlap. */
+ * zeros.  Errors as w4_cache_write, and INVALID_ARGUMENT for an output that
+ * overlaps the other or the cache. */
 w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void* k, void* v,
                         int type, int64_t rows, void* stream);
 
@@ -486,11 +487,12 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  *        16-byte aligned, zero-filled before its first use, not shared by calls
  *        that overlap on the GPU; it may be the one of the products.
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
- * statistics and sums are fp32, and the probabilities (of at most 1, times the
- * value's scale over the row's largest) are rounded to fp16 before the product
- * with the values.  Errors as w4_cache_write, plus INVALID_ARGUMENT
+ * statistics and sums are fp32, and each key's probability times its value's
+ * scale is rounded to fp16 (relative to the row's largest) before the product
+ * with the values' codes.  Errors as w4_cache_write, plus INVALID_ARGUMENT
  * for heads not a multiple of the cache's, a scale that is not finite, negative
- * sinks, or out overlapping q; WORKSPACE. */
+ * sinks, or out overlapping q or the cache; UNSUPPORTED for heads above 65535 or
+ * rows * heads above 2^30; WORKSPACE. */
 size_t w4_attention_workspace_size(const w4_kv_cache* cache, const w4_kv_batch* batch,
                                    int64_t rows, int heads);
 w4_status w4_cache_attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const void* q,

@@ -1338,6 +1338,13 @@ w4_status cache_views(const w4_kv_cache* cache, const w4_kv_batch* batch, int ty
   return W4_OK;
 }
 
+// Whether an output shares a byte with one of the cache's arrays.
+bool overlaps_cache(const w4_kv_cache* c, const void* out, size_t bytes) {
+  const size_t slots = static_cast<size_t>(c->pages) * c->heads * c->page_size;
+  return overlap(out, bytes, c->k, slots * c->head_dim) || overlap(out, bytes, c->v, slots * c->head_dim) ||
+         overlap(out, bytes, c->k_scales, slots * 4) || overlap(out, bytes, c->v_scales, slots * 4);
+}
+
 // Which kernel attends, and (tensor cores) whether the visible keys and values are
 // unpacked to 16 bits first, each tile of 128 keys once (tiles_each: tiles of a
 // sequence and key head), instead of by every unit of 256 rows that visits it.
@@ -1401,6 +1408,7 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   const int64_t dense = static_cast<int64_t>(heads) * cache->head_dim;
   if (q_stride < dense && rows > 1)
     return fail(W4_ERR_INVALID_ARGUMENT, "q_stride is below heads * head_dim");
+  if (heads > 65535) return fail(W4_ERR_UNSUPPORTED, "more than 65535 heads");
   if (rows * static_cast<int64_t>(heads) > (int64_t{1} << 30))
     return fail(W4_ERR_UNSUPPORTED, "more than 2^30 rows times heads");
   if (rows == 0 || batch->sequences == 0) return W4_OK;
@@ -1410,6 +1418,8 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   if (overlap(out, static_cast<size_t>(rows) * dense * 2, q,
               (static_cast<size_t>(rows - 1) * q_stride + dense) * 2))
     return fail(W4_ERR_INVALID_ARGUMENT, "out overlaps q");
+  if (overlaps_cache(cache, out, static_cast<size_t>(rows) * dense * 2))
+    return fail(W4_ERR_INVALID_ARGUMENT, "out overlaps the cache");
   a.q = q;
   a.q_stride = q_stride;
   a.out = out;
@@ -1704,7 +1714,8 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
   if (!aligned_to(k, 2) || !aligned_to(v, 2))
     return fail(W4_ERR_INVALID_ARGUMENT, "k or v is not aligned to its element size");
   const size_t bytes = static_cast<size_t>(rows) * cache->heads * cache->head_dim * 2;
-  if (overlap(k, bytes, v, bytes)) return fail(W4_ERR_INVALID_ARGUMENT, "k and v overlap");
+  if (overlap(k, bytes, v, bytes) || overlaps_cache(cache, k, bytes) || overlaps_cache(cache, v, bytes))
+    return fail(W4_ERR_INVALID_ARGUMENT, "an output overlaps the other or the cache");
   a.k = k;
   a.v = v;
   a.bf16 = type == W4_BF16;

@@ -345,6 +345,52 @@ def test_captured_and_replayed(gpu_lib, D, n, wide):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,wide", [(1, False), (40, False), (40, True), (900, False)])
+def test_rows_before_the_first_sequence(gpu_lib, n, wide):
+    """starts[0] rows belong to no sequence: left as they were."""
+    batch = kv.Batch([n, 3], [n + 50, 90], 16, behind=0, wide=wide)
+    cache = kv.random_cache(batch, 2, 128, S8)
+    q = torch.randn(batch.T + 5, 8, 128).half()
+    table, starts, lens = batch.plan(DEV)
+    out = torch.full((batch.T + 5, 8, 128), 7.0, dtype=torch.float16, device=DEV)
+    held = kv.on(cache, DEV)
+    w4.cache_attention(held, q.to(DEV), table, starts + 5, lens, out=out)
+    assert bool((out[:5] == 7.0).all())
+    ref, bound = kv.attention(q[5:], cache, batch)
+    assert bool(((out[5:].cpu().double() - ref).abs() <= bound).all())
+    k, v = w4.cache_read(held, table, starts + 5, lens, batch.T + 5, torch.float16)
+    k0, v0 = w4.cache_read(held, table, starts, lens, batch.T, torch.float16)
+    assert torch.equal(k[5:], k0) and torch.equal(v[5:], v0)
+
+
+@pytest.mark.gpu
+def test_two_host_threads(gpu_lib):
+    """Calls of two host threads on one stream with its cached workspace give what
+    each gives alone."""
+    import threading
+    jobs = []
+    for n, k, D in ((1, 700, 128), (300, 900, 128), (60, 2000, 64), (1, 3000, 64)):
+        batch = kv.Batch([n, n], [k, k - 200], 16, behind=0)
+        held = kv.on(kv.random_cache(batch, 2, D, S8), DEV)
+        args = (held, torch.randn(batch.T, 16, D).half().to(DEV), *batch.plan(DEV))
+        jobs.append((args, w4.cache_attention(*args)))
+    torch.cuda.synchronize()
+    start, wrong = threading.Barrier(2), []
+
+    def work(mine):
+        start.wait()
+        outs = [(w4.cache_attention(*args), ref) for _ in range(30) for args, ref in mine]
+        wrong.extend(i for i, (out, ref) in enumerate(outs) if not torch.equal(out, ref))
+
+    threads = [threading.Thread(target=work, args=(jobs[i::2],)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@pytest.mark.gpu
 def test_layer_step(gpu_lib):
     """The calls together as a serving step makes them: prompts, then tokens one
     by one, then a tree whose accepted path is written again; against attention
@@ -422,6 +468,7 @@ INVALID, UNSUPPORTED = w4.ERR_INVALID_ARGUMENT, w4.ERR_UNSUPPORTED
     (dict(out=None), INVALID), (dict(q=8 * P + 1), INVALID), (dict(out=9 * P + 1), INVALID),
     (dict(out=8 * P), INVALID), (dict(out=8 * P + 1024), INVALID), (dict(ws=None), w4.ERR_WORKSPACE),
     (dict(ws=0x40000008), w4.ERR_WORKSPACE), (dict(nws=256), w4.ERR_WORKSPACE),
+    (dict(out=P + 256), INVALID), (dict(out=3 * P), INVALID), (dict(heads=65536, stride=1 << 23), UNSUPPORTED),
     (dict(rows=1 << 29), UNSUPPORTED), (dict(cache=_cache(page_size=24)), UNSUPPORTED),
     (dict(cache=_cache(head_dim=40)), UNSUPPORTED), (dict(batch=_of(starts=None)), INVALID)])
 @pytest.mark.parametrize("tree", [False, True])
@@ -432,6 +479,29 @@ def test_refused(kw, status, tree):
 def test_refused_masks():
     assert _attend(tree=True, mask=None) == INVALID
     assert _attend(tree=True, mask=7 * P, width=-1) == INVALID
+
+
+def test_another_gpu(monkeypatch):
+    """The extension module leaves calls on another GPU's tensors to be made again
+    with that GPU current."""
+    w4.build()
+    w4._load_host()
+    asked = []
+
+    class Elsewhere:
+        def __getattr__(self, name):
+            return lambda *args: NotImplemented
+
+    monkeypatch.setattr(w4, "_host", Elsewhere())
+    monkeypatch.setattr(w4, "_there", lambda dev, call, args: asked.append(dev) or "done")
+    cache = w4.kv_cache(2, 1, 16, 64, device="cpu")
+    x = torch.zeros(1, 1, 64, dtype=torch.float16)
+    plan = [torch.zeros(*z, dtype=torch.int32) for z in ((1, 1), (2,), (1,))]
+    w4.cache_write(cache, x, x, *plan)
+    assert w4.cache_read(cache, *plan, 1) == "done"
+    assert w4.cache_attention(cache, x, *plan) == "done"
+    assert w4.tree_attention(cache, x, torch.ones(1, 1, dtype=torch.bool), *plan) == "done"
+    assert asked == [x.device] * 4
 
 
 def test_nothing_to_do():

@@ -267,6 +267,7 @@ def test_refused(call, kw, status):
 def test_refused_strides_and_overlap():
     assert _write(ks=127) == INVALID and _write(vs=0) == INVALID
     assert _read(v=8 * P + 256) == INVALID
+    assert _read(k=P + 512) == INVALID and _read(v=4 * P + 64) == INVALID
     lib = w4.load()
     assert lib.w4_cache_write(None, ctypes.byref(_of()), P, P, w4.F16, 1, 128, 128, None) == INVALID
     assert lib.w4_cache_read(ctypes.byref(_cache()), None, P, P, w4.F16, 1, None) == INVALID
