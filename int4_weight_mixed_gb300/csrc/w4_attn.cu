@@ -1,5 +1,7 @@
 // w4_attn.cu — attention over the paged key-value cache on the CUDA cores: any
-// head dimension the cache takes.
+// head dimension the cache takes, for those without a kernel on the tensor cores
+// (a correctness path: 64 sequences of up to 8192 positions, 8 key heads of 128, take
+// 5.5 ms here).
 //
 // For row i of a sequence and its visible keys j,
 //   t_j = (q_i . k_j) * scale * log2 e,   out_i = sum_j 2^(t_j - m) v_j / sum_j 2^(t_j - m)
