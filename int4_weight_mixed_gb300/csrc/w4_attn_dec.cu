@@ -4,9 +4,11 @@
 // 128 dimensions).  64 sequences of up to 8192 positions, 8 key heads of 128: 144 us,
 // 4.5 TB/s; two of 131072: 77 us, 4.7 TB/s; one of 1500: 10 us, latency.
 //
-// A unit is 16 rows (query heads of a key head, of one token or a few) by the
+// A unit is 8 or 16 rows (query heads of a key head, of one token or a few) by the
 // key tiles they see; four warps of a CTA take 32 keys each of a 128-key tile.
-// mma.sync m16n8k16 in fp16, both kinds of codes being exact there:
+// mma.sync m16n8k16 in fp16, both kinds of codes being exact there, with keys (for
+// the sums, dimensions) as its 16 rows and the unit's rows as its 8 columns: a decode
+// step's few rows leave none of it empty.
 //
 //   t_j = (q . code_j) * (scale * log2 e * ks_j) + log2 vs_j
 //   p_j = 2^(t_j - m) <= 2^8,  m a running maximum of t
@@ -23,7 +25,8 @@
 // (cp.async, 16 bytes a lane) and meets the others only at the unit's end.
 // Positions are read in any order within an MMA, so that a lane loads 16
 // neighbouring codes at once: for scores they are consecutive k of its key's
-// row, for sums consecutive columns of its four keys, whose bytes PRMT pairs.
+// row, for sums consecutive dimensions of its four keys, whose bytes PRMT pairs.
+// Probabilities come out a key a lane and are transposed by movmatrix.
 // Slots behind the sequence's end and pages that are none are not read: zeros
 // stand for their codes, and log2 vs = kNoKey for their scales.
 #include <cuda_bf16.h>
@@ -34,30 +37,27 @@
 namespace w4 {
 namespace {
 
-constexpr int kRows = 16;          // rows of a unit
 constexpr int kWarps = 4;
 constexpr int kKeys = 32;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
 
-// CTAs an SM: two for 128 dimensions (three spill registers: two contexts of
-// 131072 keys 83 us, with two 77), three for 64 (48 windows of 4096 57 us, 66).
-__host__ __device__ constexpr int ctas_per_sm(int dim) { return dim == 128 ? 2 : 3; }
+// CTAs an SM: two for 16 rows of 128 dimensions (three spill registers), else three.
+__host__ __device__ constexpr int ctas_per_sm(int dim, int nt) { return dim == 128 && nt == 2 ? 2 : 3; }
 
-template <int D>
+template <int D, int NT>
 struct Ring {
   static constexpr int kCodes = kKeys * D;                // bytes of one array
   static constexpr int kStage = 2 * kCodes + 2 * kKeys * 4;
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  // then the factors of the stage in use: of pairs of keys ks, ks, log2 vs, log2 vs;
-  // then of pairs 1 / vs
+  static constexpr int kStages = D == 64 ? 4 : NT == 2 ? 3 : 2;
+  // then the factors of the stage in use: of a key ks, log2 vs, 1 / vs
   static constexpr int kFactors = kStage * kStages;
-  static constexpr int kWarp = kFactors + kKeys * 12;
+  static constexpr int kWarp = kFactors + kKeys * 16;
 };
-template <int D>
+template <int D, int NT>
 constexpr size_t smem_bytes() {
-  constexpr size_t ring = static_cast<size_t>(Ring<D>::kWarp) * kWarps;
-  constexpr size_t sums = static_cast<size_t>(kWarps) * kRows * D * 4;
+  constexpr size_t ring = static_cast<size_t>(Ring<D, NT>::kWarp) * kWarps;
+  constexpr size_t sums = static_cast<size_t>(kWarps) * 8 * NT * D * 4;
   return ring > sums ? ring : sums;
 }
 
@@ -70,13 +70,19 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+// Transposes an 8 x 8 matrix of 16-bit values, a row's pair a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Where 16-byte chunk c of key `key` (of the stage's 16) lies within an array's
 // bytes, so that the lanes of a 16-byte (8-byte: values of 64) access hit
@@ -93,17 +99,19 @@ __device__ __forceinline__ uint32_t v_chunk(int key, int c) {
   else
     return (key >> 1) * 128 + ((key ^ key >> 1) & 1) * 64 + ((c ^ (key >> 2 & 1) << 1) << 4);
 }
-// The place of 16-byte chunk c of a row of sums, by the same token (a lane's
-// columns are D / 8 neighbouring ones).
+// The place of 16-byte chunk c of a row of sums, by the same token: lanes write D / 8
+// neighbouring dimensions of every other row.
 template <int D>
 __device__ __forceinline__ int sum_chunk(int row, int c) {
-  const int x = D == 128 ? (c >> 3 & 3) | (row & 1) << 2 : (c >> 3 & 1) | (row & 1) << 1;
-  return row * (D / 4) + ((c & ~7) | ((c & 7) ^ x));
+  const int t = row >> 1 & 3;
+  const int x = D == 128 ? t : (t & 1) | (t & 2) << 1;
+  return row * (D / 4) + (c ^ x);
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(AttnArgs a, int least) {
-  using R = Ring<D>;
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(AttnArgs a, int least) {
+  using R = Ring<D, NT>;
+  constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Piece piece;
   __shared__ float part_m[kWarps][kRows], part_l[kWarps][kRows];
@@ -135,26 +143,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
       __syncthreads();
     }
 
-    // the two rows of this lane: what they see, their queries
-    int hi[2], lo[2];
-    const uint8_t* mask[2];
-    float rf[2];  // scale of a row's scores
-    uint32_t qf[D / 16][4];
+    // queries of row 8 e + g, as fp16 times a power of two; the scale of its scores
+    float row_rf[NT];
+    uint32_t qf[NT][D / 16][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < NT; ++e) {
       const int r = g + 8 * e;
-      hi[e] = lo[e] = 0;
-      mask[e] = nullptr;
       float x[D / 4];
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
       if (r < nr) {
         const int token = (r0 + r) / group, head = w.h * group + (r0 + r) % group;
-        const int pos = a.mask ? position[token - r0 / group] : s.prefix + token;
-        const Visible v = visible(pos, a.mask ? s.len : min(s.len, pos + 1), a.window, a.sinks);
-        hi[e] = v.hi;
-        lo[e] = v.lo;
-        if (a.mask) mask[e] = a.mask + (static_cast<int64_t>(s.row0) + token) * a.mask_width;
         const uint16_t* q = static_cast<const uint16_t*>(a.q) +
                             (static_cast<int64_t>(s.row0) + token) * a.q_stride + head * D;
         const bool vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0;
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
       const int E = __float_as_int(top) >> 23;
       const int up = E == 255 ? 127 : min(max(254 - E, 1), 253);
       const float grow = __int_as_float(up << 23);
-      rf[e] = a.scale * 1.44269504f * __int_as_float((254 - up) << 23);
+      row_rf[e] = a.scale * 1.44269504f * __int_as_float((254 - up) << 23);
 #pragma unroll
       for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -199,9 +198,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
           const int o = 16 * j + 4 * i;
           const __half2 p0 = __floats2half2_rn(x[o] * grow, x[o + 1] * grow);
           const __half2 p1 = __floats2half2_rn(x[o + 2] * grow, x[o + 3] * grow);
-          qf[4 * j + i][e] = *reinterpret_cast<const uint32_t*>(&p0);
-          qf[4 * j + i][2 + e] = *reinterpret_cast<const uint32_t*>(&p1);
+          qf[e][4 * j + i][0] = *reinterpret_cast<const uint32_t*>(&p0);
+          qf[e][4 * j + i][1] = *reinterpret_cast<const uint32_t*>(&p1);
         }
+    }
+    // this lane's rows of the scores, 8 e + 2 t4 + i: what they see
+    int hi[NT][2], lo[NT][2];
+    const uint8_t* mask[NT][2];
+    float2 rf[NT];
+#pragma unroll
+    for (int e = 0; e < NT; ++e) {
+      rf[e].x = __shfl_sync(0xffffffffu, row_rf[e], 8 * t4);
+      rf[e].y = __shfl_sync(0xffffffffu, row_rf[e], 8 * t4 + 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * e + 2 * t4 + i;
+        hi[e][i] = lo[e][i] = 0;
+        mask[e][i] = nullptr;
+        if (r < nr) {
+          const int token = (r0 + r) / group;
+          const int pos = a.mask ? position[token - r0 / group] : s.prefix + token;
+          const Visible v = visible(pos, a.mask ? s.len : min(s.len, pos + 1), a.window, a.sinks);
+          hi[e][i] = v.hi;
+          lo[e][i] = v.lo;
+          if (a.mask) mask[e][i] = a.mask + (static_cast<int64_t>(s.row0) + token) * a.mask_width;
+        }
+      }
     }
     // keys that every row sees: [lo_all, hi_all) and below `sinks`
     int hi_all, lo_all;
@@ -213,13 +235,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
       lo_all = a.window > 0 ? s.prefix + (r0 + nr - 1) / group - a.window + 1 : 0;
     }
 
-    float m[2] = {-INFINITY, -INFINITY};
-    float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // of even and odd keys
-    float o[D / 8][4];
+    float m[NT][2];
+    float2 l[NT];  // of rows 2 t4 and 2 t4 + 1, this lane's keys
+    float o[NT][D / 16][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int e = 0; e < NT; ++e) {
+      m[e][0] = m[e][1] = -INFINITY;
+      l[e] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[e][i][k] = 0.f;
+    }
 
     // the pages of this warp's two groups of 16 keys in a tile, looked up 16 tiles at
     // a time: lane 2 i + n has that of group n of tile base + i
@@ -289,106 +316,122 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
           const bool in = (lane < 16 ? page0 : page1) >= 0 && key0 + lane < s.len;
           const float ks = sc[lane], vs = sc[kKeys + lane];
           const float safe = fmaxf(vs, kLeastScale);
-          float* const f = reinterpret_cast<float*>(factors);
-          f[4 * (lane >> 1) + (lane & 1)] = in ? ks + (vs - vs) : 0.f;  // NaN where vs is
-          f[4 * (lane >> 1) + 2 + (lane & 1)] = in ? lg2(safe) : kNoKey;
-          f[4 * kKeys / 2 + lane] = in ? rcp(safe) : 0.f;
+          factors[lane] = make_float4(in ? ks + (vs - vs) : 0.f,  // NaN where vs is
+                                      in ? lg2(safe) : kNoKey, in ? rcp(safe) : 0.f, 0.f);
           __syncwarp();
         }
-        // scores: four blocks of eight keys
-        float c[4][4];
+        // scores: two blocks of sixteen keys by the rows
+        float c[2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
+          for (int e = 0; e < NT; ++e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[b][e][k] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           uint32_t ww[4][4];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(st + (nt >> 1) * 16 * D +
-                                                             k_chunk<D>(8 * (nt & 1) + g, 4 * j + t4));
-            ww[nt][0] = w4.x, ww[nt][1] = w4.y, ww[nt][2] = w4.z, ww[nt][3] = w4.w;
+          for (int n = 0; n < 4; ++n) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(st + (n >> 1) * 16 * D +
+                                                             k_chunk<D>(8 * (n & 1) + g, 4 * j + t4));
+            ww[n][0] = w4.x, ww[n][1] = w4.y, ww[n][2] = w4.z, ww[n][3] = w4.w;
           }
-          // (the four blocks in turn: products of one block wait for each other)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-              uint32_t b0, b1;
-              codes4_f16<E4M3>(ww[nt][q], b0, b1);
-              mma16816(c[nt], qf[4 * j + q], b0, b1);
+            for (int b = 0; b < 2; ++b) {
+              uint32_t a0, a1, a2, a3;
+              codes4_f16<E4M3>(ww[2 * b][q], a0, a2);
+              codes4_f16<E4M3>(ww[2 * b + 1][q], a1, a3);
+#pragma unroll
+              for (int e = 0; e < NT; ++e)
+                mma16816(c[b][e], a0, a1, a2, a3, qf[e][4 * j + q][0], qf[e][4 * j + q][1]);
             }
         }
-        // this lane's keys: 2 t4, 2 t4 + 1 of the four blocks
-        float2 rvs[4];
+        // this lane's keys: g, g + 8, g + 16, g + 24
+        float rvs[4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const float4 f = factors[4 * nt + t4];
-          rvs[nt] = reinterpret_cast<const float2*>(factors + kKeys / 2)[4 * nt + t4];
+        for (int n = 0; n < 4; ++n) {
+          const float4 f = factors[8 * n + g];
+          rvs[n] = f.z;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 x = fma2(mul2(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), make_float2(rf[e], rf[e])),
-                                  make_float2(f.x, f.y), make_float2(f.z, f.w));
-            c[nt][2 * e] = x.x;
-            c[nt][2 * e + 1] = x.y;
+          for (int e = 0; e < NT; ++e) {
+            float* const y = &c[n >> 1][e][2 * (n & 1)];
+            const float2 x = fma2(mul2(make_float2(y[0], y[1]), rf[e]), make_float2(f.x, f.x),
+                                  make_float2(f.y, f.y));
+            y[0] = x.x, y[1] = x.y;
           }
         }
         if (!(key0 + kKeys <= hi_all && (key0 >= lo_all || key0 + kKeys <= a.sinks))) {
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = key0 + 8 * (n >> 1) + 2 * t4 + (n & 1);
-              bool see = j < hi[e];
-              if (mask[e] && j >= s.prefix)
-                see = see && j - s.prefix < a.mask_width && mask[e][j - s.prefix] != 0;
-              else
-                see = see && (j >= lo[e] || j < a.sinks);
-              if (!see) c[n >> 1][2 * e + (n & 1)] = -INFINITY;
+            for (int e = 0; e < NT; ++e)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int j = key0 + 8 * n + g;
+                bool see = j < hi[e][i];
+                if (mask[e][i] && j >= s.prefix)
+                  see = see && j - s.prefix < a.mask_width && mask[e][i][j - s.prefix] != 0;
+                else
+                  see = see && (j >= lo[e][i] || j < a.sinks);
+                if (!see) c[n >> 1][e][2 * (n & 1) + i] = -INFINITY;
+              }
+        }
+        // the running maximum, of a row over the eight lanes that have its keys
+        float top[NT][2];
+        bool grows = false;
+#pragma unroll
+        for (int e = 0; e < NT; ++e)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = fmaxf(max3(c[0][e][i], c[0][e][2 + i], c[1][e][i]), c[1][e][2 + i]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            if (x < 0.5f * kNoKey) x = -INFINITY;  // no key but such that are none
+            top[e][i] = x;
+            grows |= x > m[e][i] + kSlack;
+          }
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+          for (int e = 0; e < NT; ++e) {
+            float shrink[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float to = fmaxf(m[e][i], top[e][i]);
+              shrink[i] = to == -INFINITY ? 1.f : ex2(m[e][i] - to);
+              m[e][i] = to;
             }
-        }
-        // the running maximum, of a row over its four lanes
-        float top[2];
+            l[e].x *= shrink[0];
+            l[e].y *= shrink[1];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[e] = max3(max3(c[0][2 * e], c[0][2 * e + 1], c[1][2 * e]),
-                        max3(c[1][2 * e + 1], c[2][2 * e], c[2][2 * e + 1]),
-                        fmaxf(c[3][2 * e], c[3][2 * e + 1]));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-          top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-          if (top[e] < 0.5f * kNoKey) top[e] = -INFINITY;  // no key but such that are none
-        }
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float to = fmaxf(m[e], top[e]);
-            const float shrink = to == -INFINITY ? 1.f : ex2(m[e] - to);
-            m[e] = to;
-            l[e].x *= shrink;
-            l[e].y *= shrink;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              o[d][2 * e] *= shrink;
-              o[d][2 * e + 1] *= shrink;
+            for (int d = 0; d < D / 16; ++d) {
+              o[e][d][0] *= shrink[0];
+              o[e][d][1] *= shrink[1];
+              o[e][d][2] *= shrink[0];
+              o[e][d][3] *= shrink[1];
             }
           }
         }
-        uint32_t p[2][4];
+        uint32_t p[NT][4];  // of eight keys each: row g's pair of keys 2 t4
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float from = m[e] == -INFINITY ? 0.f : -m[e];
+        for (int e = 0; e < NT; ++e) {
+          const float2 from = make_float2(m[e][0] == -INFINITY ? 0.f : -m[e][0],
+                                          m[e][1] == -INFINITY ? 0.f : -m[e][1]);
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            float2 x = add2(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), make_float2(from, from));
+          for (int n = 0; n < 4; ++n) {
+            const float* const y = &c[n >> 1][e][2 * (n & 1)];
+            float2 x = add2(make_float2(y[0], y[1]), from);
             x.x = ex2(x.x);
             x.y = ex2(x.y);
-            l[e] = fma2(x, rvs[nt], l[e]);
+            l[e] = fma2(x, make_float2(rvs[n], rvs[n]), l[e]);
             const __half2 h = __floats2half2_rn(x.x, x.y);
-            p[nt >> 1][2 * (nt & 1) + e] = *reinterpret_cast<const uint32_t*>(&h);
+            p[e][n] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
           }
         }
-        // sums: columns D / 8 * g .. of four keys at a time
+        // sums: this lane's dimensions D / 8 * g .. of four keys at a time
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           const uint8_t* const vp = st + R::kCodes + kk * 16 * D;
@@ -408,13 +451,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
           for (int q = 0; q < D / 32; ++q)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
+              // dimensions 4 q + 2 hf and the next of the lane's: rows g and g + 8
               const uint32_t sel = hf ? 0x7362 : 0x5140;
-              uint32_t b[2][2];
+              uint32_t a0, a1, a2, a3;
+              codes4_f16<E4M3>(prmt(v[0][q], v[1][q], sel), a0, a1);
+              codes4_f16<E4M3>(prmt(v[2][q], v[3][q], sel), a2, a3);
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt)
-                codes4_f16<E4M3>(prmt(v[2 * nt][q], v[2 * nt + 1][q], sel), b[nt][0], b[nt][1]);
-              mma16816(o[4 * q + 2 * hf], p[kk], b[0][0], b[1][0]);
-              mma16816(o[4 * q + 2 * hf + 1], p[kk], b[0][1], b[1][1]);
+              for (int e = 0; e < NT; ++e)
+                mma16816(o[e][2 * q + hf], a0, a1, a2, a3, p[e][2 * kk], p[e][2 * kk + 1]);
             }
         }
       }
@@ -424,29 +468,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
 
     // the four warps' sums, relative to the largest maximum
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float sum = l[e].x + l[e].y;
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t4 == 0) {
-        part_m[warp][g + 8 * e] = m[e];
-        part_l[warp][g + 8 * e] = sum;
+    for (int e = 0; e < NT; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[e].x += __shfl_xor_sync(0xffffffffu, l[e].x, x);
+        l[e].y += __shfl_xor_sync(0xffffffffu, l[e].y, x);
+      }
+      if (g == 0) {
+        part_m[warp][8 * e + 2 * t4] = m[e][0];
+        part_m[warp][8 * e + 2 * t4 + 1] = m[e][1];
+        part_l[warp][8 * e + 2 * t4] = l[e].x;
+        part_l[warp][8 * e + 2 * t4 + 1] = l[e].y;
       }
     }
     __syncthreads();  // the rings are free
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = g + 8 * e;
-      if (row < nr) {
+    for (int e = 0; e < NT; ++e)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * e + 2 * t4 + i;
+        if (row < nr) {
 #pragma unroll
           for (int q = 0; q < D / 32; ++q)
-            sums[warp * kRows * (D / 4) + sum_chunk<D>(row, (D / 32) * (2 * t4 + n) + q)] =
-                make_float4(o[4 * q][2 * e + n], o[4 * q + 1][2 * e + n], o[4 * q + 2][2 * e + n],
-                            o[4 * q + 3][2 * e + n]);
+            sums[warp * kRows * (D / 4) + sum_chunk<D>(row, (D / 32) * g + q)] =
+                make_float4(o[e][2 * q][i], o[e][2 * q][2 + i], o[e][2 * q + 1][i], o[e][2 * q + 1][2 + i]);
+        }
       }
-    }
     __syncthreads();
     const int64_t u0 = w.unit_begin();
     const int c0 = piece_of(piece.total, piece.pieces, u0);
@@ -559,27 +606,36 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D)) attn_dec_kernel(Attn
   }
 }
 
-template <int D, bool E4M3>
-cudaError_t launch(const AttnArgs& a, int ctas, cudaStream_t s) {
-  constexpr size_t smem = smem_bytes<D>();
-  const cudaError_t e = cudaFuncSetAttribute(attn_dec_kernel<D, E4M3>,
+template <int D, bool E4M3, int NT>
+cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
+  constexpr size_t smem = smem_bytes<D, NT>();
+  const cudaError_t e = cudaFuncSetAttribute(attn_dec_kernel<D, E4M3, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_dec_kernel<D, E4M3><<<ctas, kThreads, smem, s>>>(a, 1);
+  attn_dec_kernel<D, E4M3, NT><<<ctas_per_sm(D, NT) * sms, kThreads, smem, s>>>(a, 1);
   return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_dim(const AttnArgs& a, int sms, cudaStream_t s) {
+  // eight rows a unit where a key head has no more on average
+  const bool eight = static_cast<int64_t>(a.b.rows) * a.heads <=
+                     8 * static_cast<int64_t>(a.b.sequences) * a.c.heads;
+  if (eight) return a.c.e4m3 ? launch<D, true, 1>(a, sms, s) : launch<D, false, 1>(a, sms, s);
+  return a.c.e4m3 ? launch<D, true, 2>(a, sms, s) : launch<D, false, 2>(a, sms, s);
 }
 
 }  // namespace
 
 size_t attn_dec_partials(int sms, int dim) {
-  return 2 * static_cast<size_t>(ctas_per_sm(dim) * sms) * (kRows * dim + 2 * kRows) * sizeof(float);
+  const auto bytes = [&](int nt) {
+    return 2 * static_cast<size_t>(ctas_per_sm(dim, nt) * sms) * (8 * nt * dim + 2 * 8 * nt) * sizeof(float);
+  };
+  return bytes(1) > bytes(2) ? bytes(1) : bytes(2);
 }
 
 cudaError_t launch_attn_dec(const AttnArgs& a, int sms, cudaStream_t s) {
-  const int ctas = ctas_per_sm(a.c.dim) * sms;
-  if (a.c.dim == 128) return a.c.e4m3 ? launch<128, true>(a, ctas, s) : launch<128, false>(a, ctas, s);
-  return a.c.e4m3 ? launch<64, true>(a, ctas, s) : launch<64, false>(a, ctas, s);
+  return a.c.dim == 128 ? launch_dim<128>(a, sms, s) : launch_dim<64>(a, sms, s);
 }
 
 }  // namespace w4
