@@ -613,7 +613,13 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  attn_dec_kernel<D, E4M3, NT><<<ctas_per_sm(D, NT) * sms, kThreads, smem, s>>>(a, 1);
+  // no more CTAs than there can be tiles
+  const int64_t units = static_cast<int64_t>(a.c.heads) *
+                        (static_cast<int64_t>(a.b.rows) * (a.heads / a.c.heads) / (8 * NT) + a.b.sequences);
+  const int64_t tiles = units * (((a.b.width << a.c.page_shift) + kTile - 1) / kTile + 1);
+  const int ctas = ctas_per_sm(D, NT) * sms;
+  attn_dec_kernel<D, E4M3, NT>
+      <<<tiles < ctas ? static_cast<int>(tiles) : ctas, kThreads, smem, s>>>(a, 1);
   return cudaGetLastError();
 }
 template <int D>
