@@ -1,8 +1,10 @@
 // w4_attn_dec.cu — attention over the paged key-value cache for few rows a key
 // head (decode steps): bound by the bytes of the visible codes and, short of that,
-// by the instructions that make operands of them (about 790 a warp for 32 keys of
-// 128 dimensions).  64 sequences of up to 8192 positions, 8 key heads of 128: 144 us,
-// 4.5 TB/s; two of 131072: 77 us, 4.7 TB/s; one of 1500: 10 us, latency.
+// by the instructions that make operands of them (642 a warp for 32 keys of 128
+// dimensions).  64 sequences of up to 8192 positions, 8 key heads of 128: 131 us,
+// 5.0 TB/s; two of 131072: 74 us, 4.9 TB/s; one of 1500: 10 us, latency.  With the
+// unit's rows as the MMA's 16 and the keys as its 8 (half of it empty with up to
+// eight rows): 144 and 77 us.
 //
 // A unit is 8 or 16 rows (query heads of a key head, of one token or a few) by the
 // key tiles they see; four warps of a CTA take 32 keys each of a 128-key tile.
@@ -42,7 +44,8 @@ constexpr int kKeys = 32;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
 
-// CTAs an SM: two for 16 rows of 128 dimensions (three spill registers), else three.
+// CTAs an SM: two for 16 rows of 128 dimensions (three spill registers), else three
+// (64 sequences 131 us, with two 139; 64 dimensions: 48 windows 50 us, with four 51).
 __host__ __device__ constexpr int ctas_per_sm(int dim, int nt) { return dim == 128 && nt == 2 ? 2 : 3; }
 
 template <int D, int NT>
