@@ -489,7 +489,9 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
  * statistics and sums are fp32, and each key's probability times its value's
  * scale is rounded to fp16 (relative to the row's largest) before the product
- * with the values' codes.  Errors as w4_cache_write, plus INVALID_ARGUMENT
+ * with the values' codes.  A key whose probability times value scale (0 counts as
+ * 2^-60 here) is below 2^-116 of the row's largest may count as none: value scales
+ * may lie some 2^90 apart.  Errors as w4_cache_write, plus INVALID_ARGUMENT
  * for heads not a multiple of the cache's, a scale that is not finite, negative
  * sinks, or out overlapping q or the cache; UNSUPPORTED for heads above 65535 or
  * rows * heads above 2^30; WORKSPACE. */

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
           const float* const sc = reinterpret_cast<const float*>(st + 2 * R::kCodes);
           const bool in = (lane < 16 ? page0 : page1) >= 0 && key0 + lane < s.len;
           const float ks = sc[lane], vs = sc[kKeys + lane];
-          const float safe = fmaxf(vs, kLeastScale);
+          const float safe = counted(vs);
           factors[lane] = make_float4(in ? ks + (vs - vs) : 0.f,  // NaN where vs is
                                       in ? lg2(safe) : kNoKey, in ? rcp(safe) : 0.f, 0.f);
           __syncwarp();

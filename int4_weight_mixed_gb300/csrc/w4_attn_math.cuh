@@ -15,9 +15,13 @@ namespace {
 constexpr float kSlack = 8.f;
 // log2 vs of a key that is none: far below any score, and still a number.
 constexpr float kNoKey = -0x1p120f;
-// Scales count as this at least where their logarithm is taken (a row of zeros
-// has scale 0; the cache's writer makes none smaller than this but that).
+// Where its logarithm is taken, a value's scale counts as this at least (the
+// cache's writer makes none smaller but 0) ...
 constexpr float kLeastScale = 0x1p-100f;
+// ... and that of a row of zeros, which weighs in a row's sum alone, as this.  A p
+// below 2^-126 is lost from the sum, so it must not lie too far below the other
+// values' scales; nor above them, or theirs would leave fp16.
+constexpr float kZeroScale = 0x1p-60f;
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -38,6 +42,10 @@ __device__ __forceinline__ float rcp(float x) {
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// A value's scale, as it counts in exponents.  (A NaN is dealt with elsewhere.)
+__device__ __forceinline__ float counted(float vs) {
+  return vs > 0.f ? fmaxf(vs, kLeastScale) : kZeroScale;
 }
 
 // Four codes as two pairs of fp16.  int8: 1024 + (code + 128) by its bits, less

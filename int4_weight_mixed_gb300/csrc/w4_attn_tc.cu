@@ -412,7 +412,7 @@ struct AttnTc {
   __device__ __forceinline__ void put_factors(uint32_t to, int key, bool none, float ks, float vs) const {
     const uint32_t f = to + 16 * (key >> 1) + 4 * (key & 1);
     const float x = none ? 0.f : (ks + (vs - vs)) * (a.scale * 1.44269504f);
-    const float y = none ? kNoKey : lg2(fmaxf(vs, kLeastScale));
+    const float y = none ? kNoKey : lg2(counted(vs));
     if constexpr (SOURCE == kUnpack) {
       *reinterpret_cast<float*>(record + f) = x;
       *reinterpret_cast<float*>(record + f + 8) = y;

@@ -129,8 +129,9 @@ def attention(q, cache, batch, window=0, sinks=0, mask=None, scale=None):
         added: 2^-25 max|q| sum|k| scale) and by |t| 2^-21 (its scaling, and the
         logarithm of the value's scale, in fp32);
       a probability is then off by twice the largest of these (numerator and
-        denominator), by 2^-17 (the logarithm of a value's scale, of magnitude up
-        to 2^5, by 2^-22 of itself; exponential, reciprocals, sums) and by half a
+        denominator), by 2^-17 (exponential, reciprocals, sums; the logarithm
+        of a value's scale by 2^-22 of itself, so 2^-22 of its magnitude where
+        that is above 2^5; a scale of 0 counts as 2^-60) and by half a
         step of fp16, 2^-11, or by 2^-25 of the row's largest probability times
         scale where fp16 has no more bits;
       the output is rounded by half a step of its type."""
@@ -166,10 +167,11 @@ def attention(q, cache, batch, window=0, sinks=0, mask=None, scale=None):
         o = torch.einsum("hgnk,hkd->hgnd", p, V)
         mag = torch.einsum("hgnk,hkd->hgnd", p, V.abs())
         worst = off.amax(-1, keepdim=True)
-        rel = 2 * worst + 2.0**-17 + 2.0**-11
         # p' below fp16's normal range: 2^-25 of the largest p' = p * scale
         pg, sl = batch.slots(b, 0, k)
         vs = cache.v_scales[pg, :, sl].double().movedim(1, 0)[:, None, None]  # [Hkv,1,1,k]
+        log = torch.where(vs > 0, vs, 2.0**-60).log2().abs().amax()
+        rel = 2 * worst + 2.0**-22 * log.clamp(min=32.0) + 2.0**-11
         big = torch.where(see, p * vs, 0.0).amax(-1, keepdim=True)
         codes = (V.abs() / torch.where(vs[:, 0, 0] > 0, vs[:, 0, 0], 1.0)[..., None])
         tiny = 2.0**-25 * big * torch.einsum("nk,hkd->hnd", see.double(), codes)[:, None]

@@ -200,6 +200,22 @@ def test_scales_far_apart(gpu_lib, D, rows, codes, wide):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,rows", [(128, 1), (64, 1), (128, 90), (64, 40), (96, 3)])
+@pytest.mark.parametrize("log", [-40, 0, 35])
+def test_values_of_zeros_weigh(gpu_lib, D, rows, log, wide):
+    """Three keys of four with values of zeros beside large, ordinary and small
+    values: they weigh in the sum whatever the others' scales are."""
+    batch = kv.Batch([rows], [500], 32, behind=2, wide=wide)
+    cache = kv.random_cache(batch, 1, D, S8)
+    cache.v_scales.mul_(2.0**log)
+    for i in range(3):
+        cache.v_scales[:, :, i::4] = 0.0
+        cache.v.view(torch.uint8)[:, :, i::4] = 0
+    _check(None, None, 4, 1, D, 32, S8, torch.bfloat16, cache=cache, batch=batch)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D,rows", [(128, 1), (128, 70), (64, 70), (32, 2)])
 def test_sizes_of_queries(gpu_lib, D, rows, wide):
     """Queries near the types' ends: large, small, zero rows, one channel far
