@@ -491,7 +491,8 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  * scale is rounded to fp16 (relative to the row's largest) before the product
  * with the values' codes.  A key whose probability times value scale (0 counts as
  * 2^-60 here) is below 2^-116 of the row's largest may count as none: value scales
- * may lie some 2^90 apart.  Errors as w4_cache_write, plus INVALID_ARGUMENT
+ * may lie some 2^90 apart.  Scores (times log2 e) lie within 2^119 of zero.
+ * Errors as w4_cache_write, plus INVALID_ARGUMENT
  * for heads not a multiple of the cache's, a scale that is not finite, negative
  * sinks, or out overlapping q or the cache; UNSUPPORTED for heads above 65535 or
  * rows * heads above 2^30; WORKSPACE. */
