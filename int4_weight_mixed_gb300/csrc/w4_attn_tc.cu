@@ -219,13 +219,15 @@ struct AttnTc {
     if ((threadIdx.x & 31) == 0) way().start(a, sh().piece);
     __syncwarp();
   }
-  // The unit after this one, in w_next; false if there is none.
+  // The unit after this one, in w_next; false if there is none.  (A shuffle orders no
+  // memory: the lanes meet before they read what lane 0 wrote, here and in next().)
   __device__ __forceinline__ bool look_ahead() const {
     int more = 0;
     if ((threadIdx.x & 31) == 0) {
       way_next() = way();
       more = way_next().next(a);
     }
+    __syncwarp();
     return __shfl_sync(0xffffffffu, more, 0) != 0;
   }
   // This warp's share of a unit's Q is in shared memory.
@@ -237,6 +239,7 @@ struct AttnTc {
     __syncwarp();
     int more = 0;
     if ((threadIdx.x & 31) == 0) more = way().next(a);
+    __syncwarp();
     return __shfl_sync(0xffffffffu, more, 0) != 0;
   }
 
