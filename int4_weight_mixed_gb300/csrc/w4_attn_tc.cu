@@ -78,7 +78,7 @@ struct Tc {
 };
 
 struct TcBarriers {
-  uint64_t q_full, join, k_full[4], k_empty[4], v_full[4], v_empty[4], f_full[6], s_full[2], p_half[2],
+  uint64_t q_full, join, fin, k_full[4], k_empty[4], v_full[4], v_empty[4], f_full[6], s_full[2], p_half[2],
       p_full[2], pv_half[2], pv_done[2];
 };
 
@@ -87,7 +87,7 @@ struct TcShared {
   TcBarriers bar;
   Piece piece;
   uint32_t tmem;
-  int abort;
+  int abort, never;  // (never: 0, for waits that go on after an abort)
   float join_m[kHalf], join_l[kHalf];
   // of each half's rows: they see keys below x; those from y on, and the sinks
   int2 sees[2][kTcRows];
@@ -255,6 +255,11 @@ struct AttnTc {
   __device__ __forceinline__ bool wait(uint64_t& b, uint32_t parity) const {
     return __all_sync(0xffffffffu, mbar_wait(&b, parity & 1, &sh().abort, a.status));
   }
+  // What is still in flight when a role ends (it gave up, then): its last phase of b,
+  // waited for whoever gave up, so that no copy or product outlives the CTA's memory.
+  __device__ __forceinline__ void settle(uint64_t& b, uint32_t parity) const {
+    mbar_wait(&b, parity & 1, &sh().never, a.status);
+  }
   // Both halves of the softmax meet (bounded, like every wait here).
   __device__ __forceinline__ bool meet(uint32_t& meets) const {
     __syncwarp();
@@ -309,6 +314,12 @@ struct AttnTc {
   }
 
   __device__ void issue() const {
+    issue_units();
+    commit(sh().bar.fin);  // of all products
+    settle(sh().bar.fin, 0);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void issue_units() const {
     Way& w = way();
     uint32_t units = 0, kc = 0, vc = 0, pc0 = 0, pc1 = 0;
     start();
@@ -608,6 +619,17 @@ struct AttnTc {
 
   // ---- kTiles: warp 8 copies the unpacked tiles instead
   __device__ void copy() const {
+    uint32_t k = 0, v = 0;  // copied tiles of K (and factors), of V
+    copy_tiles(k, v);
+    for (uint32_t j = k > T::kStages ? k - T::kStages : 0; j < k; ++j)
+      settle(sh().bar.k_full[j % T::kStages], j / T::kStages);
+    for (uint32_t j = k > T::kSlots ? k - T::kSlots : 0; j < k; ++j)
+      settle(sh().bar.f_full[j % T::kSlots], j / T::kSlots);
+    for (uint32_t j = v > T::kStages ? v - T::kStages : 0; j < v; ++j)
+      settle(sh().bar.v_full[j % T::kStages], j / T::kStages);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void copy_tiles(uint32_t& copied_k, uint32_t& copied_v) const {
     Way& w = way();
     start();
     const uint32_t tiles = static_cast<uint32_t>(sh().piece.end - sh().piece.begin);
@@ -631,6 +653,7 @@ struct AttnTc {
           bulk_g2s_a(factors(slot), now + 2 * T::kTileBytes, T::kFactors, smem_addr(&sh().bar.f_full[slot]));
         }
         __syncwarp();
+        copied_k = kc + 1;
       }
       if (kc > 0) {
         const uint32_t vc = kc - 1, st = vc % T::kStages;
@@ -640,6 +663,7 @@ struct AttnTc {
           bulk_g2s_a(v_at(st), before + T::kTileBytes, T::kTileBytes, smem_addr(&sh().bar.v_full[st]));
         }
         __syncwarp();
+        copied_v = vc + 1;
       }
     }
   }
@@ -839,6 +863,11 @@ struct AttnTc {
   }
 
   __device__ void softmax() const {
+    softmax_units();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    tmem_wait_st();
+  }
+  __device__ __forceinline__ void softmax_units() const {
     Way& w = way();
     const int half = threadIdx.x >> 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
@@ -1153,10 +1182,11 @@ __global__ void __launch_bounds__(tc_threads(SOURCE), 1)
   plan_piece<kTcRows, kTcKeys, tc_threads(SOURCE)>(a, least, &sh.piece);
   if (sh.piece.begin == sh.piece.end) return;
   if (tid == 0) {
-    sh.abort = 0;
+    sh.abort = sh.never = 0;
     TcBarriers& bar = sh.bar;
     mbar_init(&bar.q_full, kConvWarp);
     mbar_init(&bar.join, kConvWarp);
+    mbar_init(&bar.fin, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.k_full[i], SOURCE == kTiles ? 1 : kConvWarps);
       mbar_init(&bar.k_empty[i], 1);
