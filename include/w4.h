@@ -487,9 +487,12 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  *        16-byte aligned, zero-filled before its first use, not shared by calls
  *        that overlap on the GPU; it may be the one of the products.
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
- * statistics and sums are fp32, and each key's probability times its value's
- * scale is rounded to fp16 (relative to the row's largest) before the product
- * with the values' codes.  A key whose probability times value scale (0 counts as
+ * statistics and sums are fp32, and each key's weight (probability times value
+ * scale) is rounded to fp16 before the product with the values' codes: to 2^-11 of
+ * itself, or to 2^-31 of the row's largest weight where that is more.  fp32 sums of
+ * many keys, as the tensor cores add them, may drop up to 2^-24 of a sum from each
+ * key's part: a key far below the largest may be lost where that one's value is large.
+ * In the sum of the probabilities a key whose weight (a value scale of 0 counts as
  * 2^-60 here) is below 2^-116 of the row's largest may count as none: value scales
  * may lie some 2^90 apart.  Scores (times log2 e) lie within 2^119 of zero.
  * Errors as w4_cache_write, plus INVALID_ARGUMENT

@@ -13,8 +13,8 @@
 // step's few rows leave none of it empty.
 //
 //   t_j = (q . code_j) * (scale * log2 e * ks_j) + log2 vs_j
-//   p_j = 2^(t_j - m) <= 2^8,  m a running maximum of t
-//   O  += p_j * code_j (fp16 p, fp32 sums),  l += p_j / vs_j,  out = O / l
+//   p_j = 2^(t_j - m + 7) <= 2^15,  m a running maximum of t
+//   O  += p_j * code_j (fp16 p, fp32 sums),  l += p_j 2^-7 / vs_j,  out = 2^-7 O / l
 //
 // with ks, vs the key's and value's scales: both enter the exponent, so the
 // codes go to the tensor cores as they are, and p is rounded to fp16 relative to
@@ -43,6 +43,7 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 32;          // keys of a warp's stage
 constexpr int kTile = kKeys * kWarps;
 constexpr int kThreads = 32 * kWarps;
+constexpr float kUnlift = 1.f / (1 << kDecLift);
 
 // CTAs an SM: two for 16 rows of 128 dimensions (three spill registers), else three
 // (64 sequences 131 us, with two 139; 64 dimensions: 48 windows 50 us, with four 51).
@@ -53,7 +54,7 @@ struct Ring {
   static constexpr int kCodes = kKeys * D;                // bytes of one array
   static constexpr int kStage = 2 * kCodes + 2 * kKeys * 4;
   static constexpr int kStages = D == 64 ? 4 : NT == 2 ? 3 : 2;
-  // then the factors of the stage in use: of a key ks, log2 vs, 1 / vs
+  // then the factors of the stage in use: of a key ks, log2 vs, 2^-7 / vs
   static constexpr int kFactors = kStage * kStages;
   static constexpr int kWarp = kFactors + kKeys * 16;
 };
@@ -320,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
           const float ks = sc[lane], vs = sc[kKeys + lane];
           const float safe = counted(vs);
           factors[lane] = make_float4(in ? ks + (vs - vs) : 0.f,  // NaN where vs is
-                                      in ? lg2(safe) : kNoKey, in ? rcp(safe) : 0.f, 0.f);
+                                      in ? lg2(safe) : kNoKey,
+                                      in ? rcp(safe) * kUnlift : 0.f, 0.f);
           __syncwarp();
         }
         // scores: two blocks of sixteen keys by the rows
@@ -421,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
         uint32_t p[NT][4];  // of eight keys each: row g's pair of keys 2 t4
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
-          const float2 from = make_float2(m[e][0] == -INFINITY ? 0.f : -m[e][0],
-                                          m[e][1] == -INFINITY ? 0.f : -m[e][1]);
+          const float2 from = make_float2(m[e][0] == -INFINITY ? 0.f : kDecLift - m[e][0],
+                                          m[e][1] == -INFINITY ? 0.f : kDecLift - m[e][1]);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const float* const y = &c[n >> 1][e][2 * (n & 1)];
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
         y.w = fmaf(f, x.w, y.w);
       }
       if (whole) {
-        const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+        const float inv = sum_l == 0.f ? 0.f : kUnlift / sum_l;
         store(r, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
       } else {
         float* const to = slot_of(blockIdx.x);
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
               y.w = y.w * f + fk * x[k].w;
             }
           }
-          const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+          const float inv = sum_l == 0.f ? 0.f : kUnlift / sum_l;
           store(r, c, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
         }
       }

@@ -10,9 +10,13 @@ namespace w4 {
 namespace {
 
 // A row's running maximum moves only when the maximum grows by more than this
-// (log2): probabilities reach 2^8, well within fp16, and sums are seldom
-// rescaled.
+// (log2), so that sums are seldom rescaled (a published method): probabilities
+// relative to it reach 2^8 (2^9 in the kernel that rounds it to a whole number).
+// They enter the product with the values 2^7 (2^6) times as large, up to 2^15: fp16
+// then holds half a step of 2^-11 of a probability down to 2^-20 of the row's largest
+// one, and 2^-31 of that one below.
 constexpr float kSlack = 8.f;
+constexpr int kDecLift = 7, kTcLift = 6;
 // log2 vs of a key that is none: far below any score, and still a number.
 constexpr float kNoKey = -0x1p120f;
 // Where its logarithm is taken, a value's scale counts as this at least (the

@@ -8,8 +8,8 @@
 //
 //   S_X = Q_X K^T         K: codes as 16-bit values, exact; S in tensor memory
 //   t_j = S_j * (scale * log2 e * ks_j) + log2 vs_j       (ks, vs: the scales)
-//   P_j = 2^(t_j - m) <= 2^9, fp16, written over S in tensor memory
-//   O_X += P V            V: codes as fp16, exact;  l += P_j / vs_j;  out = O / l
+//   P_j = 2^(t_j - m + 6) <= 2^15, fp16, written over S in tensor memory
+//   O_X += P V            V: codes as fp16, exact;  l += P_j 2^-4 / vs_j;  out = 2^-4 O / l
 //                         (64 keys at a time: the first half's product runs while
 //                         the second half's P is made)
 //
@@ -48,6 +48,10 @@ static_assert(2 * kSoftRegs + 2 * kConvRegs + kIssueRegs <= 5 * kTcRegs, "regist
 // a warp's 32 rows by 32 columns of the result on their way out: 64 bytes a row,
 // rows 80 bytes apart (16-byte accesses of eight rows hit different banks)
 constexpr int kOutRow = 80, kOutBytes = 32 * kOutRow;
+// log2 vs is kept with this added (t and m, too): its negative is the exponent of what
+// l adds, which stays in range for all vs, from 2^-100 (l) to 2^121 (normal numbers).
+constexpr int kLogLift = 4;
+constexpr float kUnlift = 1.f / (1 << kLogLift);
 
 // Where codes become 16-bit values: by the CTA's own converter warps, tile by tile
 // (kOwn), or once for all units by attn_unpack_kernel, whose tiles a warp copies
@@ -63,7 +67,7 @@ struct Tc {
   static constexpr int kSlots = kStages + 2;
   static constexpr int kQ = kHalf * D * 2;            // bytes of a half's queries
   static constexpr int kTileBytes = kTcKeys * D * 2;  // of a stage of K or V
-  // for a pair of keys ks', ks', log2 vs, log2 vs
+  // for a pair of keys ks', ks', log2 vs + 4, log2 vs + 4
   static constexpr int kFactors = 2 * kTcKeys * 4;
   static constexpr int kFactorsAt = 2 * kQ + 2 * kStages * kTileBytes;
   static constexpr int kOutAt = kFactorsAt + kSlots * kFactors;
@@ -426,7 +430,7 @@ struct AttnTc {
   __device__ __forceinline__ void put_factors(uint32_t to, int key, bool none, float ks, float vs) const {
     const uint32_t f = to + 16 * (key >> 1) + 4 * (key & 1);
     const float x = none ? 0.f : (ks + (vs - vs)) * (a.scale * 1.44269504f);
-    const float y = none ? kNoKey : lg2(counted(vs));
+    const float y = none ? kNoKey : lg2(counted(vs)) + kLogLift;
     if constexpr (SOURCE == kUnpack) {
       *reinterpret_cast<float*>(record + f) = x;
       *reinterpret_cast<float*>(record + f + 8) = y;
@@ -1004,7 +1008,7 @@ struct AttnTc {
           float2 neg[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float y = m[k] == -INFINITY ? 0.f : -m[k];
+            const float y = m[k] == -INFINITY ? 0.f : kTcLift - m[k];
             neg[k] = make_float2(y, y);
           }
           uint32_t p[2][8];
@@ -1118,7 +1122,7 @@ struct AttnTc {
     mine_f = ex2(m - from);
     other_f = ex2(om - from);
     const float sum_l = full ? l : l * mine_f + ol * other_f;
-    const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+    const float inv = sum_l == 0.f ? 0.f : kUnlift / sum_l;
     uint16_t* const to = static_cast<uint16_t*>(a.out) +
                          ((static_cast<int64_t>(w.s.row0) + token) * a.heads + w.h * group +
                           flat - token * group) * D;
@@ -1306,7 +1310,7 @@ __global__ void __launch_bounds__(kReduceThreads) attn_tc_reduce_kernel(AttnArgs
         y.w = y.w * f + fk * x[k].w;
       }
     }
-    const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+    const float inv = sum_l == 0.f ? 0.f : kUnlift / sum_l;
     uint2 u;
     if (a.bf16) {
       const __nv_bfloat162 p = __floats2bfloat162_rn(y.x * inv, y.y * inv);

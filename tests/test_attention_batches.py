@@ -3,6 +3,7 @@ has threads (the plan then takes them in blocks), with runs of sequences that
 have no rows, and batches that mix single tokens with chunks: each kernel,
 against the definition in 64 bits."""
 import ctypes
+import math
 import random
 
 import pytest
@@ -11,7 +12,7 @@ import torch
 import int4_weight_mixed_gb300 as w4
 import kv
 from fake_cuda import build
-from test_attention import _attend, _check, _tree
+from test_attention import DEV, _check, _tree
 from test_kv_cache import _cache, _of
 
 S8, F8 = torch.int8, torch.float8_e4m3fn
@@ -117,3 +118,77 @@ def test_tokens_beside_chunks(gpu_lib, D, codes, dt, wide):
     lens = [max(n, r.randint(1, 900)) for n in rows]
     _check(rows, lens, 8, 2, D, 64, codes, dt, wide=wide)
     _check(rows, lens, 8, 2, D, 64, codes, dt, 100, 4, wide=wide)
+
+
+# dimension, sequences, rows of each, keys above the others (one for every running
+# maximum of the kernel: a warp's of the decode kernel, a half's of units of up to
+# 128 rows), kernel
+PEAKS = [(128, 456, 1, [70, 100, 10, 50], DEC), (64, 456, 1, [70, 100, 10, 50], DEC),
+         (128, 152, 20, [70, 200], OWN), (64, 152, 20, [70, 200], OWN),
+         (128, 152, 40, [70], OWN), (64, 152, 40, [70], OWN),
+         (128, 3, 3201, [70], UNPACKED), (64, 3, 3201, [70], UNPACKED)]
+
+
+@pytest.mark.parametrize("case", PEAKS)
+def test_kernel_of_the_peaks(rec, case):
+    D, B, n, peaks, kernel = case
+    got = _kernels(rec, 4, 1, D, B * n, B, 2048 * len(peaks), 64)
+    assert kernel in got
+    assert (UNPACKED in got) == (kernel == UNPACKED) and (DEC in got) == (kernel == DEC)
+
+
+def _far_apart(D, B, n, peaks, below, codes, dt):
+    """131072 alike keys for each of a few (at the positions `peaks`) that weigh
+    2^below of one; values of 1, or of -1, that the few share in their second half of
+    the dimensions alone, with zeros in the first.  Sequences share their pages: there
+    are enough of them that one CTA takes all keys of its rows.
+
+    The results and 64 bits' of either half, for both signs: [rows, heads, D / 2], [rows]."""
+    L = 131072 * len(peaks)
+    one = kv.Batch([n], [L], 64, seed=3, spare=0, behind=0)
+    cache = w4.kv_cache(one.pages, 1, 64, D, codes, DEV)
+    high, low = (torch.tensor(s * kv.TOP[codes]).to(codes).view(torch.uint8).item() for s in (1, -1))
+    pg, sl = one.table[0, torch.tensor(peaks) // 64].long().to(DEV), torch.tensor(peaks, device=DEV) % 64
+    # q of ones: such a key's score is below * log 2, the others' (keys of zeros) 0
+    ks = torch.tensor(below * math.log(2.0) / (kv.TOP[codes] * D**0.5))
+    cache.k.view(torch.uint8)[pg, :, sl] = high
+    cache.k_scales[pg, :, sl] = ks.to(DEV)
+    cache.v_scales.fill_(1 / kv.TOP[codes])
+    table = one.table.expand(B, one.width).contiguous().to(DEV)
+    starts = torch.arange(B + 1, dtype=torch.int32, device=DEV) * n
+    lens = torch.full((B,), L, dtype=torch.int32, device=DEV)
+    q = torch.ones(B * n, 4, D, dtype=dt, device=DEV)
+    w = len(peaks) * math.exp(float(ks.double()) * kv.TOP[codes] * D**0.5)
+    keys = L - n + 1 + torch.arange(n).double().repeat(B) - len(peaks)  # alike ones that a row sees
+    v = float(cache.v_scales[0, 0, 0].double()) * kv.TOP[codes]
+    for sign in (1, -1):
+        cache.v.view(torch.uint8).fill_(high if sign > 0 else low)
+        cache.v.view(torch.uint8)[pg, :, sl, :D // 2] = 0
+        cache.v.view(torch.uint8)[pg, :, sl, D // 2:] = high
+        out = w4.cache_attention(cache, q, table, starts, lens).cpu().double()
+        yield out[..., :D // 2], v * sign * keys / (w + keys)
+        yield out[..., D // 2:], v * (w + sign * keys) / (w + keys)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes,dt", [(S8, torch.float16), (F8, torch.float16), (S8, torch.bfloat16)])
+@pytest.mark.parametrize("below", [18, 25.01, 26, 28])
+@pytest.mark.parametrize("case", PEAKS)
+def test_many_small_weights(gpu_lib, case, below, codes, dt):
+    """Weights of 2^-below of the largest are not lost on their way into 16 bits.
+
+    The bound, relative to the largest weight, in the half of the dimensions where it
+    has no value.  With it at 2^6 at least, a weight in fp16 is off by 2^-11 of itself
+    or by 2^-25, 2^-31 of the largest, 131072 by 2^-14.  The tensor cores drop up to
+    2^-24 of a sum from each product that they add to it: 2^-7 of the result.  The sum
+    of the weights is off by 2^-9 (2^14 additions a lane, half a unit in the last
+    place each; small ones lost beside a large one, 2^-9 of it all together), the
+    scores and their exponentials by 2^-17, the result by half a step.  In the other
+    half the dropped parts are of the largest weight's value: 2^-7 of it."""
+    for i, (out, ref) in enumerate(_far_apart(*case[:4], below, codes, dt)):
+        ref = ref[:, None, None]
+        half = torch.finfo(dt).eps / 2
+        rel = 2.0**-11 + 2.0**-7 + 2.0**-9 + 2.0**-17
+        bound = (rel * (ref.abs() if i % 2 == 0 else 1.0) + 2.0**-14) * (1 + half) + half * ref.abs()
+        off = (out - ref).abs()
+        assert bool((off <= bound).all()), (i, float((off / bound).max()), float(off.max()), float(ref[0]))
