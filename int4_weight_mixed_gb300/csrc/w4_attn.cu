@@ -82,8 +82,11 @@ __global__ void __launch_bounds__(32 * kSimtWarps) attn_simt_kernel(AttnArgs a) 
       const float p = at >= 0 ? exp2f(t - from) : 0.f;
       l = l * shrink + p;
       const float pv = at >= 0 ? p * __ldg(a.c.v_scales + at) : 0.f;
+      // 32 keys' part by itself: added one by one, many small ones would vanish beside a
+      // large one (131072 at 2^-25 of it)
+      float sum[kMaxDim / 32];
 #pragma unroll
-      for (int e = 0; e < kMaxDim / 32; ++e) acc[e] *= shrink;
+      for (int e = 0; e < kMaxDim / 32; ++e) sum[e] = 0.f;
       for (int n = 0; n < 32; ++n) {
         const int64_t from_n = __shfl_sync(0xffffffffu, at, n);
         const float w = __shfl_sync(0xffffffffu, pv, n);
@@ -91,8 +94,10 @@ __global__ void __launch_bounds__(32 * kSimtWarps) attn_simt_kernel(AttnArgs a) 
         const uint8_t* v = a.c.v + from_n * D;
 #pragma unroll
         for (int e = 0; e < kMaxDim / 32; ++e)
-          if (lane + 32 * e < D) acc[e] = fmaf(w, codes2_f32<E4M3>(v[lane + 32 * e]).x, acc[e]);
+          if (lane + 32 * e < D) sum[e] = fmaf(w, codes2_f32<E4M3>(v[lane + 32 * e]).x, sum[e]);
       }
+#pragma unroll
+      for (int e = 0; e < kMaxDim / 32; ++e) acc[e] = fmaf(acc[e], shrink, sum[e]);
     }
   }
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

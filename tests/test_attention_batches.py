@@ -192,3 +192,19 @@ def test_many_small_weights(gpu_lib, case, below, codes, dt):
         bound = (rel * (ref.abs() if i % 2 == 0 else 1.0) + 2.0**-14) * (1 + half) + half * ref.abs()
         off = (out - ref).abs()
         assert bool((off <= bound).all()), (i, float((off / bound).max()), float(off.max()), float(ref[0]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes,dt", [(S8, torch.float16), (F8, torch.float16), (S8, torch.bfloat16)])
+@pytest.mark.parametrize("below", [18, 25.01, 26, 28])
+def test_many_small_weights_on_the_cuda_cores(gpu_lib, below, codes, dt):
+    """The same of the kernel for other head dimensions, all in fp32: keys are added 32
+    at a time, so 2^12 additions in a row to each sum, each off by half a unit in the
+    last place; scores and exponentials by 2^-17, the result by half a step."""
+    for i, (out, ref) in enumerate(_far_apart(96, 1, 1, [70], below, codes, dt)):
+        ref = ref[:, None, None]
+        half = torch.finfo(dt).eps / 2
+        rel = 2 * 2.0**-12 + 2.0**-17
+        bound = rel * (ref.abs() if i % 2 == 0 else 1.0) * (1 + half) + half * ref.abs()
+        off = (out - ref).abs()
+        assert bool((off <= bound).all()), (i, float((off / bound).max()), float(off.max()), float(ref[0]))
