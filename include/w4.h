@@ -481,11 +481,15 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  *   q    [rows, heads, head_dim] of `type` (W4_F16 / W4_BF16), q_stride
  *        elements from row to row; out the same shape and type, contiguous.
  *   scale  finite; usually 1 / sqrt(head_dim).
- *   workspace  as w4_gemm's: w4_attention_workspace_size bytes at least (it goes
- *        by the sizes in cache and batch and reads no array; with many rows it
- *        includes up to 256 MB for 16-bit copies of the keys and values),
- *        16-byte aligned, zero-filled before its first use, not shared by calls
- *        that overlap on the GPU; it may be the one of the products.
+ *   workspace  as w4_gemm's: w4_attention_workspace_size bytes (it goes by the
+ *        sizes in cache and batch and reads no array), 16-byte aligned,
+ *        zero-filled before its first use, not shared by calls that overlap on
+ *        the GPU; it may be the one of the products.  With many rows this includes
+ *        up to 256 MB for 16-bit copies of the keys and values, where those of all
+ *        sequences fit: a smaller batch may come to more.  One of the size for a
+ *        single row does for any batch on the cache: where the copies do not fit in
+ *        what there is, keys and values are converted wherever they are read (a
+ *        prompt of 8192 takes a tenth longer).
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
  * statistics and sums are fp32, and each key's weight (probability times value
  * scale) is rounded to fp16 before the product with the values' codes: to 2^-11 of

@@ -619,8 +619,9 @@ class _Batch(ctypes.Structure):  # w4_kv_batch
 
 def attention_workspace_size(cache: KVCache, rows: int, heads: int, table: torch.Tensor) -> int:
     """Bytes of ws that cache_attention and tree_attention of q [rows, heads,
-    head_dim] with this table need (for calls captured in a CUDA graph, which
-    pass one)."""
+    head_dim] with this table take (for calls captured in a CUDA graph, which
+    pass one).  Fewer sequences may take more; one of the size for one row does
+    for any call on the cache, many rows are slower with it."""
     c = _Cache(None, None, None, None, *cache.k.shape, _DTYPE_CODE[cache.k.dtype])
     b = _Batch(None, table.shape[1], None, None, table.shape[0])
     return int(load().w4_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), rows, heads))

@@ -1431,14 +1431,15 @@ w4_status attention(const w4_kv_cache* cache, const w4_kv_batch* batch, const vo
   a.mask = mask;
   a.mask_width = mask_width;
   const AttnPlan plan = attn_plan(cache, batch, rows, heads, a.window, a.sinks);
-  const size_t need = kWsHeader + kCounterBytes + align256(plan.partials) + plan.tiles;
+  // (without room for unpacked tiles every unit converts those that it visits)
+  const size_t need = kWsHeader + kCounterBytes + align256(plan.partials);
   if (!workspace || workspace_bytes < need || !aligned16(workspace))
     return fail(W4_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, is required", need);
   char* const ws = static_cast<char*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<int*>(ws + kWsHeader);
   a.partials = reinterpret_cast<float*>(ws + kWsHeader + kCounterBytes);
-  if (plan.tiles_each > 0) {
+  if (plan.tiles_each > 0 && workspace_bytes - need >= plan.tiles) {
     a.tiles = reinterpret_cast<uint8_t*>(ws + kWsHeader + kCounterBytes + align256(plan.partials));
     a.tiles_each = plan.tiles_each;
   }

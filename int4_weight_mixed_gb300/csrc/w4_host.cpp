@@ -573,22 +573,25 @@ PyObject* attention(PyObject*, PyObject* const* o, Py_ssize_t nargs) {
     const int code = code_of(q->scalar_type());
     // (a mask of no drafts has no address: any will do, none is read)
     const uint8_t none = 0;
-    int st;
-    for (int64_t bytes = 0;; bytes = static_cast<int64_t>(w4_attention_workspace_size(
-                                 &c.cache, &c.batch, T, static_cast<int>(heads)))) {
-      if (!ws) w_new = workspace(o[0], dev, stream, bytes);
-      const at::Tensor& w8 = ws ? *ws : w_new;
-      void* const pw = out_ptr(&w8);
-      const size_t nw = static_cast<size_t>(w8.nbytes());
-      Py_BEGIN_ALLOW_THREADS
-      st = mask ? w4_tree_attention(&c.cache, &c.batch, pq, pm ? pm : &none, mw, code, T,
-                                    static_cast<int>(heads), qs, static_cast<float>(scale), w,
-                                    n_sinks, po, pw, nw, stream)
-                : w4_cache_attention(&c.cache, &c.batch, pq, code, T, static_cast<int>(heads), qs,
-                                     static_cast<float>(scale), w, n_sinks, po, pw, nw, stream);
-      Py_END_ALLOW_THREADS
-      if (st != W4_ERR_WORKSPACE || ws || bytes) break;
+    if (!ws) {
+      // (the call makes do with less, but is slower then)
+      const size_t bytes =
+          w4_attention_workspace_size(&c.cache, &c.batch, T, static_cast<int>(heads));
+      w_new = workspace(o[0], dev, stream, 0);
+      if (static_cast<size_t>(w_new.nbytes()) < bytes)
+        w_new = workspace(o[0], dev, stream, static_cast<int64_t>(bytes));
+      ws = &w_new;
     }
+    void* const pw = out_ptr(ws);
+    const size_t nw = static_cast<size_t>(ws->nbytes());
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = mask ? w4_tree_attention(&c.cache, &c.batch, pq, pm ? pm : &none, mw, code, T,
+                                  static_cast<int>(heads), qs, static_cast<float>(scale), w,
+                                  n_sinks, po, pw, nw, stream)
+              : w4_cache_attention(&c.cache, &c.batch, pq, code, T, static_cast<int>(heads), qs,
+                                   static_cast<float>(scale), w, n_sinks, po, pw, nw, stream);
+    Py_END_ALLOW_THREADS
     check(st, mask ? "w4_tree_attention" : "w4_cache_attention");
     return result(o[12], *out);
   } catch (const Bad&) {

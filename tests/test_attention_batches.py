@@ -208,3 +208,67 @@ def test_many_small_weights_on_the_cuda_cores(gpu_lib, below, codes, dt):
         bound = rel * (ref.abs() if i % 2 == 0 else 1.0) * (1 + half) + half * ref.abs()
         off = (out - ref).abs()
         assert bool((off <= bound).all()), (i, float((off / bound).max()), float(off.max()), float(ref[0]))
+
+
+# ------------------------------------------------------------------ workspaces
+def _size(rec, heads, kv_heads, dim, rows, sequences, width, page=32):
+    return rec.lib.w4_attention_workspace_size(
+        ctypes.byref(_cache(heads=kv_heads, head_dim=dim, page_size=page)),
+        ctypes.byref(_of(table_width=width, sequences=sequences)), rows, heads)
+
+
+def test_workspace_of_a_larger_batch(rec):
+    """A workspace sized for 64 sequences, whose copies of keys and values are over the
+    limit, does for one, whose are not: without them."""
+    shape = dict(heads=32, kv_heads=8, dim=128, rows=16384, width=256)
+    large, small = (_size(rec, sequences=n, **shape) for n in (64, 1))
+    assert large < small
+    assert UNPACKED in _kernels(rec, sequences=1, nws=small, **shape)
+    for nws in (large, small - 1):
+        got = _kernels(rec, sequences=1, nws=nws, **shape)
+        assert OWN in got and UNPACKED not in got
+
+
+@pytest.mark.parametrize("dim", [64, 128, 96])
+def test_workspace_for_one_row_does(rec, dim):
+    least = _size(rec, 32, 8, dim, 1, 1, 1)
+    for rows, sequences, width in ((1, 1, 1), (300, 300, 4), (1000, 7, 64), (8192, 1, 256),
+                                   (8192, 1, 1 << 20), (100000, 40, 512)):
+        assert _size(rec, 32, 8, dim, rows, sequences, width) >= least
+        _kernels(rec, 32, 8, dim, rows, sequences, width, nws=least)
+        cache, of = _cache(heads=8, head_dim=dim, page_size=32), _of(table_width=width,
+                                                                     sequences=sequences)
+        st = rec.lib.w4_cache_attention(ctypes.byref(cache), ctypes.byref(of), 0x80000000, w4.F16,
+                                        rows, 32, 32 * dim, 0.1, 0, 0, 1 << 40, 1 << 41, least - 1,
+                                        None)
+        assert st == w4.ERR_WORKSPACE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,codes,dt", [(128, S8, torch.bfloat16), (64, F8, torch.float16)])
+def test_with_and_without_copies(gpu_lib, D, codes, dt):
+    """Rows enough for copies of keys and values, in a workspace with room for them
+    and in one without; and the binding's own, which has room."""
+    batch = kv.Batch([300, 1, 250], [700, 90, 250], 32, seed=1, behind=0)
+    cache = kv.random_cache(batch, 2, D, codes)
+    held, plan = kv.on(cache, DEV), batch.plan(DEV)
+    q = torch.randn(batch.T, 16, D, generator=torch.Generator().manual_seed(2)).to(dt)
+    ref, bound = kv.attention(q, cache, batch, 130, 5)
+    full = w4.attention_workspace_size(held, batch.T, 16, plan[0])
+    least = w4.attention_workspace_size(held, 1, 16, plan[0])
+    assert least < full
+    out = {}
+    side = torch.cuda.Stream()  # (with no workspace yet)
+    with torch.cuda.stream(side):
+        out[0] = w4.cache_attention(held, q.to(DEV), *plan, window=130, sinks=5)
+        assert w4.workspace(held.k.device, 0).numel() >= full
+    side.synchronize()
+    for n in (full, least):
+        ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+        out[n] = w4.cache_attention(held, q.to(DEV), *plan, window=130, sinks=5, ws=ws)
+        assert w4.check_status(ws) == w4.OK
+    for x in out.values():
+        assert bool(((x.cpu().double() - ref).abs() <= bound).all())
+    with pytest.raises(w4.W4Error):
+        w4.cache_attention(held, q.to(DEV), *plan,
+                           ws=torch.zeros(least - 1, dtype=torch.uint8, device=DEV))
