@@ -31,16 +31,25 @@ __global__ void __launch_bounds__(32 * kSimtWarps) attn_simt_kernel(AttnArgs a) 
   if (row < s.row0 || row >= s.row0 + s.n) return;
   const int D = a.c.dim, i = row - s.row0;
   const uint16_t* q = static_cast<const uint16_t*>(a.q) + row * a.q_stride + static_cast<int64_t>(head) * D;
+  // queries times a power of two (the scores' scale takes it back): their largest is in
+  // [1, 2), so that no product with the codes leaves fp32
+  float top_q = 0.f;
   for (int d = lane; d < D; d += 32) {
     const uint16_t w = q[d];
-    qs[warp][d] = a.bf16 ? __bfloat162float(__ushort_as_bfloat16(w)) : __half2float(__ushort_as_half(w));
+    const float x = a.bf16 ? __bfloat162float(__ushort_as_bfloat16(w)) : __half2float(__ushort_as_half(w));
+    qs[warp][d] = x;
+    top_q = fmaxf(top_q, fabsf(x));
   }
+  for (int o = 16; o > 0; o >>= 1) top_q = fmaxf(top_q, __shfl_xor_sync(0xffffffffu, top_q, o));
+  const int E = __float_as_int(top_q) >> 23;
+  const int up = E == 255 ? 127 : min(max(254 - E, 1), 253);
+  for (int d = lane; d < D; d += 32) qs[warp][d] *= __int_as_float(up << 23);
   __syncwarp();
   const int hk = head / (a.heads / a.c.heads);
   const int pos = a.mask ? draft_position(a, s, i) : s.prefix + i;
   const Visible vis = visible(pos, a.mask ? s.len : min(s.len, pos + 1), a.window, a.sinks);
   const uint8_t* mask = a.mask ? a.mask + static_cast<int64_t>(row) * a.mask_width : nullptr;
-  const float scale = a.scale * 1.44269504f;
+  const float scale = a.scale * 1.44269504f * __int_as_float((254 - up) << 23);
   float m = -INFINITY, l = 0.f, acc[kMaxDim / 32];
 #pragma unroll
   for (int e = 0; e < kMaxDim / 32; ++e) acc[e] = 0.f;
@@ -71,7 +80,7 @@ __global__ void __launch_bounds__(32 * kSimtWarps) attn_simt_kernel(AttnArgs a) 
             dot = fmaf(v.y, qs[warp][d + 2 * e + 1], dot);
           }
         }
-        t = dot * __ldg(a.c.k_scales + at) * scale;
+        t = dot * (scale * __ldg(a.c.k_scales + at));
       }
       float top = t;
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));

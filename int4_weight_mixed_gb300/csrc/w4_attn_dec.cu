@@ -363,7 +363,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_dec_kernel(
 #pragma unroll
           for (int e = 0; e < NT; ++e) {
             float* const y = &c[n >> 1][e][2 * (n & 1)];
-            const float2 x = fma2(mul2(make_float2(y[0], y[1]), rf[e]), make_float2(f.x, f.x),
+            // (the factors first: products of large queries would leave fp32 before a small
+            // key's scale brings them back)
+            const float2 x = fma2(make_float2(y[0], y[1]), mul2(rf[e], make_float2(f.x, f.x)),
                                   make_float2(f.y, f.y));
             y[0] = x.x, y[1] = x.y;
           }

@@ -72,14 +72,17 @@ __device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& h
   }
 }
 
-// The same as bf16.  int8: with the code's low seven bits u and sign bit s, code =
-// (128 + u) - (128 + 128 s), and bf16 holds 128 + u as 0x4300 | u, 128 + 128 s
-// as 0x4300 | s << 7.  E4M3: the code's exponent and mantissa at bf16's place are
-// the value times 2^-120, subnormals too.
+// The same as bf16, times 2^-8, exactly: so products with queries, which bf16 lets be
+// as large as fp32's largest number, leave fp32 2^8 later.  int8: with the code's low
+// seven bits u and sign bit s, code = (128 + u) - (128 + 128 s), and bf16 holds
+// (128 + u) 2^-8 as 0x3F00 | u, (128 + 128 s) 2^-8 as 0x3F00 | s << 7.  E4M3: the
+// code's exponent and mantissa at bf16's place are the value times 2^-120, subnormals
+// too.
+constexpr float kBf16Code = 0x1p-8f;
 template <bool E4M3>
 __device__ __forceinline__ void codes4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (E4M3) {
-    const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7B80));  // 2^120
+    const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7780));  // 2^112
     const uint32_t a = prmt(w, 0u, 0x1404), b = prmt(w, 0u, 0x3424);
     const uint32_t x = (a & 0x80008000u) | (a >> 4 & 0x07F007F0u);
     const uint32_t y = (b & 0x80008000u) | (b >> 4 & 0x07F007F0u);
@@ -88,7 +91,7 @@ __device__ __forceinline__ void codes4_bf16(uint32_t w, uint32_t& lo, uint32_t& 
     lo = *reinterpret_cast<const uint32_t*>(&p);
     hi = *reinterpret_cast<const uint32_t*>(&q);
   } else {
-    const uint32_t a = prmt(w, 0x43434343u, 0x4140), b = prmt(w, 0x43434343u, 0x4342);
+    const uint32_t a = prmt(w, 0x3F3F3F3Fu, 0x4140), b = prmt(w, 0x3F3F3F3Fu, 0x4342);
     const uint32_t au = a & 0xFF7FFF7Fu, as = a & 0xFF80FF80u;
     const uint32_t bu = b & 0xFF7FFF7Fu, bs = b & 0xFF80FF80u;
     const __nv_bfloat162 p = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&au),

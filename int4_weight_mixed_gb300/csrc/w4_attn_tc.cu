@@ -6,7 +6,8 @@
 // A unit is up to 256 rows (query heads of a key head times tokens) by the tiles
 // of 128 keys they see.  Per tile and 128 rows X:
 //
-//   S_X = Q_X K^T         K: codes as 16-bit values, exact; S in tensor memory
+//   S_X = Q_X K^T         K: codes as 16-bit values, exact (bf16: times 2^-8, which ks
+//                         takes back); S in tensor memory
 //   t_j = S_j * (scale * log2 e * ks_j) + log2 vs_j       (ks, vs: the scales)
 //   P_j = 2^(t_j - m + 6) <= 2^15, fp16, written over S in tensor memory
 //   O_X += P V            V: codes as fp16, exact;  l += P_j 2^-4 / vs_j;  out = 2^-4 O / l
@@ -429,7 +430,7 @@ struct AttnTc {
   }
   __device__ __forceinline__ void put_factors(uint32_t to, int key, bool none, float ks, float vs) const {
     const uint32_t f = to + 16 * (key >> 1) + 4 * (key & 1);
-    const float x = none ? 0.f : (ks + (vs - vs)) * (a.scale * 1.44269504f);
+    const float x = none ? 0.f : (ks + (vs - vs)) * (a.scale * (BF16 ? 1.44269504f / kBf16Code : 1.44269504f));
     const float y = none ? kNoKey : lg2(counted(vs)) + kLogLift;
     if constexpr (SOURCE == kUnpack) {
       *reinterpret_cast<float*>(record + f) = x;

@@ -272,3 +272,48 @@ def test_with_and_without_copies(gpu_lib, D, codes, dt):
     with pytest.raises(w4.W4Error):
         w4.cache_attention(held, q.to(DEV), *plan,
                            ws=torch.zeros(least - 1, dtype=torch.uint8, device=DEV))
+
+
+# -------------------------------------------------------------------- queries
+def _heads(rows):
+    return 96 if rows == 300 else 6
+
+
+@pytest.mark.parametrize("D,rows,wide,kernel", [(128, 1, False, DEC), (64, 1, False, DEC),
+                                                (128, 20, True, OWN), (64, 20, True, OWN),
+                                                (128, 90, True, OWN), (64, 90, True, OWN),
+                                                (128, 300, False, UNPACKED), (64, 300, False, UNPACKED)])
+def test_kernel_of_large_queries(rec, D, rows, wide, kernel):
+    got = _kernels(rec, _heads(rows), 2, D, 3 * rows, 3, (1 << 16) if wide else 13, 32)
+    assert kernel in got
+    assert (UNPACKED in got) == (kernel == UNPACKED) and (DEC in got) == (kernel == DEC)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rows,wide", [(128, 1, False), (64, 1, False), (128, 20, True),
+                                         (64, 20, True), (128, 90, True), (64, 90, True),
+                                         (128, 300, False), (64, 300, False), (96, 3, False),
+                                         (256, 1, False)])
+@pytest.mark.parametrize("codes", [S8, F8])
+@pytest.mark.parametrize("sizes,scale,log", [((1e35, 1.0, 1e34), 1e-35, 0),
+                                             ((5e34, 1e20, 1e30), -2e-35, 0),
+                                             ((1e35, 1e-3, 1e35), None, -90)])
+def test_large_queries(gpu_lib, D, rows, wide, codes, sizes, scale, log):
+    """bf16 queries whose products with the codes pass fp32's largest number (some
+    rows have the signs of a key's codes), with scores of some tens or more, beside
+    rows of other sizes."""
+    batch = kv.Batch([rows] * 3, [400] * 3, 32, behind=0, wide=wide)
+    cache = kv.random_cache(batch, 2, D, codes)
+    cache.k_scales.mul_(2.0**log)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(batch.T, _heads(rows), D, generator=g).clamp(-3, 3)
+    K, _ = kv.dequantised(cache, batch, 0)
+    q[:rows, 0] = 2.5 * K[0, 11].sign().float()
+    q[:rows, -1] = -2.5 * K[1, 11].sign().float()
+    for i, size in enumerate(sizes):
+        q[i * rows:(i + 1) * rows] *= size
+    q[::5, 2] *= 1e-7  # (heads of other sizes beside them)
+    code = cache.k.float().abs().sum(-1).nan_to_num(0).max()
+    assert 2.0**128 < float(q.abs().max().double() * code) < 2.0**135
+    _check(None, None, _heads(rows), 2, D, 32, codes, torch.bfloat16, q=q.to(torch.bfloat16),
+           cache=cache, batch=batch, scale=scale, behind=0)
