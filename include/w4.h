@@ -418,7 +418,12 @@ w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void
  *                       (W4_S8 or W4_E4M3), 16-byte aligned
  *   k_scales, v_scales  [pages, heads, page_size] fp32, 16-byte aligned
  * page_size is a power of two, 16 at least; head_dim a multiple of 16 up to
- * 256 (64 and 128 have the fast kernels). */
+ * 256 (64 and 128 have the fast kernels).
+ * Codes and scales at positions of a sequence are such as w4_cache_write makes, also
+ * where a caller fills the arrays: codes that are numbers (E4M3's NaN codes, 0x7F and
+ * 0xFF, are outside the contract here as in the products: what is NaN is so by its
+ * scale), scales of 2^-100 or more, of 0 with codes of 0, or NaN with codes of 0.
+ * Slots of no position may hold anything. */
 typedef struct w4_kv_cache {
   void *k, *v;
   float *k_scales, *v_scales;

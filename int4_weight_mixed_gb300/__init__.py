@@ -554,7 +554,9 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
 class KVCache(NamedTuple):
     """A paged key-value cache in 8 bits (w4_kv_cache): codes [pages, heads,
     page_size, head_dim] int8 or float8_e4m3fn and one fp32 scale for each
-    position and head [pages, heads, page_size].  kv_cache() makes one.
+    position and head [pages, heads, page_size].  kv_cache() makes one.  Where a
+    program fills one itself it holds what cache_write makes: no NaN codes (a NaN
+    is a scale of NaN), no scales below 2^-100 but 0 with codes of 0.
 
     The calls on it share the batch (w4_kv_batch), int32 tensors on its device:
     starts [B + 1], sequence b's rows being starts[b] .. starts[b+1] - 1 of the

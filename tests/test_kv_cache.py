@@ -344,3 +344,29 @@ def test_another_stream(gpu_lib):
         w4.cache_write(cache, kd, vd, *plan)
     side.synchronize()
     assert all(_same(a, b) for a, b in zip(cache, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes", [S8, F8])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_what_the_cache_holds(gpu_lib, dt, codes):
+    """Of every 16-bit value, alone and beside others: codes that are numbers, scales
+    that are 0 (codes 0), 2^-100 at least, or NaN (codes 0)."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dt)
+    g = torch.Generator().manual_seed(0)
+    alone = torch.zeros(65536, 1, 16, dtype=dt)
+    alone[:, 0, 5] = x
+    mixed = x[torch.randperm(65536, generator=g)].view(-1, 1, 16)
+    near = x.view(-1, 1, 16)  # values of one size
+    rows = torch.cat([alone, mixed, near])
+    T = rows.shape[0]
+    cache = w4.kv_cache(-(-T // 64), 1, 64, 16, codes, DEV)
+    table = torch.arange(cache.k.shape[0], dtype=torch.int32, device=DEV)[None].contiguous()
+    starts, lens = (torch.tensor(n, dtype=torch.int32, device=DEV) for n in ([0, T], [T]))
+    w4.cache_write(cache, rows.to(DEV), rows.flip(0).contiguous().to(DEV), table, starts, lens)
+    for c, s in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+        c, s = c.float().view(-1, 16)[:T], s.view(-1)[:T]
+        assert bool(torch.isfinite(c).all())
+        assert bool((s.isnan() | (s == 0) | (s >= 2.0**-100)).all())
+        assert float(c[s.isnan() | (s == 0)].abs().sum()) == 0
+        assert float(c.abs().max()) == kv.TOP[codes] and not bool(torch.isinf(s).any())
