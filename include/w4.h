@@ -410,7 +410,9 @@ w4_status w4_rmsnorm(const void* x, int x_type, int64_t M, int64_t K, const void
  * A paged key-value cache in 8 bits and the attention over it: what stands
  * between the product that makes queries, keys and values and the output
  * product.  Codes are symmetric with one scale for each position and head, from
- * that row's own values, as in the per-token quantization above ([PT], [QQQ]).
+ * that row's own values, the scheme of the per-token quantization above ([PT],
+ * [QQQ]); the scale is a product (below) where that one divides, so that the two
+ * may differ in its last bits, and in codes next to a tie.
  *
  * The cache: `pages` pages of page_size positions.  Codes of a page and head
  * are contiguous.  Arrays on the device, owned by the caller:
@@ -494,7 +496,7 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  *        sequences fit: a smaller batch may come to more.  One of the size for a
  *        single row does for any batch on the cache: where the copies do not fit in
  *        what there is, keys and values are converted wherever they are read (a
- *        prompt of 8192 takes a tenth longer).
+ *        prompt of 8192 takes 15% longer).
  * Codes enter the products exactly and are scaled in fp32; scores, softmax
  * statistics and sums are fp32, and each key's weight (probability times value
  * scale) is rounded to fp16 before the product with the values' codes: to 2^-11 of

@@ -2,7 +2,8 @@
 // they are written (w4_cache_write), and read back as 16-bit rows
 // (w4_cache_read).  One scale per position and head, from that row's own
 // values, as the per-token activations have (vLLM PR #6547 "Enable Dynamic Per
-// Token fp8"; pytorch/ao PR #1113: symmetric int8):
+// Token fp8"; pytorch/ao PR #1113: symmetric int8).  Their quantizer (w4_quant.cu)
+// divides by 127 or 448, this one multiplies, so scales may differ in the last bits:
 //
 //   scale = max_d |x[d]| * (1 / 127) (int8) or (1 / 448) (E4M3), the reciprocal
 //           and the product each rounded once to fp32;
