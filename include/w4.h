@@ -508,7 +508,8 @@ w4_status w4_cache_read(const w4_kv_cache* cache, const w4_kv_batch* batch, void
  * may lie some 2^90 apart.  Scores (times log2 e; with every term of their sums taken
  * as positive) lie within 2^119 of zero, a row's largest |q| times the sum of a key's
  * |codes| below 2^135 (|q| below 7e35 for 128 dimensions, whatever the keys), and
- * |scale| times the keys below 2^126.
+ * |scale| times the keys below 2^126.  A result within 2^-10 of fp16's largest number
+ * may round to infinity.
  * Errors as w4_cache_write, plus INVALID_ARGUMENT
  * for heads not a multiple of the cache's, a scale that is not finite, negative
  * sinks, or out overlapping q or the cache; UNSUPPORTED for heads above 65535 or

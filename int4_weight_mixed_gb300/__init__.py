@@ -597,7 +597,8 @@ def cache_read(cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: 
                v_out: torch.Tensor | None = None):
     """w4_cache_read: the rows' keys and values as (k, v), [rows, heads,
     head_dim] of dtype (fp16 / bf16).  starts = 0, lens[0], lens[0] + lens[1],
-    ... reads whole sequences."""
+    ... reads whole sequences.  Rows of no sequence keep what k_out and v_out held
+    (new ones: anything)."""
     if dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("dtype must be torch.float16 or torch.bfloat16")
     if _host is None:
@@ -638,7 +639,8 @@ def cache_attention(cache: KVCache, q: torch.Tensor, table: torch.Tensor, starts
     written before), as [rows, heads, head_dim].  One row a sequence is a decode
     step, all of them a prompt; a batch may mix any numbers.  window: keys a row
     sees back from itself, itself among them (0: all); sinks: first keys that
-    stay visible to it.  scale: of the scores, 1 / sqrt(head_dim) by default."""
+    stay visible to it.  scale: of the scores, 1 / sqrt(head_dim) by default.  Rows
+    of no sequence keep what out held (a new one: anything)."""
     if _host is None:
         _load_host()
     args = (q, None, *cache, table, starts, lens, scale, window, sinks, out, ws)

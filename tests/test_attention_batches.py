@@ -317,3 +317,41 @@ def test_large_queries(gpu_lib, D, rows, wide, codes, sizes, scale, log):
     assert 2.0**128 < float(q.abs().max().double() * code) < 2.0**135
     _check(None, None, _heads(rows), 2, D, 32, codes, torch.bfloat16, q=q.to(torch.bfloat16),
            cache=cache, batch=batch, scale=scale, behind=0)
+
+
+# ----------------------------------------------------------------- large caches
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,codes", [(128, S8), (64, F8), (96, S8)])
+def test_cache_beyond_32_bits(gpu_lib, D, codes):
+    """Codes beyond 2^31 and 2^32 bytes into their array: rows are written, read and
+    attended to as in a small cache, bit for bit."""
+    H, page, dt = 2, 64, torch.bfloat16
+    rows, lens = [300, 1, 40, 0], [300, 700, 90, 20]
+    batch = kv.Batch(rows, lens, page, seed=5, behind=0)
+    pages = (1 << 32) // (H * page * D) + batch.pages
+    table, starts, n = batch.plan(DEV)
+    far = torch.where(table < 0, table, pages - 1 - table)  # the last ones ...
+    half = (1 << 31) // (H * page * D)
+    far[1] = torch.where(table[1] < 0, table[1], half - 3 + table[1] % 6 + 6 * (table[1] // 6))
+    whole = torch.tensor([0, *torch.tensor(lens).cumsum(0)], dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(sum(lens), H, D, generator=g).to(dt).to(DEV) for _ in range(2))
+    q = torch.randn(batch.T, 8, D, generator=g).to(dt).to(DEV)
+    got = []
+    for count, t in ((batch.pages, table), (pages, far)):
+        cache = w4.kv_cache(count, H, page, D, codes, DEV)
+        w4.cache_write(cache, k, v, t, whole, n)
+        out = [*w4.cache_read(cache, t, whole, n, sum(lens), dt),
+               w4.cache_attention(cache, q, t, starts, n),
+               w4.cache_attention(cache, q[:4], t, torch.arange(5, dtype=torch.int32, device=DEV), n)]
+        # the tensor cores' kernel, and with its copies of keys and values
+        for heads, w in ((8, 1 << 12), (192, t.shape[1])):
+            wide = torch.nn.functional.pad(t, (0, w - t.shape[1]), value=-1)
+            many = q[:, :1].expand(-1, heads, -1).contiguous()
+            out.append(w4.cache_attention(cache, many, wide, starts, n))
+        got.append(out)
+        written = cache.k.view(torch.uint8).flatten(1).any(1).sum()
+        assert int(written) == len(set(t[t >= 0].tolist()))
+        del cache
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
