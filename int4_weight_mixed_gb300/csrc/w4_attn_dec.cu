@@ -1,6 +1,6 @@
 // w4_attn_dec.cu — attention over the paged key-value cache for few rows a key
 // head (decode steps): bound by the bytes of the visible codes and, short of that,
-// by the instructions that make operands of them (642 a warp for 32 keys of 128
+// by the instructions that make operands of them (646 a warp for 32 keys of 128
 // dimensions).  64 sequences of up to 8192 positions, 8 key heads of 128: 131 us,
 // 5.0 TB/s; two of 131072: 74 us, 4.9 TB/s; one of 1500: 10 us, latency.  With the
 // unit's rows as the MMA's 16 and the keys as its 8 (half of it empty with up to

@@ -1,7 +1,7 @@
 // w4_attn_tc.cu — attention over the paged key-value cache for many rows a key
 // head (prompts, chunks, trees of drafts): on the tensor cores (tcgen05), bound
 // by them and, short of that, by the instructions of the softmax.  A causal prompt
-// of 8192, 32 heads over 8 of 128 dimensions: 752 us, 730 TFLOP/s.
+// of 8192, 32 heads over 8 of 128 dimensions: 744 us, 739 TFLOP/s.
 //
 // A unit is up to 256 rows (query heads of a key head times tokens) by the tiles
 // of 128 keys they see.  Per tile and 128 rows X:

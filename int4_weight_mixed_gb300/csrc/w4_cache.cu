@@ -13,7 +13,7 @@
 //
 // Both are bound by HBM, 3 bytes a value and 8 bytes a row and head: 131072
 // positions of 8 heads read in 139 us (5.9 TB/s), 21000 rows written as E4M3 in
-// 45 us (2.9 TB/s: the codes' instructions; 35 us without them).  Eight
+// 45 us (2.9 TB/s; 35 us without the codes' instructions).  Eight
 // values a lane: 16 bytes of them, 8 bytes of codes; a head's row is a group of
 // dim / 8 lanes, and consecutive groups of a warp take consecutive heads of a
 // row, which are contiguous on the 16-bit side.
