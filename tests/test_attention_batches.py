@@ -355,3 +355,24 @@ def test_cache_beyond_32_bits(gpu_lib, D, codes):
         del cache
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rows,wide", [(128, 1, False), (128, 20, True), (64, 20, True),
+                                         (128, 90, True), (64, 90, True), (128, 300, False),
+                                         (64, 300, False), (96, 3, False)])
+@pytest.mark.parametrize("codes", [S8, F8])
+@pytest.mark.parametrize("sizes,log", [((1e-30, 1e-31, 1e-29), 98), ((3e-34, 1e-35, 1e-33), 110),
+                                       ((3e-37, 1e-36, 1e-37), 120)])
+def test_small_queries(gpu_lib, D, rows, wide, codes, sizes, log):
+    """bf16 queries near the smallest normal number, keys so large that scores are some
+    ones to tens."""
+    batch = kv.Batch([rows] * 3, [400] * 3, 32, behind=0, wide=wide)
+    cache = kv.random_cache(batch, 2, D, codes)
+    cache.k_scales.mul_(2.0**log)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(batch.T, _heads(rows), D, generator=g)
+    for i, size in enumerate(sizes):
+        q[i * rows:(i + 1) * rows] *= size
+    _check(None, None, _heads(rows), 2, D, 32, codes, torch.bfloat16, q=q.to(torch.bfloat16),
+           cache=cache, batch=batch, behind=0)
